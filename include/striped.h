@@ -308,6 +308,97 @@ int ring_round_bwd(const void *q_d, const void *k_e, const void *v_e, const void
                    int64_t *tile_stats, void *stream);
 int ring_bwd_finish(const float *acc, void *out, int64_t n, int dtype, float mul, void *stream);
 
+/*
+ * Causal attention over a sliding window and a few first tokens that stay
+ * visible (sinks); not on the pages: the local layers of a long-context
+ * model, in the same placed rows as its full-attention layers.  A query at
+ * position p keeps the key at position t iff
+ *     t <= p  and  (p - t < window  or  t < sinks);
+ * o = softmax(scale * q k^T on kept pairs) v and lse = the natural-log
+ * log-sum-exp of each row's kept scores.  Every query keeps itself
+ * (window >= 1); window >= S is plain causal attention.
+ *  q, o: [B,H,S,D], k, v: [B,Hkv,S,D] in `layout` order, lse: [B,H,S] fp32;
+ *  H % Hkv == 0, query head h reads key/value head h / (H/Hkv).
+ * bf16 with D == 64 or 128; sinks <= 1024; at most 128 stripes in the striped
+ * placement; S <= 2^31 - 256; zig-zag as for striped_attn_fwd; else
+ * STRIPED_ERR_UNSUPPORTED.  S need not be a multiple of any tile.  The
+ * kernels work on tiles of consecutive positions, not on the per-round tiles
+ * of the ring, so there is no tile_stats.  K and V must be finite in every
+ * row: a tile multiplies the weight 0 of a pair that is not kept with its V.
+ */
+int striped_attn_window_fwd(const void *q, const void *k, const void *v, void *o, float *lse, int64_t B, int64_t H,
+                            int64_t Hkv, int64_t S, int64_t D, int N, int layout, int dtype, int64_t window,
+                            int64_t sinks, float scale, void *stream);
+
+/* Bytes of device workspace striped_attn_window_bwd needs (fp32 dQ
+ * accumulator and softmax statistics in whole tiles, and the sink tiles'
+ * shares of dK and dV), or 0 for arguments that it rejects. */
+size_t striped_attn_window_workspace_size(int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t D, int N, int layout,
+                                          int dtype, int64_t window, int64_t sinks);
+
+/*
+ * Backward of striped_attn_window_fwd: its inputs, its outputs o and lse and
+ * the cotangent dO give dq [B,H,S,D], dk and dv [B,Hkv,S,D] (fully
+ * overwritten; a shared key/value head gets the sum over its query heads).
+ * workspace: 256-byte aligned, its contents on entry are ignored.  dK and dV
+ * are the same from run to run; dQ is accumulated with fp32 atomics (a few
+ * fp32 ulps before it is rounded).
+ */
+int striped_attn_window_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                            const void *dO, void *dq, void *dk, void *dv, void *workspace, size_t ws_bytes, int64_t B,
+                            int64_t H, int64_t Hkv, int64_t S, int64_t D, int N, int layout, int dtype,
+                            int64_t window, int64_t sinks, float scale, void *stream);
+
+/*
+ * RMS norm of every query and key head and the rotary position rotation, in
+ * one pass (not on the pages; the step between a layer's projections and its
+ * attention, where every row needs the position that the placement gives
+ * it).  For a row x of q or k at position p:
+ *     n = x / sqrt(mean(x^2) + eps),  y = n * weight,
+ *     (y_a, y_b) -> (y_a cos t - y_b sin t, y_b cos t + y_a sin t),
+ *     t = p * inv_freq[j],
+ * for the pairs (a, b) = (j, j + rotary_dim/2), or (2j, 2j + 1) with
+ * interleaved != 0, j < rotary_dim/2; elements from rotary_dim on are not
+ * rotated (rotary_dim = 0: norm only, inv_freq may be NULL).  Angles are
+ * reduced in 64 bits, so they stay exact at far positions.
+ *  q, q_out: [B,H,S,D], k, k_out: [B,Hkv,S,D] `dtype`; H and Hkv are any
+ *            counts >= 1.  q_out may be q and k_out may be k (in place); any
+ *            other overlap of a result with another tensor is
+ *            STRIPED_ERR_INVALID_ARG.
+ *  q_weight, k_weight: [D] fp32.  inv_freq: [rotary_dim/2] fp64.
+ *  positions: NULL, or int64 [B,S], the position of every row (then N,
+ *            layout and stripe are ignored).  With NULL, rows are placed:
+ *            stripe = -1: the S rows of a whole sequence in `layout` order
+ *            (S % N == 0, zig-zag S % (2N) == 0); stripe = d >= 0: the S = L
+ *            rows that device d of N holds (zig-zag: L even).
+ *  D <= 256 and D and rotary_dim whole multiples of 16 (bf16) or 8 (fp32),
+ *  else STRIPED_ERR_UNSUPPORTED.  All device pointers.
+ */
+int striped_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out, const float *q_weight,
+                         const float *k_weight, const double *inv_freq, const int64_t *positions, int64_t B,
+                         int64_t H, int64_t Hkv, int64_t S, int64_t D, int rotary_dim, int interleaved, int N,
+                         int layout, int stripe, float eps, int dtype, void *stream);
+
+/* Bytes of device workspace striped_qk_norm_rope_bwd needs (the blocks'
+ * shares of the weight gradients), or 0 for invalid sizes. */
+size_t striped_qk_norm_rope_workspace_size(int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t D, int dtype);
+
+/*
+ * Backward of striped_qk_norm_rope: q and k are the forward's INPUTS,
+ * dq_out and dk_out the cotangents of its outputs.  With g the cotangent
+ * turned back by the row's angle and h = g * weight,
+ *     d_weight = sum over all rows and heads of g * n   (fp32 [D]),
+ *     dx = r h - x r^3 mean(h x),  r = 1 / sqrt(mean(x^2) + eps).
+ * dq may be q or dq_out, dk may be k or dk_out (in place).  Sums in a fixed
+ * order: results are the same from run to run.  workspace: 16-byte aligned,
+ * >= striped_qk_norm_rope_workspace_size() bytes, its contents are ignored.
+ */
+int striped_qk_norm_rope_bwd(const void *q, const void *k, const void *dq_out, const void *dk_out, void *dq, void *dk,
+                             float *dq_weight, float *dk_weight, const float *q_weight, const float *k_weight,
+                             const double *inv_freq, const int64_t *positions, void *workspace, size_t ws_bytes,
+                             int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t D, int rotary_dim,
+                             int interleaved, int N, int layout, int stripe, float eps, int dtype, void *stream);
+
 /* Tile edge T (queries x keys) the kernels for (dtype, D) skip and count
  * with; writes *Tq and *Tk.  Returns STRIPED_ERR_UNSUPPORTED if no kernel. */
 int striped_kernel_tile(int dtype, int64_t D, int *Tq, int *Tk);

@@ -86,6 +86,16 @@ def load(build_if_missing: bool = True):
         lib.striped_attn_fwd_varlen.argtypes = [P, P, P, P, P, P, I, I64, I64, I64, I, I, I, F, P, P]
         lib.striped_attn_bwd_varlen.argtypes = [P, P, P, P, P, P, P, P, P, P, SZ, P, I, I64, I64, I64, I, I, I,
                                                 F, P, P]
+        lib.striped_attn_window_fwd.argtypes = [P, P, P, P, P, I64, I64, I64, I64, I64, I, I, I, I64, I64, F, P]
+        lib.striped_attn_window_workspace_size.argtypes = [I64, I64, I64, I64, I64, I, I, I, I64, I64]
+        lib.striped_attn_window_workspace_size.restype = SZ
+        lib.striped_attn_window_bwd.argtypes = [P, P, P, P, P, P, P, P, P, P, SZ, I64, I64, I64, I64, I64, I, I, I,
+                                                I64, I64, F, P]
+        lib.striped_qk_norm_rope.argtypes = [P, P, P, P, P, P, P, P, I64, I64, I64, I64, I64, I, I, I, I, I, F, I, P]
+        lib.striped_qk_norm_rope_workspace_size.argtypes = [I64, I64, I64, I64, I64, I]
+        lib.striped_qk_norm_rope_workspace_size.restype = SZ
+        lib.striped_qk_norm_rope_bwd.argtypes = [P, P, P, P, P, P, P, P, P, P, P, P, P, SZ, I64, I64, I64, I64, I64,
+                                                 I, I, I, I, I, F, I, P]
         lib.striped_kernel_tile.argtypes = [I, I64, P, P]
         lib.striped_fwd_query_tiles_per_cta.argtypes = [I64, I64, I64, I64, I, I, I, I]
         lib.striped_tile_counts.argtypes = [I64, I, I, I, I, P, P]
@@ -427,6 +437,186 @@ def striped_attn_bwd_varlen(q, k, v, o, lse, dO, cu_seqlens, N: int, layout: int
                                           cp, n, H, Hkv, D, N, layout, _dtype_code(q), float(scale),
                                           _ptr_or_null(tile_stats), _stream(stream)), "striped_attn_bwd_varlen")
     return dq, dk, dv
+
+
+# ------------------------------------------------------------------ argument checks
+def _need(t, name: str, shape, dtype, like: torch.Tensor):
+    """Pointer of an argument after checking its shape, type, device and
+    layout against what the call needs."""
+    p = _dev(t, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    return p
+
+
+def _rank(t, name: str, n: int):
+    """A CUDA tensor of n dimensions (before its shape is read)."""
+    _dev(t, name)
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got {t.dim()}")
+
+
+class _on:
+    """Run a call on the device of its tensors, whichever is current, on the
+    given stream or that device's current one."""
+
+    __slots__ = ("device", "stream", "guard")
+
+    def __init__(self, t: torch.Tensor, stream):
+        if stream is not None and stream.device != t.device:
+            raise ValueError(f"stream is on {stream.device}, tensors are on {t.device}")
+        self.device = t.device
+        self.stream = stream
+        self.guard = None
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.device.index:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
+        return ctypes.c_void_p(s.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+# ------------------------------------------------------------------ window attention
+def _qkv(q, k, v):
+    _rank(q, "q", 4)
+    _rank(k, "k", 4)
+    B, H, S, D = q.shape
+    Hkv = k.shape[1]
+    _need(k, "k", (B, Hkv, S, D), q.dtype, q)
+    _need(v, "v", (B, Hkv, S, D), q.dtype, q)
+    return B, H, Hkv, S, D
+
+
+def striped_attn_window_fwd(q, k, v, N: int, window: int, sinks: int = 0, layout: int = STRIPED,
+                            scale: float | None = None, out=None, lse_out=None, stream=None):
+    """Causal attention over the last `window` positions and the first `sinks`
+    tokens: q [B,H,S,D], k and v [B,Hkv,S,D] bf16 in `layout` order.  Returns
+    (o, lse)."""
+    B, H, Hkv, S, D = _qkv(q, k, v)
+    if scale is None:
+        scale = 1.0 / D ** 0.5
+    o = torch.empty_like(q) if out is None else out
+    lse = torch.empty((B, H, S), dtype=torch.float32, device=q.device) if lse_out is None else lse_out
+    with _on(q, stream) as st:
+        _check(load().striped_attn_window_fwd(_dev(q, "q"), _dev(k, "k"), _dev(v, "v"),
+                                              _need(o, "out", q.shape, q.dtype, q),
+                                              _need(lse, "lse_out", (B, H, S), torch.float32, q), B, H, Hkv, S, D, N,
+                                              layout, _dtype_code(q), int(window), int(sinks), float(scale), st),
+               "striped_attn_window_fwd")
+    return o, lse
+
+
+def new_window_workspace(q, k, N: int, window: int, sinks: int = 0, layout: int = STRIPED) -> torch.Tensor:
+    """Workspace of striped_attn_window_bwd for these tensors and arguments."""
+    B, H, S, D = q.shape
+    n = int(load().striped_attn_window_workspace_size(B, H, k.shape[1], S, D, N, layout, _dtype_code(q), int(window),
+                                                      int(sinks)))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+
+
+def striped_attn_window_bwd(q, k, v, o, lse, dO, N: int, window: int, sinks: int = 0, layout: int = STRIPED,
+                            scale: float | None = None, workspace: torch.Tensor | None = None, dq=None, dk=None,
+                            dv=None, stream=None):
+    """Backward of striped_attn_window_fwd; returns (dq, dk, dv)."""
+    B, H, Hkv, S, D = _qkv(q, k, v)
+    if scale is None:
+        scale = 1.0 / D ** 0.5
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    with _on(q, stream) as st:
+        ws = new_window_workspace(q, k, N, window, sinks, layout) if workspace is None else workspace
+        _check(load().striped_attn_window_bwd(
+            _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _need(o, "o", q.shape, q.dtype, q),
+            _need(lse, "lse", (B, H, S), torch.float32, q), _need(dO, "dO", q.shape, q.dtype, q),
+            _need(dq, "dq", q.shape, q.dtype, q), _need(dk, "dk", k.shape, q.dtype, q),
+            _need(dv, "dv", k.shape, q.dtype, q), _need(ws, "workspace", ws.shape, ws.dtype, q),
+            ws.numel() * ws.element_size(), B, H, Hkv, S, D, N, layout, _dtype_code(q), int(window), int(sinks),
+            float(scale), st), "striped_attn_window_bwd")
+    return dq, dk, dv
+
+
+# ------------------------------------------------------------------ norm and rotation
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """fp64 [rotary_dim/2]: base^(-2j/rotary_dim), the angle per position of
+    pair j, for striped_qk_norm_rope."""
+    j = torch.arange(rotary_dim // 2, dtype=torch.float64, device=device)
+    return float(base) ** (-2.0 * j / max(1, rotary_dim))
+
+
+def _rope_args(q, k, q_weight, k_weight, inv_freq, positions):
+    _rank(q, "q", 4)
+    _rank(k, "k", 4)
+    B, H, S, D = q.shape
+    Hkv = k.shape[1]
+    code = _dtype_code(q)
+    _need(k, "k", (B, Hkv, S, D), q.dtype, q)
+    _rank(inv_freq, "inv_freq", 1)
+    ptrs = [_need(q_weight, "q_weight", (D,), torch.float32, q), _need(k_weight, "k_weight", (D,), torch.float32, q),
+            _need(inv_freq, "inv_freq", inv_freq.shape, torch.float64, q),
+            None if positions is None else _need(positions, "positions", (B, S), torch.int64, q)]
+    return B, H, Hkv, S, D, code, ptrs
+
+
+def striped_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, N: int = 1, layout: int = STRIPED,
+                         stripe: int | None = None, positions: torch.Tensor | None = None, eps: float = 1e-6,
+                         interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """RMS norm per head and rotary rotation of q [B,H,S,D] and k [B,Hkv,S,D]
+    in `layout` row order (stripe=d: the rows of device d; positions int64
+    [B,S]: the rows' own positions); q_weight, k_weight fp32 [D], inv_freq
+    fp64 [rotary_dim/2] (rope_frequencies).  Returns (q_out, k_out), which may
+    be q and k themselves."""
+    B, H, Hkv, S, D, code, (qw, kw, fr, pos) = _rope_args(q, k, q_weight, k_weight, inv_freq, positions)
+    yq = torch.empty_like(q) if q_out is None else q_out
+    yk = torch.empty_like(k) if k_out is None else k_out
+    with _on(q, stream) as st:
+        _check(load().striped_qk_norm_rope(_dev(q, "q"), _dev(k, "k"), _need(yq, "q_out", q.shape, q.dtype, q),
+                                           _need(yk, "k_out", k.shape, q.dtype, q), qw, kw, fr, pos, B, H, Hkv, S, D,
+                                           2 * inv_freq.numel(), int(bool(interleaved)), N, layout,
+                                           -1 if stripe is None else int(stripe), float(eps), code, st),
+               "striped_qk_norm_rope")
+    return yq, yk
+
+
+def qk_norm_rope_workspace(q, k) -> torch.Tensor:
+    """Workspace of striped_qk_norm_rope_bwd for these q and k."""
+    B, H, S, D = q.shape
+    n = int(load().striped_qk_norm_rope_workspace_size(B, H, k.shape[1], S, D, _dtype_code(q)))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+
+
+def striped_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, inv_freq, N: int = 1, layout: int = STRIPED,
+                             stripe: int | None = None, positions: torch.Tensor | None = None, eps: float = 1e-6,
+                             interleaved: bool = False, workspace: torch.Tensor | None = None, dq=None, dk=None,
+                             dq_weight=None, dk_weight=None, stream=None):
+    """Backward of striped_qk_norm_rope: q and k are its inputs, dq_out and
+    dk_out the cotangents of its outputs.  Returns (dq, dk, dq_weight fp32
+    [D], dk_weight fp32 [D])."""
+    B, H, Hkv, S, D, code, (qw, kw, fr, pos) = _rope_args(q, k, q_weight, k_weight, inv_freq, positions)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dqw = torch.empty_like(q_weight) if dq_weight is None else dq_weight
+    dkw = torch.empty_like(k_weight) if dk_weight is None else dk_weight
+    with _on(q, stream) as st:
+        ws = qk_norm_rope_workspace(q, k) if workspace is None else workspace
+        _check(load().striped_qk_norm_rope_bwd(
+            _dev(q, "q"), _dev(k, "k"), _need(dq_out, "dq_out", q.shape, q.dtype, q),
+            _need(dk_out, "dk_out", k.shape, q.dtype, q), _need(dq, "dq", q.shape, q.dtype, q),
+            _need(dk, "dk", k.shape, q.dtype, q), _need(dqw, "dq_weight", (D,), torch.float32, q),
+            _need(dkw, "dk_weight", (D,), torch.float32, q), qw, kw, fr, pos,
+            _need(ws, "workspace", ws.shape, ws.dtype, q), ws.numel() * ws.element_size(), B, H, Hkv, S, D,
+            2 * inv_freq.numel(), int(bool(interleaved)), N, layout, -1 if stripe is None else int(stripe),
+            float(eps), code, st), "striped_qk_norm_rope_bwd")
+    return dq, dk, dqw, dkw
 
 
 # ------------------------------------------------------------------ host model

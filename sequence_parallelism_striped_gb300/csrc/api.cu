@@ -9,6 +9,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "window.cuh"
 
 namespace striped {
 
@@ -64,10 +65,10 @@ typedef CUresult (*EncodeTiledFnT)(CUtensorMap *, CUtensorMapDataType, cuuint32_
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 // [BH][N][L][D] tensor of `esize`-byte elements -> 4-D tiled tensor map,
-// boxes of box_x elements x box_rows rows, 128-byte swizzle, zero fill.
+// boxes of box_x elements x box_rows rows x box_stripes, 128-byte swizzle, zero fill.
 static int make_map(CUtensorMap *map, CUtensorMapDataType dt, int64_t esize, const void *base, int64_t D,
                     int64_t L, int64_t N, int64_t BH, int64_t stripe_stride, int64_t stride_bh, int box_x,
-                    int box_rows) {
+                    int box_rows, int box_stripes = 1) {
     // the driver entry point is process-wide: resolved once, under a lock
     static std::mutex mu;
     static EncodeTiledFnT fn = nullptr;
@@ -86,7 +87,7 @@ static int make_map(CUtensorMap *map, CUtensorMapDataType dt, int64_t esize, con
     cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)L, (cuuint64_t)N, (cuuint64_t)BH};
     cuuint64_t strides[3] = {(cuuint64_t)(D * esize), (cuuint64_t)(stripe_stride * esize),
                              (cuuint64_t)(stride_bh * esize)};
-    cuuint32_t box[4] = {(cuuint32_t)box_x, (cuuint32_t)box_rows, 1, 1};
+    cuuint32_t box[4] = {(cuuint32_t)box_x, (cuuint32_t)box_rows, (cuuint32_t)box_stripes, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = fn(map, dt, 4, const_cast<void *>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -108,6 +109,12 @@ int make_f32_map(CUtensorMap *map, const void *base, int64_t D, int64_t L, int64
                  int64_t stripe_stride, int64_t stride_bh, int box_rows) {
     return make_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, D, L, N, BH, stripe_stride, stride_bh, 32,
                     box_rows);
+}
+
+int make_pos_map(CUtensorMap *map, const void *base, int64_t D, const PosGeom &g, int64_t BH) {
+    const int64_t L = g.L;
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, D, L, g.N, BH, L * D, (int64_t)g.S * D, 64, g.R,
+                    g.layout == STRIPED_LAYOUT_STRIPED ? g.N : 1);
 }
 
 // ---------------------------------------------------------------- validation
@@ -555,6 +562,142 @@ int ring_round_fwd(const void *q_d, const void *k_e, const void *v_e, float *o_a
                                  (float *)o_out, d, e, first_round ? 1 : 0, g, tile_stats, s);
     return launch_tc_round(q_d, k_e, v_e, o_acc, lse_acc, o_out, d, e, first_round ? 1 : 0, g, tile_stats,
                            s);
+}
+
+// ---------------------------------------------------------------- window attention
+static int check_window(const WindowArgs &a, int dtype) {
+    if (a.Hkv < 1 || a.H < 1 || a.H % a.Hkv != 0 || a.window < 1 || a.sinks < 0) return STRIPED_ERR_INVALID_ARG;
+    const int st = check_attn(a.B, a.H, a.S, a.D, a.N, a.layout, dtype);
+    if (st) return st;
+    if (dtype != STRIPED_BF16 || a.sinks > kMaxSinks || a.S > kMaxPositions) return STRIPED_ERR_UNSUPPORTED;
+    if (a.layout == STRIPED_LAYOUT_STRIPED && a.N > 128) return STRIPED_ERR_UNSUPPORTED;
+    return STRIPED_OK;
+}
+
+int striped_attn_window_fwd(const void *q, const void *k, const void *v, void *o, float *lse, int64_t B, int64_t H,
+                            int64_t Hkv, int64_t S, int64_t D, int N, int layout, int dtype, int64_t window,
+                            int64_t sinks, float scale, void *stream) {
+    if (!q || !k || !v || !o || !lse) return STRIPED_ERR_INVALID_ARG;
+    const WindowArgs a{B, H, Hkv, S, D, N, layout, window, sinks, scale};
+    const int st = check_window(a, dtype);
+    if (st) return st;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse)) return STRIPED_ERR_ALIGN;
+    return launch_tc_window_fwd(q, k, v, o, lse, a, (cudaStream_t)stream);
+}
+
+size_t striped_attn_window_workspace_size(int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t D, int N, int layout,
+                                          int dtype, int64_t window, int64_t sinks) {
+    const WindowArgs a{B, H, Hkv, S, D, N, layout, window, sinks, 1.f};
+    if (check_window(a, dtype)) return 0;
+    return align256(window_bwd_workspace(a));
+}
+
+int striped_attn_window_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                            const void *dO, void *dq, void *dk, void *dv, void *workspace, size_t ws_bytes, int64_t B,
+                            int64_t H, int64_t Hkv, int64_t S, int64_t D, int N, int layout, int dtype,
+                            int64_t window, int64_t sinks, float scale, void *stream) {
+    if (!q || !k || !v || !o || !lse || !dO || !dq || !dk || !dv) return STRIPED_ERR_INVALID_ARG;
+    const WindowArgs a{B, H, Hkv, S, D, N, layout, window, sinks, scale};
+    const int st = check_window(a, dtype);
+    if (st) return st;
+    const size_t need = window_bwd_workspace(a);
+    if (need == 0) return STRIPED_ERR_UNSUPPORTED;
+    if (!workspace || ws_bytes < need) return STRIPED_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return STRIPED_ERR_ALIGN;
+    const void *ptrs[9] = {q, k, v, o, lse, dO, dq, dk, dv};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return STRIPED_ERR_ALIGN;
+    return launch_tc_window_bwd(q, k, v, o, lse, dO, dq, dk, dv, workspace, a, (cudaStream_t)stream);
+}
+
+// ---------------------------------------------------------------- norm and rotation
+// Two buffers may be the same one (`alias`: results over their own inputs)
+// but must not overlap in any other way.
+static bool overlap(const void *a, int64_t na, const void *b, int64_t nb, bool alias) {
+    if (!a || !b || (alias && a == b && na == nb)) return false;
+    const char *x = (const char *)a, *y = (const char *)b;
+    return x < y + nb && y < x + na;
+}
+
+static int check_rope(const RopeArgs &a) {
+    if (!a.q || !a.k || !a.q_res || !a.k_res || !a.q_weight || !a.k_weight) return STRIPED_ERR_INVALID_ARG;
+    if (a.rot < 0 || a.rot > a.D || (a.rot > 0 && !a.inv_freq)) return STRIPED_ERR_INVALID_ARG;
+    if (!(a.eps >= 0.f)) return STRIPED_ERR_INVALID_ARG;
+    if (a.H < 1 || a.Hkv < 1 || !valid_layout(a.layout)) return STRIPED_ERR_INVALID_ARG;
+    // one stripe's rows: S is the stripe's length and any S fits
+    const bool placed = !a.positions && a.stripe < 0;
+    int st = check_sizes(a.B, a.H > a.Hkv ? a.H : a.Hkv, a.S, a.D, placed ? a.N : 1);
+    if (st) return st;
+    if (!a.positions) {
+        if (a.N < 1 || a.stripe < -1 || a.stripe >= a.N) return STRIPED_ERR_INVALID_ARG;
+        if (a.layout == STRIPED_LAYOUT_ZIGZAG && (placed ? a.S % (2 * (int64_t)a.N) : a.S % 2) != 0)
+            return STRIPED_ERR_INVALID_ARG;
+    }
+    int64_t unit, es;
+    if (a.dtype == STRIPED_BF16) unit = 16, es = 2;
+    else if (a.dtype == STRIPED_FP32) unit = 8, es = 4;
+    else return STRIPED_ERR_INVALID_ARG;
+    if (a.D > 256 || a.D % unit != 0 || a.rot % unit != 0) return STRIPED_ERR_UNSUPPORTED;
+    const void *ptrs[6] = {a.q, a.k, a.q_res, a.k_res, a.dq_out, a.dk_out};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return STRIPED_ERR_ALIGN;
+    const void *words[4] = {a.q_weight, a.k_weight, a.dq_weight, a.dk_weight};  // read and written one at a time
+    for (const void *p : words)
+        if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return STRIPED_ERR_ALIGN;
+    if (((reinterpret_cast<uintptr_t>(a.inv_freq) | reinterpret_cast<uintptr_t>(a.positions)) & 7u) != 0)
+        return STRIPED_ERR_ALIGN;
+    const int64_t nq = a.B * a.H * a.S * a.D * es, nk = a.B * a.Hkv * a.S * a.D * es;
+    if (overlap(a.q_res, nq, a.k_res, nk, false)) return STRIPED_ERR_INVALID_ARG;
+    for (int r = 0; r < 2; ++r) {
+        const void *res = r ? a.k_res : a.q_res;
+        const int64_t n = r ? nk : nq;
+        if (overlap(res, n, a.q, nq, !r) || overlap(res, n, a.k, nk, r) || overlap(res, n, a.dq_out, nq, !r) ||
+            overlap(res, n, a.dk_out, nk, r))
+            return STRIPED_ERR_INVALID_ARG;
+    }
+    return STRIPED_OK;
+}
+
+int striped_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out, const float *q_weight,
+                         const float *k_weight, const double *inv_freq, const int64_t *positions, int64_t B,
+                         int64_t H, int64_t Hkv, int64_t S, int64_t D, int rotary_dim, int interleaved, int N,
+                         int layout, int stripe, float eps, int dtype, void *stream) {
+    RopeArgs a{};
+    a.q = q, a.k = k, a.q_res = q_out, a.k_res = k_out;
+    a.q_weight = q_weight, a.k_weight = k_weight, a.inv_freq = inv_freq, a.positions = positions;
+    a.B = B, a.H = H, a.Hkv = Hkv, a.S = S, a.D = D;
+    a.rot = rotary_dim, a.interleaved = interleaved, a.N = N, a.layout = layout, a.stripe = stripe;
+    a.eps = eps, a.dtype = dtype;
+    const int st = check_rope(a);
+    if (st) return st;
+    return launch_norm_rope(a, (cudaStream_t)stream);
+}
+
+size_t striped_qk_norm_rope_workspace_size(int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t D, int dtype) {
+    if (check_sizes(B, H, S, D, 1) || Hkv < 1 || (dtype != STRIPED_BF16 && dtype != STRIPED_FP32)) return 0;
+    if (D > 256 || D % (dtype == STRIPED_BF16 ? 16 : 8) != 0) return 0;
+    return align256(rope_bwd_workspace(B, H, Hkv, S, D, dtype));
+}
+
+int striped_qk_norm_rope_bwd(const void *q, const void *k, const void *dq_out, const void *dk_out, void *dq, void *dk,
+                             float *dq_weight, float *dk_weight, const float *q_weight, const float *k_weight,
+                             const double *inv_freq, const int64_t *positions, void *workspace, size_t ws_bytes,
+                             int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t D, int rotary_dim,
+                             int interleaved, int N, int layout, int stripe, float eps, int dtype, void *stream) {
+    if (!dq_out || !dk_out || !dq_weight || !dk_weight) return STRIPED_ERR_INVALID_ARG;
+    RopeArgs a{};
+    a.q = q, a.k = k, a.dq_out = dq_out, a.dk_out = dk_out, a.q_res = dq, a.k_res = dk;
+    a.q_weight = q_weight, a.k_weight = k_weight, a.inv_freq = inv_freq, a.positions = positions;
+    a.dq_weight = dq_weight, a.dk_weight = dk_weight, a.workspace = workspace;
+    a.B = B, a.H = H, a.Hkv = Hkv, a.S = S, a.D = D;
+    a.rot = rotary_dim, a.interleaved = interleaved, a.N = N, a.layout = layout, a.stripe = stripe;
+    a.eps = eps, a.dtype = dtype;
+    const int st = check_rope(a);
+    if (st) return st;
+    if (!workspace || ws_bytes < striped_qk_norm_rope_workspace_size(B, H, Hkv, S, D, dtype))
+        return STRIPED_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return STRIPED_ERR_ALIGN;
+    return launch_norm_rope(a, (cudaStream_t)stream);
 }
 
 }  // extern "C"

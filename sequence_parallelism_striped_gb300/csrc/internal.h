@@ -131,6 +131,40 @@ int launch_tc_round_bwd(const void *q_d, const void *k_e, const void *v_e, const
                         int64_t *tile_stats, cudaStream_t stream);
 int launch_scale_to_bf16(const float *acc, void *out, int64_t n8, float mul, cudaStream_t stream);
 
+// ---- attn_window_fwd.cu / attn_window_bwd.cu (bf16, tiles of consecutive
+// positions, window.cuh)
+struct WindowArgs {
+    int64_t B, H, Hkv, S, D;
+    int N, layout;
+    int64_t window, sinks;
+    float scale;
+};
+int launch_tc_window_fwd(const void *q, const void *k, const void *v, void *o, float *lse, const WindowArgs &a,
+                         cudaStream_t stream);
+size_t window_bwd_workspace(const WindowArgs &a);  // 0: no kernel for these sizes
+int launch_tc_window_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse, const void *dO,
+                         void *dq, void *dk, void *dv, void *workspace, const WindowArgs &a, cudaStream_t stream);
+
+// ---- norm_rope.cu
+// Norm and rotation of q [B][H][S][D] and k [B][Hkv][S][D] (forward: dq_out
+// and dk_out NULL, results in q_res and k_res; backward: cotangents in
+// dq_out and dk_out, gradients in q_res, k_res, dq_weight and dk_weight).
+struct RopeArgs {
+    const void *q, *k, *dq_out, *dk_out;
+    void *q_res, *k_res;
+    const float *q_weight, *k_weight;
+    const double *inv_freq;
+    const int64_t *positions;
+    float *dq_weight, *dk_weight;
+    void *workspace;
+    int64_t B, H, Hkv, S, D;
+    int rot, interleaved, N, layout, stripe;
+    float eps;
+    int dtype;
+};
+size_t rope_bwd_workspace(int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t D, int dtype);
+int launch_norm_rope(const RopeArgs &a, cudaStream_t stream);
+
 // bf16 tensor viewed as [BH][N][L][D] -> 4-D tensor map with boxes of
 // 64 elements x box_rows rows, 128-byte swizzle, zero fill out of range.
 // Returns a status code.
@@ -139,5 +173,10 @@ int make_bf16_map(CUtensorMap *map, const void *base, int64_t D, int64_t L, int6
 // Same for fp32 tensors: boxes of 32 elements (128 bytes) x box_rows rows.
 int make_f32_map(CUtensorMap *map, const void *base, int64_t D, int64_t L, int64_t N, int64_t BH,
                  int64_t stripe_stride, int64_t stride_bh, int box_rows);
+
+// bf16 [BH][S][D] tensor -> 4-D tensor map whose boxes are 64 elements of one
+// position tile (R rows of every stripe, see window.cuh).
+struct PosGeom;
+int make_pos_map(CUtensorMap *map, const void *base, int64_t D, const PosGeom &g, int64_t BH);
 
 }  // namespace striped

@@ -1,0 +1,182 @@
+"""CPU checks of the window and norm-and-rotation operators: the position
+tiles against the oracle's placement, the references' gradients against
+differences, and the C entry points' refusals."""
+import ctypes
+import os
+import shutil
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import sequence_parallelism_striped_gb300 as sp
+from tests._local_util import norm_rope_reference, positions, window_reference
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+INVALID, UNSUPPORTED, ALIGN, WORKSPACE = -1, -2, -3, -6
+
+
+@pytest.fixture(scope="module")
+def harness(tmp_path_factory):
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    if not os.path.exists(nvcc):
+        pytest.skip("nvcc not available")
+    exe = str(tmp_path_factory.mktemp("window") / "window_harness")
+    cmd = [nvcc, "-O1", "-std=c++17", "-I", os.path.join(ROOT, "include"),
+           "-I", os.path.join(ROOT, "sequence_parallelism_striped_gb300", "csrc"),
+           "-gencode", "arch=compute_103a,code=sm_103a",
+           os.path.join(ROOT, "tests", "window_harness.cu"), "-o", exe]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr
+    return exe
+
+
+@pytest.mark.parametrize("layout,S,N,W", [
+    (sp.STRIPED, 256, 4, 64), (sp.STRIPED, 1000, 8, 100), (sp.STRIPED, 903, 3, 200), (sp.STRIPED, 1300, 13, 1),
+    (sp.STRIPED, 1040, 65, 300), (sp.STRIPED, 1280, 128, 5), (sp.STRIPED, 1, 1, 1), (sp.STRIPED, 640, 5, 640),
+    (sp.CONTIGUOUS, 777, 7, 128), (sp.CONTIGUOUS, 130, 1, 129), (sp.ZIGZAG, 2048, 4, 300), (sp.ZIGZAG, 1536, 3, 257),
+    (sp.ZIGZAG, 512, 1, 2)])
+def test_position_tiles(harness, layout, S, N, W):
+    out = subprocess.run([harness, str(layout), str(S), str(N), str(W)], capture_output=True, text=True, check=True)
+    lines = [[x[0]] + [int(v) for v in x.split()[1:]] for x in out.stdout.splitlines()]
+    pos_of_row = np.asarray(oracle.layout_positions(S, N, layout))
+    rows = [x[1:] for x in lines if x[0] == "T"]
+    real = [(t, r, row, pos) for t, r, has, row, pos in rows if has]
+    # every row once, holding the position that the placement puts there
+    assert sorted(x[2] for x in real) == list(range(S))
+    assert all(pos_of_row[row] == pos for _, _, row, pos in real)
+    tiles = {}
+    for t, r, row, pos in real:
+        tiles.setdefault(t, []).append((r, row, pos))
+    P = max(len(v) for v in tiles.values())
+    for t, v in tiles.items():  # consecutive positions, tile after tile
+        assert sorted(x[2] for x in v) == list(range(t * P, min(S, t * P + P)))
+    # the copy box brings row r of the tile to place r: stripes outer, rows inner
+    for _, t, row0, stripe0, R, ns, L in [x for x in lines if x[0] == "B"]:
+        assert R * ns <= 128 and R <= 256 and ns <= 256
+        got = {s * R + i: (stripe0 + s) * L + row0 + i for s in range(ns) for i in range(R) if row0 + i < L}
+        for r, row, _ in tiles.get(t, []):
+            assert got[r] == row
+    # window spans: exactly the tiles that hold a kept pair
+    for _, t, lo, hi in [x for x in lines if x[0] == "W"]:
+        q = [x[2] for x in tiles[t]]
+        first = max(0, t * P - W + 1)  # of the tile's first position
+        assert lo == first // P
+        last_q = min(S - 1, t * P + P - 1 + W - 1)
+        assert hi == min(max(tiles), last_q // P if t * P + P <= S else max(tiles)) and min(q) == t * P
+
+
+def test_more_stripes_than_a_tile(harness):
+    assert subprocess.run([harness, str(sp.STRIPED), "1290", "129", "4"]).returncode == 3
+
+
+@pytest.mark.parametrize("W,ns", [(5, 2), (1, 0), (3, 9)])
+def test_window_reference_gradient_against_differences(W, ns):
+    """The formula of the gradient against central differences in 64 bits."""
+    B, H, Hkv, S, D, N = 1, 2, 1, 24, 8, 4
+    g = torch.Generator().manual_seed(0)
+    mk = lambda h: torch.randn(B, h, S, D, generator=g, dtype=torch.float64)  # noqa: E731
+    q, k, v, do = mk(H), mk(Hkv), mk(Hkv), mk(H)
+    pos = positions(S, N, sp.STRIPED)
+    r = window_reference(q, k, v, pos, W, ns, 0.4, do)
+    f = lambda *a: float((window_reference(*a, pos, W, ns, 0.4)["o"] * do).sum())  # noqa: E731
+    for i, n in enumerate(("dq", "dk", "dv")):
+        u = torch.randn(r[n].shape, generator=g, dtype=torch.float64)
+        args = [q, k, v]
+        up = f(*[a + 1e-5 * u if j == i else a for j, a in enumerate(args)])
+        dn = f(*[a - 1e-5 * u if j == i else a for j, a in enumerate(args)])
+        assert abs((up - dn) / 2e-5 - float((r[n] * u).sum())) < 1e-7
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_norm_rope_reference_gradient_against_differences(interleaved):
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn(1, 2, 6, 16, generator=g, dtype=torch.float64)
+    dy = torch.randn(1, 2, 6, 16, generator=g, dtype=torch.float64)
+    w = torch.randn(16, generator=g, dtype=torch.float64)
+    f = sp.rope_frequencies(8, 100.0, "cpu")
+    pos = positions(6, 3, sp.STRIPED)[None]
+    r = norm_rope_reference(x, w, pos, f, 1e-6, interleaved, dy)
+    loss = lambda x, w: float((norm_rope_reference(x, w, pos, f, 1e-6, interleaved)["y"] * dy).sum())  # noqa: E731
+    u = torch.randn(x.shape, generator=g, dtype=torch.float64)
+    assert abs((loss(x + 1e-5 * u, w) - loss(x - 1e-5 * u, w)) / 2e-5 - float((r["dx"] * u).sum())) < 1e-8
+    u = torch.randn(16, generator=g, dtype=torch.float64)
+    assert abs((loss(x, w + 1e-5 * u) - loss(x, w - 1e-5 * u)) / 2e-5 - float((r["dw"] * u).sum())) < 1e-8
+
+
+# ------------------------------------------------------------------ refusals
+P = 1 << 20  # 16-byte aligned addresses that no rejected call touches
+A = [P * (i + 1) * 16 for i in range(16)]
+
+
+def _window(lib, q=A[0], B=1, H=4, Hkv=2, S=256, D=64, N=4, layout=0, dtype=0, W=10, ns=0, o=A[3]):
+    return lib.striped_attn_window_fwd(q, A[1], A[2], o, A[4], B, H, Hkv, S, D, N, layout, dtype, W, ns,
+                                       ctypes.c_float(0.1), None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(q=None), INVALID), (dict(o=None), INVALID), (dict(B=0), INVALID), (dict(Hkv=3), INVALID),
+    (dict(Hkv=0), INVALID), (dict(S=255), INVALID), (dict(S=0), INVALID), (dict(N=0), INVALID),
+    (dict(layout=7), INVALID), (dict(dtype=9), INVALID), (dict(W=0), INVALID), (dict(W=-5), INVALID),
+    (dict(ns=-1), INVALID), (dict(dtype=1), UNSUPPORTED), (dict(D=96), UNSUPPORTED), (dict(ns=1025), UNSUPPORTED),
+    (dict(N=129, S=1290), UNSUPPORTED), (dict(layout=2), UNSUPPORTED), (dict(S=2 ** 31), UNSUPPORTED),
+    (dict(q=A[0] + 8), ALIGN), (dict(o=A[3] + 2), ALIGN)])
+def test_window_refusals(kw, want):
+    assert _window(sp.load(), **kw) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(dO=None), INVALID), (dict(ws=None), WORKSPACE), (dict(n=-1), WORKSPACE), (dict(ws=A[10] + 64), ALIGN),
+    (dict(dv=A[9] + 4), ALIGN), (dict(ns=2000), UNSUPPORTED), (dict(W=0), INVALID)])
+def test_window_backward_refusals(kw, want):
+    lib = sp.load()
+    a = dict(dO=A[5], dv=A[9], ws=A[10], n=0, W=10, ns=4) | kw
+    need = lib.striped_attn_window_workspace_size(1, 4, 2, 256, 64, 4, 0, 0, 10, 4)
+    assert need > 0
+    got = lib.striped_attn_window_bwd(A[0], A[1], A[2], A[3], A[4], a["dO"], A[7], A[8], a["dv"], a["ws"],
+                                      need + a["n"], 1, 4, 2, 256, 64, 4, 0, 0, a["W"], a["ns"], ctypes.c_float(0.1),
+                                      None)
+    assert got == want
+
+
+def test_window_workspace_size():
+    size = sp.load().striped_attn_window_workspace_size
+    assert size(1, 4, 2, 256, 64, 4, 0, 0, 0, 4) == 0 and size(1, 4, 2, 256, 64, 4, 0, 1, 8, 4) == 0
+    # fp32 dQ and two statistics a row; two tiles, no query lies above both windows
+    assert size(1, 4, 2, 256, 64, 4, 0, 0, 256, 4) == 4 * 256 * (64 * 4 + 8)
+    assert size(1, 4, 2, 4096, 64, 4, 0, 0, 10, 4) > 4 * 4096 * (64 * 4 + 8)
+
+
+def _rope(lib, q=A[0], k=A[1], yq=A[2], yk=A[3], w=A[4], f=A[5], pos=None, B=1, H=4, Hkv=2, S=64, D=64, rot=64, N=4,
+          layout=0, stripe=-1, eps=1e-6, dtype=0):
+    return lib.striped_qk_norm_rope(q, k, yq, yk, w, w, f, pos, B, H, Hkv, S, D, rot, 0, N, layout, stripe,
+                                    ctypes.c_float(eps), dtype, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(q=None), INVALID), (dict(yk=None), INVALID), (dict(w=None), INVALID), (dict(f=None), INVALID),
+    (dict(B=0), INVALID), (dict(H=0), INVALID), (dict(Hkv=0), INVALID), (dict(S=0), INVALID), (dict(S=63), INVALID),
+    (dict(N=0), INVALID), (dict(layout=3), INVALID), (dict(dtype=2), INVALID), (dict(rot=-16), INVALID),
+    (dict(rot=80), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID), (dict(stripe=4), INVALID),
+    (dict(stripe=-2), INVALID), (dict(layout=2, S=60), INVALID), (dict(layout=2, S=63, stripe=1), INVALID),
+    (dict(yq=A[1]), INVALID), (dict(yq=A[0] + 16), INVALID), (dict(yk=A[2] + 32), INVALID), (dict(yk=A[0]), INVALID),
+    (dict(D=40, rot=16), UNSUPPORTED), (dict(D=272, rot=16), UNSUPPORTED), (dict(rot=24), UNSUPPORTED),
+    (dict(q=A[0] + 2), ALIGN), (dict(yq=A[2] + 8), ALIGN), (dict(w=A[4] + 2), ALIGN), (dict(f=A[5] + 4), ALIGN),
+    (dict(pos=A[6] + 4), ALIGN)])
+def test_norm_rope_refusals(kw, want):
+    assert _rope(sp.load(), **kw) == want
+
+
+def test_norm_rope_backward_refusals():
+    lib = sp.load()
+    need = lib.striped_qk_norm_rope_workspace_size(1, 4, 2, 64, 64, 0)
+    assert need > 0 and lib.striped_qk_norm_rope_workspace_size(1, 4, 2, 64, 40, 0) == 0
+
+    def call(ws=A[12], n=need, g=A[2], dw=A[8]):
+        return lib.striped_qk_norm_rope_bwd(A[0], A[1], g, A[3], A[6], A[7], dw, A[9], A[10], A[11], A[13], None, ws,
+                                            n, 1, 4, 2, 64, 64, 64, 0, 4, 0, -1, ctypes.c_float(1e-6), 0, None)
+
+    assert call(ws=None) == WORKSPACE and call(n=need - 1) == WORKSPACE
+    assert call(g=None) == INVALID and call(dw=None) == INVALID and call(ws=A[12] + 4) == ALIGN
