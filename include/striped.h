@@ -350,6 +350,47 @@ int striped_attn_window_bwd(const void *q, const void *k, const void *v, const v
                             int64_t window, int64_t sinks, float scale, void *stream);
 
 /*
+ * Attention of a few new tokens of every request (decoding) against a prompt
+ * in placed rows and the request's own tail; not on the pages: what a model
+ * whose prompt was prefilled with striped_attn_fwd or striped_attn_window_fwd
+ * does next.  Bp prompts serve B requests (B % Bp == 0): request b continues
+ * prompt b / (B/Bp), whose rows are read once for all requests on it (Bp = 1:
+ * one prompt for the whole batch; Bp = B: a prompt each).
+ *  q, o:       [B,H,T,D], the T newest tokens of every request; lse [B,H,T].
+ *  k_prompt, v_prompt: [Bp,Hkv,P,D] in `layout` order over N stripes (the
+ *              rows as the prefill left them); P = 0: no prompt (NULL).
+ *  k_tail, v_tail: [B,Hkv,C,D], tail_lens: int32 [B] on the DEVICE: rows
+ *              0 .. len-1 of request b hold positions P .. P+len-1, the new
+ *              tokens' own keys among them (the T last).  Rows from len on
+ *              are never used, whatever they hold; a length outside 0..C is
+ *              taken as the nearer end.
+ * Token t stands at position P + len - T + t and keeps the keys at or before
+ * it; with window > 0 only those less than `window` before it or among the
+ * first `sinks` positions (window = 0: all).  A token before position 0
+ * (len + P < T) keeps none: o = 0, lse = -infinity.
+ * bf16 with D == 64 or 128, at most 128 stripes in the striped placement,
+ * zig-zag as for striped_attn_fwd, P + C <= 2^31 - 256; with g = H/Hkv * T
+ * rows a request, Bp * ceil(B/Bp * g / 128) (P > 0) + B * ceil(g / 128)
+ * <= 2048: else STRIPED_ERR_UNSUPPORTED (split the batch).
+ * Segments are joined in a fixed order: results are the same from run to run
+ * (on the same kind of GPU).  workspace: 256-byte aligned, >=
+ * striped_attn_decode_workspace_size() bytes, contents ignored; calls that
+ * may overlap (other streams, graphs replayed side by side) each need their
+ * own.
+ */
+int striped_attn_decode(const void *q, const void *k_prompt, const void *v_prompt, const void *k_tail,
+                        const void *v_tail, const int32_t *tail_lens, void *o, float *lse, void *workspace,
+                        size_t ws_bytes, int64_t B, int64_t Bp, int64_t H, int64_t Hkv, int64_t T, int64_t P,
+                        int64_t C, int64_t D, int N, int layout, int dtype, int64_t window, int64_t sinks, float scale,
+                        void *stream);
+
+/* Bytes of device workspace striped_attn_decode needs on the current device,
+ * or 0 for arguments that it rejects. */
+size_t striped_attn_decode_workspace_size(int64_t B, int64_t Bp, int64_t H, int64_t Hkv, int64_t T, int64_t P,
+                                          int64_t C, int64_t D, int N, int layout, int dtype, int64_t window,
+                                          int64_t sinks);
+
+/*
  * RMS norm of every query and key head and the rotary position rotation, in
  * one pass (not on the pages; the step between a layer's projections and its
  * attention, where every row needs the position that the placement gives

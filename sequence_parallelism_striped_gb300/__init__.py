@@ -52,6 +52,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = True):
     """Load libstriped.so (building it first if it is absent)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -91,6 +93,10 @@ def load(build_if_missing: bool = True):
         lib.striped_attn_window_workspace_size.restype = SZ
         lib.striped_attn_window_bwd.argtypes = [P, P, P, P, P, P, P, P, P, P, SZ, I64, I64, I64, I64, I64, I, I, I,
                                                 I64, I64, F, P]
+        lib.striped_attn_decode.argtypes = [P, P, P, P, P, P, P, P, P, SZ, I64, I64, I64, I64, I64, I64, I64, I64, I,
+                                            I, I, I64, I64, F, P]
+        lib.striped_attn_decode_workspace_size.argtypes = [I64, I64, I64, I64, I64, I64, I64, I64, I, I, I, I64, I64]
+        lib.striped_attn_decode_workspace_size.restype = SZ
         lib.striped_qk_norm_rope.argtypes = [P, P, P, P, P, P, P, P, I64, I64, I64, I64, I64, I, I, I, I, I, F, I, P]
         lib.striped_qk_norm_rope_workspace_size.argtypes = [I64, I64, I64, I64, I64, I]
         lib.striped_qk_norm_rope_workspace_size.restype = SZ
@@ -440,45 +446,60 @@ def striped_attn_bwd_varlen(q, k, v, o, lse, dO, cu_seqlens, N: int, layout: int
 
 
 # ------------------------------------------------------------------ argument checks
-def _need(t, name: str, shape, dtype, like: torch.Tensor):
-    """Pointer of an argument after checking its shape, type, device and
-    layout against what the call needs."""
-    p = _dev(t, name)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
-    return p
-
-
 def _rank(t, name: str, n: int):
     """A CUDA tensor of n dimensions (before its shape is read)."""
-    _dev(t, name)
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
     if t.dim() != n:
         raise ValueError(f"{name} must have {n} dimensions, got {t.dim()}")
 
 
+def _need(t, name: str, shape, dtype, dev: int) -> int:
+    """Address of a tensor argument that has the shape, type, device and
+    layout that the call needs."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _buffer(t, name: str, dev: int):
+    """Address and bytes of a workspace."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return _need(t, name, t.shape, t.dtype, dev), t.numel() * t.element_size()
+
+
 class _on:
-    """Run a call on the device of its tensors, whichever is current, on the
-    given stream or that device's current one."""
+    """Make a call on the device of its tensors, whichever is current, and on
+    the given stream or that device's current one.  What is allocated inside
+    belongs to that stream, so it is not handed out again before the call's
+    kernels are done with it."""
 
-    __slots__ = ("device", "stream", "guard")
+    __slots__ = ("dev", "stream", "guard")
 
-    def __init__(self, t: torch.Tensor, stream):
-        if stream is not None and stream.device != t.device:
-            raise ValueError(f"stream is on {stream.device}, tensors are on {t.device}")
-        self.device = t.device
+    def __init__(self, dev: int, stream):
+        if stream is not None and stream.device.index != dev:
+            raise ValueError(f"stream is on {stream.device}, tensors are on cuda:{dev}")
+        self.dev = dev
         self.stream = stream
         self.guard = None
 
-    def __enter__(self):
-        if torch.cuda.current_device() != self.device.index:
-            self.guard = torch.cuda.device(self.device)
+    def __enter__(self) -> int:
+        if self.stream is not None:
+            self.guard = torch.cuda.stream(self.stream)
+        elif torch.cuda.current_device() != self.dev:
+            self.guard = torch.cuda.device(self.dev)
+        if self.guard is not None:
             self.guard.__enter__()
-        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
-        return ctypes.c_void_p(s.cuda_stream)
+        return torch.cuda.current_stream().cuda_stream
 
     def __exit__(self, *exc):
         if self.guard is not None:
@@ -486,32 +507,24 @@ class _on:
 
 
 # ------------------------------------------------------------------ window attention
-def _qkv(q, k, v):
-    _rank(q, "q", 4)
-    _rank(k, "k", 4)
-    B, H, S, D = q.shape
-    Hkv = k.shape[1]
-    _need(k, "k", (B, Hkv, S, D), q.dtype, q)
-    _need(v, "v", (B, Hkv, S, D), q.dtype, q)
-    return B, H, Hkv, S, D
-
-
 def striped_attn_window_fwd(q, k, v, N: int, window: int, sinks: int = 0, layout: int = STRIPED,
                             scale: float | None = None, out=None, lse_out=None, stream=None):
     """Causal attention over the last `window` positions and the first `sinks`
     tokens: q [B,H,S,D], k and v [B,Hkv,S,D] bf16 in `layout` order.  Returns
     (o, lse)."""
-    B, H, Hkv, S, D = _qkv(q, k, v)
-    if scale is None:
-        scale = 1.0 / D ** 0.5
-    o = torch.empty_like(q) if out is None else out
-    lse = torch.empty((B, H, S), dtype=torch.float32, device=q.device) if lse_out is None else lse_out
-    with _on(q, stream) as st:
-        _check(load().striped_attn_window_fwd(_dev(q, "q"), _dev(k, "k"), _dev(v, "v"),
-                                              _need(o, "out", q.shape, q.dtype, q),
-                                              _need(lse, "lse_out", (B, H, S), torch.float32, q), B, H, Hkv, S, D, N,
-                                              layout, _dtype_code(q), int(window), int(sinks), float(scale), st),
-               "striped_attn_window_fwd")
+    _rank(q, "q", 4)
+    _rank(k, "k", 4)
+    B, H, S, D = q.shape
+    Hkv, dt, dev = k.shape[1], q.dtype, q.get_device()
+    kv = (B, Hkv, S, D)
+    with _on(dev, stream) as st:
+        o = torch.empty_like(q) if out is None else out
+        lse = torch.empty((B, H, S), dtype=torch.float32, device=q.device) if lse_out is None else lse_out
+        _check(load().striped_attn_window_fwd(
+            _need(q, "q", q.shape, dt, dev), _need(k, "k", kv, dt, dev), _need(v, "v", kv, dt, dev),
+            _need(o, "out", q.shape, dt, dev), _need(lse, "lse_out", (B, H, S), torch.float32, dev), B, H, Hkv, S, D,
+            N, layout, _dtype_code(q), int(window), int(sinks), 1.0 / D ** 0.5 if scale is None else float(scale), st),
+            "striped_attn_window_fwd")
     return o, lse
 
 
@@ -527,22 +540,78 @@ def striped_attn_window_bwd(q, k, v, o, lse, dO, N: int, window: int, sinks: int
                             scale: float | None = None, workspace: torch.Tensor | None = None, dq=None, dk=None,
                             dv=None, stream=None):
     """Backward of striped_attn_window_fwd; returns (dq, dk, dv)."""
-    B, H, Hkv, S, D = _qkv(q, k, v)
-    if scale is None:
-        scale = 1.0 / D ** 0.5
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    with _on(q, stream) as st:
+    _rank(q, "q", 4)
+    _rank(k, "k", 4)
+    B, H, S, D = q.shape
+    Hkv, dt, dev = k.shape[1], q.dtype, q.get_device()
+    qs, kv = q.shape, (B, Hkv, S, D)
+    with _on(dev, stream) as st:
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
         ws = new_window_workspace(q, k, N, window, sinks, layout) if workspace is None else workspace
+        wp, wn = _buffer(ws, "workspace", dev)
         _check(load().striped_attn_window_bwd(
-            _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _need(o, "o", q.shape, q.dtype, q),
-            _need(lse, "lse", (B, H, S), torch.float32, q), _need(dO, "dO", q.shape, q.dtype, q),
-            _need(dq, "dq", q.shape, q.dtype, q), _need(dk, "dk", k.shape, q.dtype, q),
-            _need(dv, "dv", k.shape, q.dtype, q), _need(ws, "workspace", ws.shape, ws.dtype, q),
-            ws.numel() * ws.element_size(), B, H, Hkv, S, D, N, layout, _dtype_code(q), int(window), int(sinks),
-            float(scale), st), "striped_attn_window_bwd")
+            _need(q, "q", qs, dt, dev), _need(k, "k", kv, dt, dev), _need(v, "v", kv, dt, dev),
+            _need(o, "o", qs, dt, dev), _need(lse, "lse", (B, H, S), torch.float32, dev),
+            _need(dO, "dO", qs, dt, dev), _need(dq, "dq", qs, dt, dev), _need(dk, "dk", kv, dt, dev),
+            _need(dv, "dv", kv, dt, dev), wp, wn, B, H, Hkv, S, D, N, layout, _dtype_code(q), int(window), int(sinks),
+            1.0 / D ** 0.5 if scale is None else float(scale), st), "striped_attn_window_bwd")
     return dq, dk, dv
+
+
+# ------------------------------------------------------------------ decoding
+def _decode_sizes(q, k_prompt, k_tail):
+    _rank(q, "q", 4)
+    _rank(k_tail, "k_tail", 4)
+    B, H, T, D = q.shape
+    Hkv, C = k_tail.shape[1], k_tail.shape[2]
+    Bp, P = 1, 0
+    if k_prompt is not None:
+        _rank(k_prompt, "k_prompt", 4)
+        Bp, P = k_prompt.shape[0], k_prompt.shape[2]
+    return B, Bp, H, Hkv, T, P, C, D
+
+
+def new_decode_workspace(q, k_prompt, k_tail, N: int = 1, layout: int = STRIPED, window: int = 0,
+                         sinks: int = 0) -> torch.Tensor:
+    """Workspace of striped_attn_decode for these tensors and arguments."""
+    n = _decode_sizes(q, k_prompt, k_tail)
+    with _on(q.get_device(), None):
+        need = int(load().striped_attn_decode_workspace_size(*n, N, layout, _dtype_code(q), int(window), int(sinks)))
+    return torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+
+
+def striped_attn_decode(q, k_prompt, v_prompt, k_tail, v_tail, tail_lens, N: int = 1, layout: int = STRIPED,
+                        window: int = 0, sinks: int = 0, scale: float | None = None,
+                        workspace: torch.Tensor | None = None, out=None, lse_out=None, stream=None):
+    """The T newest tokens of every request, q [B,H,T,D], against the prompt
+    [Bp,Hkv,P,D] in `layout` rows that B/Bp requests share (None: no prompt)
+    and their own tails [B,Hkv,C,D], of which the first tail_lens (int32 [B],
+    on the device) rows are written.  window 0: full attention.  Returns
+    (o [B,H,T,D], lse [B,H,T])."""
+    n = B, Bp, H, Hkv, T, P, C, D = _decode_sizes(q, k_prompt, k_tail)
+    dt, dev, code = q.dtype, q.get_device(), _dtype_code(q)
+    window, sinks = int(window), int(sinks)
+    kp = vp = None
+    if k_prompt is not None:
+        kp = _need(k_prompt, "k_prompt", (Bp, Hkv, P, D), dt, dev)
+        vp = _need(v_prompt, "v_prompt", (Bp, Hkv, P, D), dt, dev)
+    tail = (B, Hkv, C, D)
+    with _on(dev, stream) as st:
+        o = torch.empty_like(q) if out is None else out
+        lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device) if lse_out is None else lse_out
+        if workspace is None:
+            need = int(load().striped_attn_decode_workspace_size(*n, N, layout, code, window, sinks))
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        wp, wn = _buffer(workspace, "workspace", dev)
+        _check(load().striped_attn_decode(
+            _need(q, "q", q.shape, dt, dev), kp, vp, _need(k_tail, "k_tail", tail, dt, dev),
+            _need(v_tail, "v_tail", tail, dt, dev), _need(tail_lens, "tail_lens", (B,), torch.int32, dev),
+            _need(o, "out", q.shape, dt, dev), _need(lse, "lse_out", (B, H, T), torch.float32, dev), wp, wn, *n, N,
+            layout, code, window, sinks, 1.0 / D ** 0.5 if scale is None else float(scale), st),
+            "striped_attn_decode")
+    return o, lse
 
 
 # ------------------------------------------------------------------ norm and rotation
@@ -553,20 +622,6 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, device="cuda") -> t
     return float(base) ** (-2.0 * j / max(1, rotary_dim))
 
 
-def _rope_args(q, k, q_weight, k_weight, inv_freq, positions):
-    _rank(q, "q", 4)
-    _rank(k, "k", 4)
-    B, H, S, D = q.shape
-    Hkv = k.shape[1]
-    code = _dtype_code(q)
-    _need(k, "k", (B, Hkv, S, D), q.dtype, q)
-    _rank(inv_freq, "inv_freq", 1)
-    ptrs = [_need(q_weight, "q_weight", (D,), torch.float32, q), _need(k_weight, "k_weight", (D,), torch.float32, q),
-            _need(inv_freq, "inv_freq", inv_freq.shape, torch.float64, q),
-            None if positions is None else _need(positions, "positions", (B, S), torch.int64, q)]
-    return B, H, Hkv, S, D, code, ptrs
-
-
 def striped_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, N: int = 1, layout: int = STRIPED,
                          stripe: int | None = None, positions: torch.Tensor | None = None, eps: float = 1e-6,
                          interleaved: bool = False, q_out=None, k_out=None, stream=None):
@@ -575,15 +630,22 @@ def striped_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, N: int = 1, layout:
     [B,S]: the rows' own positions); q_weight, k_weight fp32 [D], inv_freq
     fp64 [rotary_dim/2] (rope_frequencies).  Returns (q_out, k_out), which may
     be q and k themselves."""
-    B, H, Hkv, S, D, code, (qw, kw, fr, pos) = _rope_args(q, k, q_weight, k_weight, inv_freq, positions)
-    yq = torch.empty_like(q) if q_out is None else q_out
-    yk = torch.empty_like(k) if k_out is None else k_out
-    with _on(q, stream) as st:
-        _check(load().striped_qk_norm_rope(_dev(q, "q"), _dev(k, "k"), _need(yq, "q_out", q.shape, q.dtype, q),
-                                           _need(yk, "k_out", k.shape, q.dtype, q), qw, kw, fr, pos, B, H, Hkv, S, D,
-                                           2 * inv_freq.numel(), int(bool(interleaved)), N, layout,
-                                           -1 if stripe is None else int(stripe), float(eps), code, st),
-               "striped_qk_norm_rope")
+    _rank(q, "q", 4)
+    _rank(k, "k", 4)
+    _rank(inv_freq, "inv_freq", 1)
+    B, H, S, D = q.shape
+    Hkv, dt, dev = k.shape[1], q.dtype, q.get_device()
+    qs, ks, half, f32 = q.shape, (B, Hkv, S, D), inv_freq.shape[0], torch.float32
+    with _on(dev, stream) as st:
+        yq = torch.empty_like(q) if q_out is None else q_out
+        yk = torch.empty_like(k) if k_out is None else k_out
+        _check(load().striped_qk_norm_rope(
+            _need(q, "q", qs, dt, dev), _need(k, "k", ks, dt, dev), _need(yq, "q_out", qs, dt, dev),
+            _need(yk, "k_out", ks, dt, dev), _need(q_weight, "q_weight", (D,), f32, dev),
+            _need(k_weight, "k_weight", (D,), f32, dev), _need(inv_freq, "inv_freq", (half,), torch.float64, dev),
+            None if positions is None else _need(positions, "positions", (B, S), torch.int64, dev), B, H, Hkv, S, D,
+            2 * half, 1 if interleaved else 0, N, layout, -1 if stripe is None else int(stripe), float(eps),
+            _dtype_code(q), st), "striped_qk_norm_rope")
     return yq, yk
 
 
@@ -601,21 +663,28 @@ def striped_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, inv_freq,
     """Backward of striped_qk_norm_rope: q and k are its inputs, dq_out and
     dk_out the cotangents of its outputs.  Returns (dq, dk, dq_weight fp32
     [D], dk_weight fp32 [D])."""
-    B, H, Hkv, S, D, code, (qw, kw, fr, pos) = _rope_args(q, k, q_weight, k_weight, inv_freq, positions)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dqw = torch.empty_like(q_weight) if dq_weight is None else dq_weight
-    dkw = torch.empty_like(k_weight) if dk_weight is None else dk_weight
-    with _on(q, stream) as st:
+    _rank(q, "q", 4)
+    _rank(k, "k", 4)
+    _rank(inv_freq, "inv_freq", 1)
+    B, H, S, D = q.shape
+    Hkv, dt, dev = k.shape[1], q.dtype, q.get_device()
+    qs, ks, half, f32 = q.shape, (B, Hkv, S, D), inv_freq.shape[0], torch.float32
+    with _on(dev, stream) as st:
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dqw = torch.empty_like(q_weight) if dq_weight is None else dq_weight
+        dkw = torch.empty_like(k_weight) if dk_weight is None else dk_weight
         ws = qk_norm_rope_workspace(q, k) if workspace is None else workspace
+        wp, wn = _buffer(ws, "workspace", dev)
         _check(load().striped_qk_norm_rope_bwd(
-            _dev(q, "q"), _dev(k, "k"), _need(dq_out, "dq_out", q.shape, q.dtype, q),
-            _need(dk_out, "dk_out", k.shape, q.dtype, q), _need(dq, "dq", q.shape, q.dtype, q),
-            _need(dk, "dk", k.shape, q.dtype, q), _need(dqw, "dq_weight", (D,), torch.float32, q),
-            _need(dkw, "dk_weight", (D,), torch.float32, q), qw, kw, fr, pos,
-            _need(ws, "workspace", ws.shape, ws.dtype, q), ws.numel() * ws.element_size(), B, H, Hkv, S, D,
-            2 * inv_freq.numel(), int(bool(interleaved)), N, layout, -1 if stripe is None else int(stripe),
-            float(eps), code, st), "striped_qk_norm_rope_bwd")
+            _need(q, "q", qs, dt, dev), _need(k, "k", ks, dt, dev), _need(dq_out, "dq_out", qs, dt, dev),
+            _need(dk_out, "dk_out", ks, dt, dev), _need(dq, "dq", qs, dt, dev), _need(dk, "dk", ks, dt, dev),
+            _need(dqw, "dq_weight", (D,), f32, dev), _need(dkw, "dk_weight", (D,), f32, dev),
+            _need(q_weight, "q_weight", (D,), f32, dev), _need(k_weight, "k_weight", (D,), f32, dev),
+            _need(inv_freq, "inv_freq", (half,), torch.float64, dev),
+            None if positions is None else _need(positions, "positions", (B, S), torch.int64, dev), wp, wn, B, H,
+            Hkv, S, D, 2 * half, 1 if interleaved else 0, N, layout, -1 if stripe is None else int(stripe),
+            float(eps), _dtype_code(q), st), "striped_qk_norm_rope_bwd")
     return dq, dk, dqw, dkw
 
 

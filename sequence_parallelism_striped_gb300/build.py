@@ -19,7 +19,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libstriped.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "permute.cu", "attn_simt.cu", "attn_fwd_tc.cu", "attn_fwd_pair.cu", "attn_bwd_tc.cu", "attn_bwd_noalloc.cu",
-           "norm_rope.cu", "attn_window_fwd.cu", "attn_window_bwd.cu", "host_model.cpp"]
+           "norm_rope.cu", "attn_window_fwd.cu", "attn_window_bwd.cu", "attn_decode.cu", "host_model.cpp"]
 
 
 def _nvcc() -> str:

@@ -610,6 +610,54 @@ int striped_attn_window_bwd(const void *q, const void *k, const void *v, const v
     return launch_tc_window_bwd(q, k, v, o, lse, dO, dq, dk, dv, workspace, a, (cudaStream_t)stream);
 }
 
+// ---------------------------------------------------------------- decoding
+static int check_decode(const DecodeArgs &a, int dtype) {
+    if (a.B < 1 || a.H < 1 || a.Hkv < 1 || a.H % a.Hkv != 0 || a.T < 1 || a.P < 0 || a.C < 1 || a.window < 0 ||
+        a.sinks < 0)
+        return STRIPED_ERR_INVALID_ARG;
+    if (dtype != STRIPED_BF16) return dtype == STRIPED_FP32 ? STRIPED_ERR_UNSUPPORTED : STRIPED_ERR_INVALID_ARG;
+    if (a.D != 64 && a.D != 128) return a.D < 1 ? STRIPED_ERR_INVALID_ARG : STRIPED_ERR_UNSUPPORTED;
+    if (a.Bp < 1 || a.B % a.Bp != 0) return STRIPED_ERR_INVALID_ARG;
+    if (a.P > 0) {
+        const int st = check_attn(a.Bp, a.Hkv, a.P, a.D, a.N, a.layout, dtype);
+        if (st) return st;
+        if (a.layout == STRIPED_LAYOUT_STRIPED && a.N > 128) return STRIPED_ERR_UNSUPPORTED;
+    }
+    const int64_t limit = 1ll << 30;  // counts that the kernels hold in 32 bits
+    if (a.P > kMaxPositions || a.C > kMaxPositions || a.P + a.C > kMaxPositions) return STRIPED_ERR_UNSUPPORTED;
+    if (a.B > limit || a.H > limit || a.T > limit || a.B * a.H > limit || a.B * a.H * a.T > limit)
+        return STRIPED_ERR_UNSUPPORTED;
+    return decode_workspace(a) == 0 ? STRIPED_ERR_UNSUPPORTED : STRIPED_OK;
+}
+
+size_t striped_attn_decode_workspace_size(int64_t B, int64_t Bp, int64_t H, int64_t Hkv, int64_t T, int64_t P,
+                                          int64_t C, int64_t D, int N, int layout, int dtype, int64_t window,
+                                          int64_t sinks) {
+    const DecodeArgs a{B, Bp, H, Hkv, T, P, C, D, N, layout, window, sinks, 1.f};
+    return check_decode(a, dtype) ? 0 : decode_workspace(a);
+}
+
+int striped_attn_decode(const void *q, const void *k_prompt, const void *v_prompt, const void *k_tail,
+                        const void *v_tail, const int32_t *tail_lens, void *o, float *lse, void *workspace,
+                        size_t ws_bytes, int64_t B, int64_t Bp, int64_t H, int64_t Hkv, int64_t T, int64_t P,
+                        int64_t C, int64_t D, int N, int layout, int dtype, int64_t window, int64_t sinks, float scale,
+                        void *stream) {
+    if (!q || !k_tail || !v_tail || !tail_lens || !o || !lse) return STRIPED_ERR_INVALID_ARG;
+    if (P > 0 && (!k_prompt || !v_prompt)) return STRIPED_ERR_INVALID_ARG;
+    const DecodeArgs a{B, Bp, H, Hkv, T, P, C, D, N, layout, window, sinks, scale};
+    const int st = check_decode(a, dtype);
+    if (st) return st;
+    if (!workspace || ws_bytes < decode_workspace(a)) return STRIPED_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return STRIPED_ERR_ALIGN;
+    const void *ptrs[5] = {q, k_tail, v_tail, o, lse};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return STRIPED_ERR_ALIGN;
+    if (P > 0 && (!aligned16(k_prompt) || !aligned16(v_prompt))) return STRIPED_ERR_ALIGN;
+    if ((reinterpret_cast<uintptr_t>(tail_lens) & 3u) != 0) return STRIPED_ERR_ALIGN;
+    return launch_tc_decode(q, k_prompt, v_prompt, k_tail, v_tail, tail_lens, o, lse, workspace, a,
+                            (cudaStream_t)stream);
+}
+
 // ---------------------------------------------------------------- norm and rotation
 // Two buffers may be the same one (`alias`: results over their own inputs)
 // but must not overlap in any other way.

@@ -145,6 +145,18 @@ size_t window_bwd_workspace(const WindowArgs &a);  // 0: no kernel for these siz
 int launch_tc_window_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse, const void *dO,
                          void *dq, void *dk, void *dv, void *workspace, const WindowArgs &a, cudaStream_t stream);
 
+// ---- attn_decode.cu
+struct DecodeArgs {
+    int64_t B, Bp, H, Hkv, T, P, C, D;
+    int N, layout;
+    int64_t window, sinks;  // window 0: none
+    float scale;
+};
+size_t decode_workspace(const DecodeArgs &a);  // 0: no kernel for these sizes
+int launch_tc_decode(const void *q, const void *kp, const void *vp, const void *kt, const void *vt,
+                     const int32_t *lens, void *o, float *lse, void *workspace, const DecodeArgs &a,
+                     cudaStream_t stream);
+
 // ---- norm_rope.cu
 // Norm and rotation of q [B][H][S][D] and k [B][Hkv][S][D] (forward: dq_out
 // and dk_out NULL, results in q_res and k_res; backward: cotangents in

@@ -180,3 +180,31 @@ def test_norm_rope_backward_refusals():
 
     assert call(ws=None) == WORKSPACE and call(n=need - 1) == WORKSPACE
     assert call(g=None) == INVALID and call(dw=None) == INVALID and call(ws=A[12] + 4) == ALIGN
+
+
+def _decode(lib, q=A[0], kp=A[1], vp=A[2], kt=A[3], vt=A[4], lens=A[5], o=A[6], lse=A[7], ws=A[8], n=1 << 40, B=4, Bp=2,
+            H=4, Hkv=2, T=1, P=256, C=16, D=64, N=4, layout=0, dtype=0, W=0, ns=0):
+    return lib.striped_attn_decode(q, kp, vp, kt, vt, lens, o, lse, ws, n, B, Bp, H, Hkv, T, P, C, D, N, layout,
+                                   dtype, W, ns, ctypes.c_float(0.1), None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(q=None), INVALID), (dict(kp=None), INVALID), (dict(vp=None), INVALID), (dict(vt=None), INVALID),
+    (dict(lens=None), INVALID), (dict(lse=None), INVALID), (dict(B=0), INVALID), (dict(Bp=3), INVALID),
+    (dict(Bp=0), INVALID), (dict(Hkv=3), INVALID), (dict(T=0), INVALID), (dict(P=-4), INVALID), (dict(C=0), INVALID),
+    (dict(P=255), INVALID), (dict(N=0), INVALID), (dict(layout=4), INVALID), (dict(dtype=5), INVALID),
+    (dict(W=-1), INVALID), (dict(ns=-1), INVALID), (dict(dtype=1), UNSUPPORTED), (dict(D=96), UNSUPPORTED),
+    (dict(N=129, P=1290), UNSUPPORTED), (dict(layout=2, P=264), UNSUPPORTED), (dict(C=2 ** 31), UNSUPPORTED),
+    (dict(B=4096, Bp=1), UNSUPPORTED), (dict(B=2048, Bp=2048), UNSUPPORTED), (dict(T=2 ** 31), UNSUPPORTED),
+    (dict(ws=None), WORKSPACE), (dict(n=100), WORKSPACE), (dict(ws=A[8] + 16), ALIGN), (dict(q=A[0] + 2), ALIGN),
+    (dict(vp=A[2] + 8), ALIGN), (dict(lens=A[5] + 2), ALIGN), (dict(lse=A[7] + 4), ALIGN)])
+def test_decode_refusals(kw, want):
+    assert _decode(sp.load(), **kw) == want
+
+
+def test_decode_workspace_size():
+    size = sp.load().striped_attn_decode_workspace_size
+    assert size(4, 2, 4, 2, 1, 256, 16, 64, 4, 0, 0, 0, 0) > 0
+    assert size(4, 3, 4, 2, 1, 256, 16, 64, 4, 0, 0, 0, 0) == 0
+    assert size(4, 2, 4, 2, 1, 256, 16, 64, 4, 0, 1, 0, 0) == 0
+    assert size(4, 1, 4, 2, 1, 0, 16, 64, 4, 0, 0, 0, 0) > 0  # no prompt: N and layout are not looked at
