@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include <mutex>
+#include <utility>
 
 #include "common.cuh"
 #include "internal.h"
@@ -65,10 +66,12 @@ typedef CUresult (*EncodeTiledFnT)(CUtensorMap *, CUtensorMapDataType, cuuint32_
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 // [BH][N][L][D] tensor of `esize`-byte elements -> 4-D tiled tensor map,
-// boxes of box_x elements x box_rows rows x box_stripes, 128-byte swizzle, zero fill.
+// boxes of box_x elements x box_rows rows, 128-byte swizzle, zero fill;
+// with box_stripes > 0 the stripes are the dimension inside the rows and a
+// box has that many.
 static int make_map(CUtensorMap *map, CUtensorMapDataType dt, int64_t esize, const void *base, int64_t D,
                     int64_t L, int64_t N, int64_t BH, int64_t stripe_stride, int64_t stride_bh, int box_x,
-                    int box_rows, int box_stripes = 1) {
+                    int box_rows, int box_stripes = 0) {
     // the driver entry point is process-wide: resolved once, under a lock
     static std::mutex mu;
     static EncodeTiledFnT fn = nullptr;
@@ -87,7 +90,13 @@ static int make_map(CUtensorMap *map, CUtensorMapDataType dt, int64_t esize, con
     cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)L, (cuuint64_t)N, (cuuint64_t)BH};
     cuuint64_t strides[3] = {(cuuint64_t)(D * esize), (cuuint64_t)(stripe_stride * esize),
                              (cuuint64_t)(stride_bh * esize)};
-    cuuint32_t box[4] = {(cuuint32_t)box_x, (cuuint32_t)box_rows, (cuuint32_t)box_stripes, 1};
+    cuuint32_t box[4] = {(cuuint32_t)box_x, (cuuint32_t)box_rows, 1, 1};
+    if (box_stripes > 0) {  // stripes inside rows: consecutive positions
+        std::swap(dims[1], dims[2]);
+        std::swap(strides[0], strides[1]);
+        box[1] = (cuuint32_t)box_stripes;
+        box[2] = (cuuint32_t)box_rows;
+    }
     cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = fn(map, dt, 4, const_cast<void *>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -114,7 +123,7 @@ int make_f32_map(CUtensorMap *map, const void *base, int64_t D, int64_t L, int64
 int make_pos_map(CUtensorMap *map, const void *base, int64_t D, const PosGeom &g, int64_t BH) {
     const int64_t L = g.L;
     return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, D, L, g.N, BH, L * D, (int64_t)g.S * D, 64, g.R,
-                    g.layout == STRIPED_LAYOUT_STRIPED ? g.N : 1);
+                    g.layout == STRIPED_LAYOUT_STRIPED ? g.N : 0);
 }
 
 // ---------------------------------------------------------------- validation

@@ -54,8 +54,7 @@ struct DecCfg {
     static constexpr int NS = HD == 128 ? 3 : 6;  // K/V stages
     static constexpr uint32_t kTile = (HD / 64) * kDBox;
     static constexpr uint32_t kStage = 2 * kTile;
-    static constexpr uint32_t kPosOff = NS * kStage;
-    static constexpr uint32_t kSpanOff = kPosOff + DT * 4;
+    static constexpr uint32_t kSpanOff = NS * kStage;
     static constexpr uint32_t kBarOff = kSpanOff + (3 * kMaxEntries + 4) * 4;
     static constexpr size_t kSmemBytes = 1024 + kBarOff + 256;
     static_assert(kSmemBytes <= 232448, "shared memory over the per-block limit");
@@ -169,7 +168,6 @@ __global__ void __launch_bounds__(kDThreads, 1)
     uint8_t *smem =
         reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     DecBars<NS> *bars = reinterpret_cast<DecBars<NS> *>(smem + Cfg::kBarOff);
-    int *col_pos = reinterpret_cast<int *>(smem + Cfg::kPosOff);
     int *cum = reinterpret_cast<int *>(smem + Cfg::kSpanOff);  // [entries + 1]
     int *lo_of = cum + kMaxEntries + 4, *ns_of = lo_of + kMaxEntries;
     const uint32_t sbase = smem_u32(smem);
@@ -193,8 +191,6 @@ __global__ void __launch_bounds__(kDThreads, 1)
         tmem_alloc(smem_u32(&bars->tmem_slot), 512);
         tmem_relinquish();
     }
-    if (threadIdx.x < DT)
-        col_pos[threadIdx.x] = p.ep > 0 && (int)threadIdx.x < g.P ? tile_pos(g, threadIdx.x) : 0x3fffffff;
     if (p.ep > 0 && g.P < DT) {
         // rows past a prompt tile's positions are never loaded: V has to be
         // finite there, because P = 0 times it is added to O
@@ -274,8 +270,8 @@ __global__ void __launch_bounds__(kDThreads, 1)
                 mbar_arrive_expect_tx(fb, bytes);
 #pragma unroll
                 for (int c = 0; c < kBoxes; ++c) {
-                    tma_load_4d(kdst + c * kDBox, mk, fb, 64 * c, at.row, at.stripe, head);
-                    tma_load_4d(vdst + c * kDBox, mv, fb, 64 * c, at.row, at.stripe, head);
+                    tma_load_4d(kdst + c * kDBox, mk, fb, 64 * c, at.c1, at.c2, head);
+                    tma_load_4d(vdst + c * kDBox, mv, fb, 64 * c, at.c1, at.c2, head);
                 }
             }
         }
@@ -283,22 +279,26 @@ __global__ void __launch_bounds__(kDThreads, 1)
         // so that on an error path none lands after the CTA has exited
         for (int t = j > NS ? j - NS : 0; t < j; ++t)
             if (!(skip_first && t == 0)) mbar_wait(smem_u32(&bars->kv_full[t % NS]), (t / NS) & 1, p.wc);
-    } else if (warp == 1 && lane == 0 && nx > 0) {
-        // ---------------- MMA issuer
+    } else if (warp == 1 && nx > 0) {
+        // ---------------- MMA issuer (the whole warp, one lane issues)
         constexpr uint32_t idesc_qk = idesc_bf16_f32(DT, DT, false, false);
         constexpr uint32_t idesc_pv = idesc_bf16_f32(DT, HD, false, true);
+        const bool leader = elect_one();
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint32_t uO = tm + 256, uQ = tm + 256 + HD;
+        const uint64_t dk = sdesc_sw128(sbase, 16, 1024), dv = sdesc_sw128(sbase + kTile, kDBox, 1024);
         auto issue_s = [&](int t) -> bool {
             const int s = t % NS;
-            if (!mbar_wait(smem_u32(&bars->kv_full[s]), (t / NS) & 1, p.wc)) return false;
+            if (!mbar_wait_warp(smem_u32(&bars->kv_full[s]), (t / NS) & 1, p.wc)) return false;
             tc_fence_after();
-            const uint32_t kaddr = sbase + s * kStage;
-            const uint32_t dS = (t & 1) ? tS1 : tS0;
+            if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < HD / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * kDBox + (kk & 3) * 32;
-                mma_ts(dS, tQ + kk * 8, sdesc_sw128(kaddr + off, 16, 1024), idesc_qk, kk > 0 ? 1u : 0u);
+                for (int kk = 0; kk < HD / 16; ++kk)
+                    mma_ts(tm + 128 * (t & 1), uQ + kk * 8,
+                           dk + s * (kStage >> 4) + (((kk >> 2) * kDBox + (kk & 3) * 32) >> 4), idesc_qk,
+                           kk > 0 ? 1u : 0u);
+                mma_commit(smem_u32(&bars->s_full[t & 1]));
             }
-            mma_commit(smem_u32(&bars->s_full[t & 1]));
             return true;
         };
         bool ok = true;
@@ -307,31 +307,31 @@ __global__ void __launch_bounds__(kDThreads, 1)
             const Segment sg = segment_at(cum, lo_of, ns_of, p.entries, p.Hkv, x0 + j, x1);
             const int j1 = j + sg.t1 - sg.t0;
             const int first = j;
-            ok = mbar_wait(smem_u32(&bars->q_full), seg & 1, p.wc);
+            ok = mbar_wait_warp(smem_u32(&bars->q_full), seg & 1, p.wc);
             tc_fence_after();
             if (ok) ok = issue_s(j);
             if (ok && j + 1 < j1) ok = issue_s(j + 1);
             for (; j < j1 && ok; ++j) {
-                ok = mbar_wait(smem_u32(&bars->p_ready), j & 1, p.wc);
+                ok = mbar_wait_warp(smem_u32(&bars->p_ready), j & 1, p.wc);
                 if (!ok) break;
                 tc_fence_after();
                 const int s = j % NS;
-                const uint32_t vaddr = sbase + s * kStage + kTile;
-                const uint32_t tP = (j & 1) ? tS1 : tS0;
+                if (leader) {
 #pragma unroll
-                for (int kk = 0; kk < DT / 16; ++kk)
-                    mma_ts(tO, tP + kk * 8, sdesc_sw128(vaddr + kk * 2048, kDBox, 1024), idesc_pv,
-                           (j > first || kk > 0) ? 1u : 0u);
-                // only stages the producer will refill get a release (no
-                // arrival may land after the CTA has exited)
-                if (j + NS < nx) mma_commit(smem_u32(&bars->kv_empty[s]));
-                mma_commit(smem_u32(&bars->o_done));
+                    for (int kk = 0; kk < DT / 16; ++kk)
+                        mma_ts(uO, tm + 128 * (j & 1) + kk * 8, dv + s * (kStage >> 4) + kk * (2048 >> 4), idesc_pv,
+                               (j > first || kk > 0) ? 1u : 0u);
+                    // only stages the producer will refill get a release (no
+                    // arrival may land after the CTA has exited)
+                    if (j + NS < nx) mma_commit(smem_u32(&bars->kv_empty[s]));
+                    mma_commit(smem_u32(&bars->o_done));
+                }
                 if (j + 2 < j1) ok = issue_s(j + 2);
             }
         }
         // every MMA issued above completes before TMEM is freed (error paths)
-        mma_commit(smem_u32(&bars->drain));
-        mbar_wait(smem_u32(&bars->drain), 0, p.wc);
+        if (leader) mma_commit(smem_u32(&bars->drain));
+        mbar_wait_warp(smem_u32(&bars->drain), 0, p.wc);
     } else if (warp >= 2 && nx > 0) {
         // ---------------- softmax + partial results
         const int quarter = warp & 3;
@@ -442,15 +442,15 @@ __global__ void __launch_bounds__(kDThreads, 1)
                     }
                     const bool full = tile_w == DT && kbase + DT - 1 <= hi && (kbase >= lo || kbase + DT <= sk);
                     if (!__all_sync(0xffffffffu, full)) {
-                        const int h2 = hi - kbase, l2 = lo - kbase, s2 = sk - kbase;
+                        // columns past the tile's positions are never kept
+                        const int h2 = min(hi - kbase, tile_w - 1), l2 = lo - kbase, s2 = sk - kbase;
 #pragma unroll
-                        for (int c = 0; c < DT; c += 4) {
-                            int4 kp = make_int4(c, c + 1, c + 2, c + 3);
-                            if (!tail) kp = *reinterpret_cast<const int4 *>(col_pos + c);
-                            if (!(kp.x <= h2 && (kp.x >= l2 || kp.x < s2))) sv[c] = -INFINITY;
-                            if (!(kp.y <= h2 && (kp.y >= l2 || kp.y < s2))) sv[c + 1] = -INFINITY;
-                            if (!(kp.z <= h2 && (kp.z >= l2 || kp.z < s2))) sv[c + 2] = -INFINITY;
-                            if (!(kp.w <= h2 && (kp.w >= l2 || kp.w < s2))) sv[c + 3] = -INFINITY;
+                        for (int w = 0; w < DT / 32; ++w) {
+                            const uint32_t k = kept_bits(32 * w, h2, l2, s2);
+                            if (!__all_sync(0xffffffffu, k == ~0u))
+#pragma unroll
+                                for (int c = 0; c < 32; ++c)
+                                    if (!(k & (1u << c))) sv[32 * w + c] = -INFINITY;
                         }
                     }
                     float mx8[8];

@@ -60,8 +60,7 @@ struct WinBwdCfg {
     static constexpr uint32_t kQOff = 2 * kTile;                // stage s: Q at kQOff + s*2*kTile, dO after
     static constexpr uint32_t kDSOff = kQOff + QS * 2 * kTile;  // dS (MN-major A operand)
     static constexpr uint32_t kStatOff = kDSOff + 2 * kBox;     // per stage: [LSE*log2e 128 | Delta 128]
-    static constexpr uint32_t kPosOff = kStatOff + QS * kStatBytes;  // position of every row of a tile
-    static constexpr uint32_t kBarOff = kPosOff + BT * 4;
+    static constexpr uint32_t kBarOff = kStatOff + QS * kStatBytes;
     static constexpr size_t kSmemBytes = kBarOff + 256;           // the dynamic smem base is 1024-aligned
     static_assert(kSmemBytes <= 232448, "shared memory over the per-block limit");
 };
@@ -115,7 +114,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     Bars *bars = reinterpret_cast<Bars *>(smem + Cfg::kBarOff);
     const uint32_t sbase = smem_u32(smem);
     const PosGeom &g = p.g;
-    int *col_pos = reinterpret_cast<int *>(smem + Cfg::kPosOff);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
     // Head-major order: resident CTAs belong to one key/value head and sweep
@@ -162,7 +160,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&bars->drain), 1);
         fence_barrier_init();
     }
-    if (threadIdx.x < BT) col_pos[threadIdx.x] = tile_pos(g, threadIdx.x);
     if (g.P < BT) {
         // rows past the tile's positions are never loaded: they must hold
         // finite values, because P = 0 times them is added to the gradients
@@ -190,9 +187,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tile_bytes = kBoxes * (uint32_t)g.P * 128;
         mbar_arrive_expect_tx(kb, 2 * tile_bytes);
 #pragma unroll
-        for (int x = 0; x < kBoxes; ++x) tma_load_4d(sbase + kKOff + x * kBox, &tmK, kb, 64 * x, kat.row, kat.stripe, (int)bh);
+        for (int x = 0; x < kBoxes; ++x) tma_load_4d(sbase + kKOff + x * kBox, &tmK, kb, 64 * x, kat.c1, kat.c2, (int)bh);
 #pragma unroll
-        for (int x = 0; x < kBoxes; ++x) tma_load_4d(sbase + kVOff + x * kBox, &tmV, kb, 64 * x, kat.row, kat.stripe, (int)bh);
+        for (int x = 0; x < kBoxes; ++x) tma_load_4d(sbase + kVOff + x * kBox, &tmV, kb, 64 * x, kat.c1, kat.c2, (int)bh);
         // test hook: the first Q tile is never loaded, so every wait on it
         // runs out (the kernel must then record the timeout and return)
         const bool skip_first = p.wc.inject == kInjectBwdSkipQ;
@@ -210,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bulk_load(sbase + kStatOff + s * kStatBytes, p.stats + ((bq * g.nt + qt) << 8), kStatBytes, fb);
 #pragma unroll
             for (int x = 0; x < kBoxes; ++x)
-                tma_load_4d(qdst + x * kBox, &tmQ, fb, 64 * x, at.row, at.stripe, (int)bq);
+                tma_load_4d(qdst + x * kBox, &tmQ, fb, 64 * x, at.c1, at.c2, (int)bq);
         }
         // K, V and loads [0, i) were issued: wait (bounded) for the last of
         // each stage, so that on an error path none lands after the CTA exits
@@ -232,98 +229,107 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx(fb, kBoxes * (uint32_t)g.P * 128);
 #pragma unroll
             for (int x = 0; x < kBoxes; ++x)
-                tma_load_4d(odst + x * kBox, &tmdO, fb, 64 * x, at.row, at.stripe, bq);
+                tma_load_4d(odst + x * kBox, &tmdO, fb, 64 * x, at.c1, at.c2, bq);
         }
         for (int t = i > QS ? i - QS : 0; t < i; ++t)  // in-flight loads, as above
             mbar_wait(smem_u32(&bars->do_full[t % QS]), (t / QS) & 1, p.wc);
-    } else if (warp == 1 && lane == 0 && nt > 0) {
-        // ---------------- MMA issuer
+    } else if (warp == 1 && nt > 0) {
+        // ---------------- MMA issuer (the whole warp, one lane issues)
         // Per query tile i (TMEM: S = S^T then P^T; DP = dP^T then dQ_i):
         //   dV += P^T dO | S(i+1) | dK += dS^T Q | dQ_i = dS K | dP(i+1)
         // so S(i+1) runs while the compute warps form dS_i and P(i+1), Q_i
         // is released at dK_i, and dP(i+1) follows as soon as dQ_i is out.
+        const bool leader = elect_one();
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint32_t uS = tm, udP = tm + 128, udV = tm + 256, udK = tm + 256 + HD;
         constexpr uint32_t id_kk = idesc_bf16_f32(BT, BT, false, false);
         constexpr uint32_t id_kmn = idesc_bf16_f32(BT, HD, false, true);
         constexpr uint32_t id_mnmn = idesc_bf16_f32(BT, HD, true, true);
         constexpr uint32_t id_dqt = idesc_bf16_f32(HD, BT, true, true);  // dQ^T: M = HD, N = 128 queries
+        // descriptors of the operand tiles read K-major and MN-major; steps
+        // along K and further stages lie whole 16-byte units above
+        const uint64_t k_k = sdesc_sw128(sbase + kKOff, 16, 1024), k_mn = sdesc_sw128(sbase + kKOff, kBox, 1024);
+        const uint64_t v_k = sdesc_sw128(sbase + kVOff, 16, 1024);
+        const uint64_t q_k = sdesc_sw128(sbase + kQOff, 16, 1024), q_mn = sdesc_sw128(sbase + kQOff, kBox, 1024);
+        const uint64_t ds_k = sdesc_sw128(sbase + kDSOff, 16, 1024), ds_mn = sdesc_sw128(sbase + kDSOff, kBox, 1024);
+        constexpr uint32_t kStep = (2 * kTile) >> 4, kdO = kTile >> 4;  // next stage; dO after Q
+        auto along_k = [](int kk) -> uint32_t { return ((kk >> 2) * kBox + (kk & 3) * 32) >> 4; };
         auto issue_s = [&](int t) -> bool {
             const int s = t % QS;
-            if (!mbar_wait(smem_u32(&bars->q_full[s]), (t / QS) & 1, p.wc)) return false;
+            if (!mbar_wait_warp(smem_u32(&bars->q_full[s]), (t / QS) & 1, p.wc)) return false;
             tc_fence_after();
-            const uint32_t qaddr = sbase + kQOff + s * 2 * kTile;
+            if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < HD / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * kBox + (kk & 3) * 32;
-                mma_ss(tS, sdesc_sw128(sbase + kKOff + off, 16, 1024), sdesc_sw128(qaddr + off, 16, 1024),
-                       id_kk, kk > 0 ? 1u : 0u);
+                for (int kk = 0; kk < HD / 16; ++kk)
+                    mma_ss(uS, k_k + along_k(kk), q_k + s * kStep + along_k(kk), id_kk, kk > 0 ? 1u : 0u);
+                mma_commit(smem_u32(&bars->s_full));
             }
-            mma_commit(smem_u32(&bars->s_full));
             return true;
         };
         auto issue_dp = [&](int t) -> bool {
-            if (!mbar_wait(smem_u32(&bars->do_full[t % QS]), (t / QS) & 1, p.wc)) return false;
+            const int s = t % QS;
+            if (!mbar_wait_warp(smem_u32(&bars->do_full[s]), (t / QS) & 1, p.wc)) return false;
             tc_fence_after();
-            const uint32_t oaddr = sbase + kQOff + (t % QS) * 2 * kTile + kTile;
+            if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < HD / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * kBox + (kk & 3) * 32;
-                mma_ss(tdP, sdesc_sw128(sbase + kVOff + off, 16, 1024), sdesc_sw128(oaddr + off, 16, 1024),
-                       id_kk, kk > 0 ? 1u : 0u);
+                for (int kk = 0; kk < HD / 16; ++kk)
+                    mma_ss(udP, v_k + along_k(kk), q_k + s * kStep + kdO + along_k(kk), id_kk, kk > 0 ? 1u : 0u);
+                mma_commit(smem_u32(&bars->dp_full));
             }
-            mma_commit(smem_u32(&bars->dp_full));
             return true;
         };
-        bool ok = mbar_wait(smem_u32(&bars->kv_full), 0, p.wc) && issue_s(0);
+        bool ok = mbar_wait_warp(smem_u32(&bars->kv_full), 0, p.wc) && issue_s(0);
         if (ok) ok = issue_dp(0);
         for (int i = 0; i < nt && ok; ++i) {
             const int s = i % QS;
-            const uint32_t qaddr = sbase + kQOff + s * 2 * kTile;
-            const uint32_t oaddr = qaddr + kTile;
             // dV += P^T dO: P^T (bf16 pairs) in TMEM columns [0,32) for
             // queries 0..63 and [64,96) for queries 64..127
-            if (!mbar_wait(smem_u32(&bars->p_ready), i & 1, p.wc)) break;
+            if (!mbar_wait_warp(smem_u32(&bars->p_ready), i & 1, p.wc)) break;
             tc_fence_after();
+            if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < BT / 16; ++kk)
-                mma_ts(tdV, tS + (kk < 4 ? kk * 8 : 64 + (kk - 4) * 8),
-                       sdesc_sw128(oaddr + kk * 2048, kBox, 1024), id_kmn, (i > 0 || kk > 0) ? 1u : 0u);
-            // HD 128: dO_i (read by dP_i and dV_i only) is free once dV_i completes
-            if (HD == 128 && i + QS < nt) mma_commit(smem_u32(&bars->do_empty[s]));
+                for (int kk = 0; kk < BT / 16; ++kk)
+                    mma_ts(udV, uS + (kk < 4 ? kk * 8 : 64 + (kk - 4) * 8), q_mn + s * kStep + kdO + kk * (2048 >> 4),
+                           id_kmn, (i > 0 || kk > 0) ? 1u : 0u);
+                // HD 128: dO_i (read by dP_i and dV_i only) is free once dV_i completes
+                if (HD == 128 && i + QS < nt) mma_commit(smem_u32(&bars->do_empty[s]));
+            }
             if (i + 1 < nt && !issue_s(i + 1)) break;
             // dK += dS^T Q (A = dS^T, K-major view of the dS smem tile)
-            if (!mbar_wait(smem_u32(&bars->ds_ready), i & 1, p.wc)) break;
+            if (!mbar_wait_warp(smem_u32(&bars->ds_ready), i & 1, p.wc)) break;
             tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < BT / 16; ++kk)
-                mma_ss(tdK, sdesc_sw128(sbase + kDSOff + (kk >> 2) * kBox + (kk & 3) * 32, 16, 1024),
-                       sdesc_sw128(qaddr + kk * 2048, kBox, 1024), id_kmn, (i > 0 || kk > 0) ? 1u : 0u);
-            // Q_i (and its statistics) are free once dK_i completes
-            if (i + QS < nt) mma_commit(smem_u32(&bars->q_empty[s]));
-            if constexpr (HD == 128) {
-                // dQ_i^T = K^T dS^T (A = K, MN-major; B = the dS tile, MN-major)
-                // -> DP columns, head dimension in TMEM lanes, queries in columns
+            if (leader) {
 #pragma unroll
                 for (int kk = 0; kk < BT / 16; ++kk)
-                    mma_ss(tdP, sdesc_sw128(sbase + kKOff + kk * 2048, kBox, 1024),
-                           sdesc_sw128(sbase + kDSOff + kk * 2048, kBox, 1024), id_dqt, kk > 0 ? 1u : 0u);
-            } else {
-                // dQ_i = dS K (A = dS, MN-major view of the same tile) -> DP columns
+                    mma_ss(udK, ds_k + along_k(kk), q_mn + s * kStep + kk * (2048 >> 4), id_kmn,
+                           (i > 0 || kk > 0) ? 1u : 0u);
+                // Q_i (and its statistics) are free once dK_i completes
+                if (i + QS < nt) mma_commit(smem_u32(&bars->q_empty[s]));
+                if constexpr (HD == 128) {
+                    // dQ_i^T = K^T dS^T (A = K, MN-major; B = the dS tile,
+                    // MN-major) -> DP columns, head dimension in TMEM lanes,
+                    // queries in columns
 #pragma unroll
-                for (int kk = 0; kk < BT / 16; ++kk)
-                    mma_ss(tdP, sdesc_sw128(sbase + kDSOff + kk * 2048, kBox, 1024),
-                           sdesc_sw128(sbase + kKOff + kk * 2048, kBox, 1024), id_mnmn, kk > 0 ? 1u : 0u);
+                    for (int kk = 0; kk < BT / 16; ++kk)
+                        mma_ss(udP, k_mn + kk * (2048 >> 4), ds_mn + kk * (2048 >> 4), id_dqt, kk > 0 ? 1u : 0u);
+                } else {
+                    // dQ_i = dS K (A = dS, MN-major view of the same tile) -> DP columns
+#pragma unroll
+                    for (int kk = 0; kk < BT / 16; ++kk)
+                        mma_ss(udP, ds_mn + kk * (2048 >> 4), k_mn + kk * (2048 >> 4), id_mnmn, kk > 0 ? 1u : 0u);
+                }
+                mma_commit(smem_u32(&bars->dq_full));
             }
-            mma_commit(smem_u32(&bars->dq_full));
             if (i + 1 < nt) {
-                if (!mbar_wait(smem_u32(&bars->dq_free), i & 1, p.wc)) break;
+                if (!mbar_wait_warp(smem_u32(&bars->dq_free), i & 1, p.wc)) break;
                 tc_fence_after();
                 if (!issue_dp(i + 1)) break;
             }
         }
-        if (ok) mma_commit(smem_u32(&bars->acc_done));
+        if (ok && leader) mma_commit(smem_u32(&bars->acc_done));
         // every MMA issued above completes before TMEM is freed (error paths)
-        mma_commit(smem_u32(&bars->drain));
-        mbar_wait(smem_u32(&bars->drain), 0, p.wc);
+        if (leader) mma_commit(smem_u32(&bars->drain));
+        mbar_wait_warp(smem_u32(&bars->drain), 0, p.wc);
     } else if (warp >= 4) {
         // ---------------- compute: two warpgroups split the 128 query columns
         // of S^T/dP^T (64 each) and the HD columns of dQ_i, dK, dV (HD/2 each)
@@ -338,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
         const float cl2 = p.scale * 1.4426950408889634f;
         const bool key_valid = tile_has(g, kt, row);
-        const int kpos = kbase + tile_pos(g, row);  // position of this key
+        const int kpos = kbase + row;  // position of this key
         uint8_t *sDS = smem + kDSOff + wg * kBox + row * 128;
         bool ok = nt > 0;
 
@@ -359,15 +365,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             // query when the key is a sink; uniform test: all pairs are kept
             const int qt = a_lo + i % cnt, qbase = qt * g.P;
             const bool full = kt < qt && (qbase + g.P - 1 - kbase < p.W || kbase + g.P <= p.sinks);
-            const int first = full ? -1 : kpos - qbase;
-            const int last = !key_valid ? -2 : (full || kpos < p.sinks) ? 0x7fffffff : kpos - qbase + p.W - 1;
-            const int *qp = col_pos + cbase;
+            const int first = kpos - qbase - cbase;
+            const int last = kpos < p.sinks ? 0x7fffffff : kpos - qbase + p.W - 1 - cbase;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 uint32_t rr[32];
                 tmem_ld32(tS + lane_off + cbase + c * 32, rr);
                 tmem_ld_wait(rr);
                 uint32_t pk[16];
+                const uint32_t kept = !key_valid ? 0u : full ? ~0u : kept_bits(32 * c, last, first, 0);
 #pragma unroll
                 for (int u = 0; u < 16; u += 2) {
                     // four row statistics per 16-byte shared-memory load
@@ -376,13 +382,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float e[4];
 #pragma unroll
                     for (int h = 0; h < 4; ++h) e[h] = ex2(fmaf(__uint_as_float(rr[2 * u + h]), cl2, -lv[h]));
-                    if (!full || !key_valid) {
-                        const int4 q4 = *reinterpret_cast<const int4 *>(qp + c * 32 + 2 * u);
-                        if (q4.x < first || q4.x > last) e[0] = 0.f;
-                        if (q4.y < first || q4.y > last) e[1] = 0.f;
-                        if (q4.z < first || q4.z > last) e[2] = 0.f;
-                        if (q4.w < first || q4.w > last) e[3] = 0.f;
-                    }
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+                        if (!(kept & (1u << (2 * u + h)))) e[h] = 0.f;
                     pk[u] = pack_bf16x2(e[0], e[1]);
                     pk[u + 1] = pack_bf16x2(e[2], e[3]);
                     pkP[c * 16 + u] = pk[u];

@@ -367,6 +367,25 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
         : "memory");
 }
 
+// One lane of a converged warp, the same one every time.  A warp that runs
+// its issue loop as a whole and lets this lane alone issue keeps addresses
+// and descriptors in uniform registers, which tcgen05.mma reads: from a loop
+// of a single lane every operand is first moved there (about 90 clocks a
+// product instead of the tensor core's 64 for 128 x 128 x 16).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+// mbar_wait of a whole warp, with one answer for all lanes.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, const WaitCtl &w) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, w));
+}
+
 // Arrive on an mbarrier once all previously issued tcgen05 ops of this
 // thread have completed.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {

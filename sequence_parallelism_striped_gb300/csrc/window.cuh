@@ -5,12 +5,13 @@
 // order, but N bands (one per stripe) in striped rows: tiles of 128 rows of
 // one stripe would visit N * (W / (128 N) + 2) key tiles instead of
 // W / 128 + 2.  All stripes are in one GPU's memory here, so a tile is
-// formed from positions instead: a TMA box of {64 columns, R rows, N
-// stripes}, R = 128 / N, brings rows d*L + i for R consecutive i and all d,
-// which are the P = N * R consecutive positions i*N + d, in one copy of the
-// same size.  Row r of such a tile holds position (r % R) * N + r / R of the
-// tile.  The zig-zag and contiguous placements hold 128 consecutive
-// positions in 128 consecutive rows.
+// formed from positions instead: the tensor map puts the stripe dimension
+// inside the row dimension, and a box of {64 columns, N stripes, R rows}, R =
+// 128 / N, brings the P = N * R consecutive positions i*N + d of R
+// consecutive i, in order, in one copy of the same size (measured: the same
+// time as from contiguous rows).  The zig-zag and contiguous placements hold
+// 128 consecutive positions in 128 consecutive rows.  Row r of tile t
+// always holds position t * P + r.
 #pragma once
 
 #include <stdint.h>
@@ -54,31 +55,38 @@ static inline bool pos_geom(PosGeom *g, int64_t S, int N, int layout) {
     return true;
 }
 
-// Tensor-map coordinates of position tile t: first row inside a stripe's
-// slice and (first) stripe.  Zig-zag chunks are whole tiles.
+// Tensor-map coordinates of position tile t between the column and the head:
+// {stripe, row} in the striped placement, {row, device} in the zig-zag one,
+// whose chunks are whole tiles.
 struct TileAt {
-    int row, stripe;
+    int c1, c2;
 };
 __host__ __device__ __forceinline__ TileAt tile_at(const PosGeom &g, int t) {
-    if (g.layout == STRIPED_LAYOUT_STRIPED) return TileAt{t * g.R, 0};
+    if (g.layout == STRIPED_LAYOUT_STRIPED) return TileAt{0, t * g.R};
     const int per = g.L / 256;  // tiles of a chunk
     const int c = t / per, in = (t - c * per) * 128;
     return c < g.N ? TileAt{in, c} : TileAt{g.L / 2 + in, 2 * g.N - 1 - c};
 }
 
-// Position (inside the tile) of row r, and the row of the [S] tensors that
-// holds row r of tile t.
-__host__ __device__ __forceinline__ int tile_pos(const PosGeom &g, int r) {
-    return (r % g.R) * g.N * (g.layout == STRIPED_LAYOUT_STRIPED) + (g.layout == STRIPED_LAYOUT_STRIPED ? r / g.R : r);
-}
+// The row of the [S] tensors that holds row r of tile t.
 __host__ __device__ __forceinline__ int64_t tile_row(const PosGeom &g, int t, int r) {
     const TileAt a = tile_at(g, t);
-    if (g.layout == STRIPED_LAYOUT_STRIPED) return (int64_t)(r / g.R) * g.L + a.row + r % g.R;
-    return (int64_t)a.stripe * g.L + a.row + r;
+    if (g.layout == STRIPED_LAYOUT_STRIPED) return (int64_t)(r % g.N) * g.L + a.c2 + r / g.N;
+    return (int64_t)a.c2 * g.L + a.c1 + r;
 }
 // Row r of tile t holds a position of the sequence.
 __host__ __device__ __forceinline__ bool tile_has(const PosGeom &g, int t, int r) {
-    return r < g.P && t * (int64_t)g.P + tile_pos(g, r) < g.S;
+    return r < g.P && t * (int64_t)g.P + r < g.S;
+}
+
+// Bits 0 .. 31 for columns base .. base + 31: column <= hi and (column >= lo
+// or column < sk).
+__host__ __device__ __forceinline__ uint32_t kept_bits(int base, int hi, int lo, int sk) {
+    hi -= base, lo -= base, sk -= base;
+    const uint32_t below = hi >= 31 ? ~0u : hi < 0 ? 0u : (2u << hi) - 1u;
+    const uint32_t above = lo <= 0 ? ~0u : lo > 31 ? 0u : ~0u << lo;
+    const uint32_t sink = sk >= 32 ? ~0u : sk <= 0 ? 0u : (1u << sk) - 1u;
+    return below & (above | sink);
 }
 
 // Lowest key tile inside the window of query tile t, and highest query tile

@@ -53,10 +53,10 @@ def test_position_tiles(harness, layout, S, N, W):
     P = max(len(v) for v in tiles.values())
     for t, v in tiles.items():  # consecutive positions, tile after tile
         assert sorted(x[2] for x in v) == list(range(t * P, min(S, t * P + P)))
-    # the copy box brings row r of the tile to place r: stripes outer, rows inner
+    # the copy box brings row r of the tile to place r: stripes inside rows
     for _, t, row0, stripe0, R, ns, L in [x for x in lines if x[0] == "B"]:
         assert R * ns <= 128 and R <= 256 and ns <= 256
-        got = {s * R + i: (stripe0 + s) * L + row0 + i for s in range(ns) for i in range(R) if row0 + i < L}
+        got = {i * ns + s: (stripe0 + s) * L + row0 + i for s in range(ns) for i in range(R) if row0 + i < L}
         for r, row, _ in tiles.get(t, []):
             assert got[r] == row
     # window spans: exactly the tiles that hold a kept pair
@@ -66,6 +66,15 @@ def test_position_tiles(harness, layout, S, N, W):
         assert lo == first // P
         last_q = min(S - 1, t * P + P - 1 + W - 1)
         assert hi == min(max(tiles), last_q // P if t * P + P <= S else max(tiles)) and min(q) == t * P
+
+
+def test_kept_bits(harness):
+    out = subprocess.run([harness, "1", "128", "1", "1"], capture_output=True, text=True, check=True).stdout
+    rows = [[int(v) for v in x.split()[1:]] for x in out.splitlines() if x[0] == "K"]
+    assert len(rows) > 1000
+    for base, hi, lo, sk, bits in rows:
+        want = sum(1 << c for c in range(32) if base + c <= hi and (base + c >= lo or base + c < sk))
+        assert bits == want
 
 
 def test_more_stripes_than_a_tile(harness):
