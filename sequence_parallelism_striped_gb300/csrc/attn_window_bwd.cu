@@ -50,7 +50,7 @@ constexpr int BT = 128;
 constexpr int QS = 2;  // Q/dO stages
 constexpr uint32_t kBox = 128 * 128;  // 128 rows x 64 bf16 (one 128-byte-swizzle box)
 constexpr uint32_t kStatBytes = 2 * 128 * 4;
-constexpr int kThreads = 384;  // warp 0 and 2 TMA, warp 1 MMA, warps 4..11 compute
+constexpr int kThreads = 512;  // warp 0 and 2 TMA, warp 1 MMA, warps 4..11 compute, 12..15 dQ
 
 template <int HD>
 struct WinBwdCfg {
@@ -75,7 +75,7 @@ struct WinBwdParams {
     int G;          // query heads per key/value head
     float scale;
     const float *stats;  // [BH][nt][LSE*log2e 128 | Delta 128], rows of a tile
-    float *dq_acc;       // [BH][nt][128][D] fp32, rows of a tile
+    float *dq_acc;       // [BH][nt] tiles of fp32: HD = 128 [query / 4][D][4], HD = 64 [D / 4][query][4]
     float *parts;        // [BHkv][nst][slots][dK 128 D | dV 128 D] fp32
     __nv_bfloat16 *dk, *dv;
     WaitCtl wc;  // status word, wait bound, test hook
@@ -84,7 +84,7 @@ struct WinBwdParams {
 struct Bars {
     uint64_t kv_full;
     uint64_t q_full[QS], q_empty[QS];    // Q_i + statistics of tile i
-    uint64_t do_full[QS], do_empty[QS];  // dO_i (HD 64: its buffer also stages half of dQ_i)
+    uint64_t do_full[QS], do_empty[QS];  // dO_i
     uint64_t s_full, dp_full, p_ready, ds_ready, dq_full, dq_free, acc_done;
     uint64_t drain;  // every MMA of the issuer has completed (before TMEM is freed)
     uint32_t tmem_slot;
@@ -99,8 +99,8 @@ __host__ __device__ __forceinline__ int far_units(const PosGeom &g, int kt, int 
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
     tc_window_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
-                  const __grid_constant__ CUtensorMap tmdQ, const WinBwdParams p) {
+                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
+                         const WinBwdParams p) {
     using Cfg = WinBwdCfg<HD>;
     constexpr uint32_t kTile = Cfg::kTile, kKOff = Cfg::kKOff, kVOff = Cfg::kVOff, kQOff = Cfg::kQOff,
                        kDSOff = Cfg::kDSOff, kStatOff = Cfg::kStatOff;
@@ -148,14 +148,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&bars->q_full[s]), 1);
             mbar_init(smem_u32(&bars->q_empty[s]), 1);   // released by dK_i's commit
             mbar_init(smem_u32(&bars->do_full[s]), 1);
-            mbar_init(smem_u32(&bars->do_empty[s]), HD == 128 ? 1 : 4);  // dV_i's commit; HD 64: warpgroup-1 warps
+            mbar_init(smem_u32(&bars->do_empty[s]), 1);  // released by dV_i's commit
         }
         mbar_init(smem_u32(&bars->s_full), 1);
         mbar_init(smem_u32(&bars->dp_full), 1);
         mbar_init(smem_u32(&bars->p_ready), 8);
         mbar_init(smem_u32(&bars->ds_ready), 8);
         mbar_init(smem_u32(&bars->dq_full), 1);
-        mbar_init(smem_u32(&bars->dq_free), 8);
+        mbar_init(smem_u32(&bars->dq_free), 4);
         mbar_init(smem_u32(&bars->acc_done), 1);
         mbar_init(smem_u32(&bars->drain), 1);
         fence_barrier_init();
@@ -177,160 +177,166 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = bars->tmem_slot;
     const uint32_t tS = tmem, tdP = tmem + 128, tdV = tmem + 256, tdK = tmem + 256 + HD;
 
-    if (warp == 0 && lane == 0 && nt > 0) {
-        // ---------------- TMA producer: K, V once, then Q_i + statistics
-        tma_prefetch_desc(&tmQ);
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmV);
-        tma_prefetch_desc(&tmdO);
-        const uint32_t kb = smem_u32(&bars->kv_full);
-        const uint32_t tile_bytes = kBoxes * (uint32_t)g.P * 128;
-        mbar_arrive_expect_tx(kb, 2 * tile_bytes);
+    // 512 threads start with 128 registers each; the compute and dQ
+    // warpgroups take what the first one gives up: 56 + 2 * 152 + 152 = 4 * 128
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 0 && lane == 0 && nt > 0) {
+            // ---------------- TMA producer: K, V once, then Q_i + statistics
+            tma_prefetch_desc(&tmQ);
+            tma_prefetch_desc(&tmK);
+            tma_prefetch_desc(&tmV);
+            tma_prefetch_desc(&tmdO);
+            const uint32_t kb = smem_u32(&bars->kv_full);
+            const uint32_t tile_bytes = kBoxes * (uint32_t)g.P * 128;
+            mbar_arrive_expect_tx(kb, 2 * tile_bytes);
 #pragma unroll
-        for (int x = 0; x < kBoxes; ++x) tma_load_4d(sbase + kKOff + x * kBox, &tmK, kb, 64 * x, kat.c1, kat.c2, (int)bh);
+            for (int x = 0; x < kBoxes; ++x) tma_load_4d(sbase + kKOff + x * kBox, &tmK, kb, 64 * x, kat.c1, kat.c2, (int)bh);
 #pragma unroll
-        for (int x = 0; x < kBoxes; ++x) tma_load_4d(sbase + kVOff + x * kBox, &tmV, kb, 64 * x, kat.c1, kat.c2, (int)bh);
-        // test hook: the first Q tile is never loaded, so every wait on it
-        // runs out (the kernel must then record the timeout and return)
-        const bool skip_first = p.wc.inject == kInjectBwdSkipQ;
-        int i = 0;
-        for (; i < nt; ++i) {
-            const int s = i % QS;
-            if (i >= QS && !mbar_wait(smem_u32(&bars->q_empty[s]), ((i / QS) + 1) & 1, p.wc)) break;
-            if (skip_first && i == 0) continue;
-            const uint32_t fb = smem_u32(&bars->q_full[s]);
-            const uint32_t qdst = sbase + kQOff + s * 2 * kTile;
-            const int64_t bq = bh * G + i / cnt;  // query head
-            const int qt = a_lo + i % cnt;
-            const TileAt at = tile_at(g, qt);
-            mbar_arrive_expect_tx(fb, tile_bytes + kStatBytes);
-            bulk_load(sbase + kStatOff + s * kStatBytes, p.stats + ((bq * g.nt + qt) << 8), kStatBytes, fb);
+            for (int x = 0; x < kBoxes; ++x) tma_load_4d(sbase + kVOff + x * kBox, &tmV, kb, 64 * x, kat.c1, kat.c2, (int)bh);
+            // test hook: the first Q tile is never loaded, so every wait on it
+            // runs out (the kernel must then record the timeout and return)
+            const bool skip_first = p.wc.inject == kInjectBwdSkipQ;
+            int i = 0;
+            for (; i < nt; ++i) {
+                const int s = i % QS;
+                if (i >= QS && !mbar_wait(smem_u32(&bars->q_empty[s]), ((i / QS) + 1) & 1, p.wc)) break;
+                if (skip_first && i == 0) continue;
+                const uint32_t fb = smem_u32(&bars->q_full[s]);
+                const uint32_t qdst = sbase + kQOff + s * 2 * kTile;
+                const int64_t bq = bh * G + i / cnt;  // query head
+                const int qt = a_lo + i % cnt;
+                const TileAt at = tile_at(g, qt);
+                mbar_arrive_expect_tx(fb, tile_bytes + kStatBytes);
+                bulk_load(sbase + kStatOff + s * kStatBytes, p.stats + ((bq * g.nt + qt) << 8), kStatBytes, fb);
 #pragma unroll
-            for (int x = 0; x < kBoxes; ++x)
-                tma_load_4d(qdst + x * kBox, &tmQ, fb, 64 * x, at.c1, at.c2, (int)bq);
-        }
-        // K, V and loads [0, i) were issued: wait (bounded) for the last of
-        // each stage, so that on an error path none lands after the CTA exits
-        mbar_wait(kb, 0, p.wc);
-        for (int t = i > QS ? i - QS : 0; t < i; ++t)
-            if (!(skip_first && t == 0)) mbar_wait(smem_u32(&bars->q_full[t % QS]), (t / QS) & 1, p.wc);
-    } else if (warp == 2 && lane == 0 && nt > 0) {
-        // ---------------- TMA producer: dO_i (its own stream: the buffer is
-        // released at dV_i, or at HD 64 after the dQ_i half staged in it is read)
-        tma_prefetch_desc(&tmdO);
-        int i = 0;
-        for (; i < nt; ++i) {
-            const int s = i % QS;
-            if (i >= QS && !mbar_wait(smem_u32(&bars->do_empty[s]), ((i / QS) + 1) & 1, p.wc)) break;
-            const uint32_t fb = smem_u32(&bars->do_full[s]);
-            const uint32_t odst = sbase + kQOff + s * 2 * kTile + kTile;
-            const int bq = (int)(bh * G) + i / cnt;
-            const TileAt at = tile_at(g, a_lo + i % cnt);
-            mbar_arrive_expect_tx(fb, kBoxes * (uint32_t)g.P * 128);
-#pragma unroll
-            for (int x = 0; x < kBoxes; ++x)
-                tma_load_4d(odst + x * kBox, &tmdO, fb, 64 * x, at.c1, at.c2, bq);
-        }
-        for (int t = i > QS ? i - QS : 0; t < i; ++t)  // in-flight loads, as above
-            mbar_wait(smem_u32(&bars->do_full[t % QS]), (t / QS) & 1, p.wc);
-    } else if (warp == 1 && nt > 0) {
-        // ---------------- MMA issuer (the whole warp, one lane issues)
-        // Per query tile i (TMEM: S = S^T then P^T; DP = dP^T then dQ_i):
-        //   dV += P^T dO | S(i+1) | dK += dS^T Q | dQ_i = dS K | dP(i+1)
-        // so S(i+1) runs while the compute warps form dS_i and P(i+1), Q_i
-        // is released at dK_i, and dP(i+1) follows as soon as dQ_i is out.
-        const bool leader = elect_one();
-        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        const uint32_t uS = tm, udP = tm + 128, udV = tm + 256, udK = tm + 256 + HD;
-        constexpr uint32_t id_kk = idesc_bf16_f32(BT, BT, false, false);
-        constexpr uint32_t id_kmn = idesc_bf16_f32(BT, HD, false, true);
-        constexpr uint32_t id_mnmn = idesc_bf16_f32(BT, HD, true, true);
-        constexpr uint32_t id_dqt = idesc_bf16_f32(HD, BT, true, true);  // dQ^T: M = HD, N = 128 queries
-        // descriptors of the operand tiles read K-major and MN-major; steps
-        // along K and further stages lie whole 16-byte units above
-        const uint64_t k_k = sdesc_sw128(sbase + kKOff, 16, 1024), k_mn = sdesc_sw128(sbase + kKOff, kBox, 1024);
-        const uint64_t v_k = sdesc_sw128(sbase + kVOff, 16, 1024);
-        const uint64_t q_k = sdesc_sw128(sbase + kQOff, 16, 1024), q_mn = sdesc_sw128(sbase + kQOff, kBox, 1024);
-        const uint64_t ds_k = sdesc_sw128(sbase + kDSOff, 16, 1024), ds_mn = sdesc_sw128(sbase + kDSOff, kBox, 1024);
-        constexpr uint32_t kStep = (2 * kTile) >> 4, kdO = kTile >> 4;  // next stage; dO after Q
-        auto along_k = [](int kk) -> uint32_t { return ((kk >> 2) * kBox + (kk & 3) * 32) >> 4; };
-        auto issue_s = [&](int t) -> bool {
-            const int s = t % QS;
-            if (!mbar_wait_warp(smem_u32(&bars->q_full[s]), (t / QS) & 1, p.wc)) return false;
-            tc_fence_after();
-            if (leader) {
-#pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk)
-                    mma_ss(uS, k_k + along_k(kk), q_k + s * kStep + along_k(kk), id_kk, kk > 0 ? 1u : 0u);
-                mma_commit(smem_u32(&bars->s_full));
+                for (int x = 0; x < kBoxes; ++x)
+                    tma_load_4d(qdst + x * kBox, &tmQ, fb, 64 * x, at.c1, at.c2, (int)bq);
             }
-            return true;
-        };
-        auto issue_dp = [&](int t) -> bool {
-            const int s = t % QS;
-            if (!mbar_wait_warp(smem_u32(&bars->do_full[s]), (t / QS) & 1, p.wc)) return false;
-            tc_fence_after();
-            if (leader) {
+            // K, V and loads [0, i) were issued: wait (bounded) for the last of
+            // each stage, so that on an error path none lands after the CTA exits
+            mbar_wait(kb, 0, p.wc);
+            for (int t = i > QS ? i - QS : 0; t < i; ++t)
+                if (!(skip_first && t == 0)) mbar_wait(smem_u32(&bars->q_full[t % QS]), (t / QS) & 1, p.wc);
+        } else if (warp == 2 && lane == 0 && nt > 0) {
+            // ---------------- TMA producer: dO_i (its own stream: the buffer is
+            // released at dV_i, or at HD 64 after the dQ_i half staged in it is read)
+            tma_prefetch_desc(&tmdO);
+            int i = 0;
+            for (; i < nt; ++i) {
+                const int s = i % QS;
+                if (i >= QS && !mbar_wait(smem_u32(&bars->do_empty[s]), ((i / QS) + 1) & 1, p.wc)) break;
+                const uint32_t fb = smem_u32(&bars->do_full[s]);
+                const uint32_t odst = sbase + kQOff + s * 2 * kTile + kTile;
+                const int bq = (int)(bh * G) + i / cnt;
+                const TileAt at = tile_at(g, a_lo + i % cnt);
+                mbar_arrive_expect_tx(fb, kBoxes * (uint32_t)g.P * 128);
 #pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk)
-                    mma_ss(udP, v_k + along_k(kk), q_k + s * kStep + kdO + along_k(kk), id_kk, kk > 0 ? 1u : 0u);
-                mma_commit(smem_u32(&bars->dp_full));
+                for (int x = 0; x < kBoxes; ++x)
+                    tma_load_4d(odst + x * kBox, &tmdO, fb, 64 * x, at.c1, at.c2, bq);
             }
-            return true;
-        };
-        bool ok = mbar_wait_warp(smem_u32(&bars->kv_full), 0, p.wc) && issue_s(0);
-        if (ok) ok = issue_dp(0);
-        for (int i = 0; i < nt && ok; ++i) {
-            const int s = i % QS;
-            // dV += P^T dO: P^T (bf16 pairs) in TMEM columns [0,32) for
-            // queries 0..63 and [64,96) for queries 64..127
-            if (!mbar_wait_warp(smem_u32(&bars->p_ready), i & 1, p.wc)) break;
-            tc_fence_after();
-            if (leader) {
-#pragma unroll
-                for (int kk = 0; kk < BT / 16; ++kk)
-                    mma_ts(udV, uS + (kk < 4 ? kk * 8 : 64 + (kk - 4) * 8), q_mn + s * kStep + kdO + kk * (2048 >> 4),
-                           id_kmn, (i > 0 || kk > 0) ? 1u : 0u);
-                // HD 128: dO_i (read by dP_i and dV_i only) is free once dV_i completes
-                if (HD == 128 && i + QS < nt) mma_commit(smem_u32(&bars->do_empty[s]));
-            }
-            if (i + 1 < nt && !issue_s(i + 1)) break;
-            // dK += dS^T Q (A = dS^T, K-major view of the dS smem tile)
-            if (!mbar_wait_warp(smem_u32(&bars->ds_ready), i & 1, p.wc)) break;
-            tc_fence_after();
-            if (leader) {
-#pragma unroll
-                for (int kk = 0; kk < BT / 16; ++kk)
-                    mma_ss(udK, ds_k + along_k(kk), q_mn + s * kStep + kk * (2048 >> 4), id_kmn,
-                           (i > 0 || kk > 0) ? 1u : 0u);
-                // Q_i (and its statistics) are free once dK_i completes
-                if (i + QS < nt) mma_commit(smem_u32(&bars->q_empty[s]));
-                if constexpr (HD == 128) {
-                    // dQ_i^T = K^T dS^T (A = K, MN-major; B = the dS tile,
-                    // MN-major) -> DP columns, head dimension in TMEM lanes,
-                    // queries in columns
-#pragma unroll
-                    for (int kk = 0; kk < BT / 16; ++kk)
-                        mma_ss(udP, k_mn + kk * (2048 >> 4), ds_mn + kk * (2048 >> 4), id_dqt, kk > 0 ? 1u : 0u);
-                } else {
-                    // dQ_i = dS K (A = dS, MN-major view of the same tile) -> DP columns
-#pragma unroll
-                    for (int kk = 0; kk < BT / 16; ++kk)
-                        mma_ss(udP, ds_mn + kk * (2048 >> 4), k_mn + kk * (2048 >> 4), id_mnmn, kk > 0 ? 1u : 0u);
-                }
-                mma_commit(smem_u32(&bars->dq_full));
-            }
-            if (i + 1 < nt) {
-                if (!mbar_wait_warp(smem_u32(&bars->dq_free), i & 1, p.wc)) break;
+            for (int t = i > QS ? i - QS : 0; t < i; ++t)  // in-flight loads, as above
+                mbar_wait(smem_u32(&bars->do_full[t % QS]), (t / QS) & 1, p.wc);
+        } else if (warp == 1 && nt > 0) {
+            // ---------------- MMA issuer (the whole warp, one lane issues)
+            // Per query tile i (TMEM: S = S^T then P^T; DP = dP^T then dQ_i):
+            //   dV += P^T dO | S(i+1) | dK += dS^T Q | dQ_i = dS K | dP(i+1)
+            // so S(i+1) runs while the compute warps form dS_i and P(i+1), Q_i
+            // is released at dK_i, and dP(i+1) follows as soon as dQ_i is out.
+            const bool leader = elect_one();
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t uS = tm, udP = tm + 128, udV = tm + 256, udK = tm + 256 + HD;
+            constexpr uint32_t id_kk = idesc_bf16_f32(BT, BT, false, false);
+            constexpr uint32_t id_kmn = idesc_bf16_f32(BT, HD, false, true);
+            constexpr uint32_t id_mnmn = idesc_bf16_f32(BT, HD, true, true);
+            constexpr uint32_t id_dqt = idesc_bf16_f32(HD, BT, true, true);  // dQ^T: M = HD, N = 128 queries
+            // descriptors of the operand tiles read K-major and MN-major; steps
+            // along K and further stages lie whole 16-byte units above
+            const uint64_t k_k = sdesc_sw128(sbase + kKOff, 16, 1024), k_mn = sdesc_sw128(sbase + kKOff, kBox, 1024);
+            const uint64_t v_k = sdesc_sw128(sbase + kVOff, 16, 1024);
+            const uint64_t q_k = sdesc_sw128(sbase + kQOff, 16, 1024), q_mn = sdesc_sw128(sbase + kQOff, kBox, 1024);
+            const uint64_t ds_k = sdesc_sw128(sbase + kDSOff, 16, 1024), ds_mn = sdesc_sw128(sbase + kDSOff, kBox, 1024);
+            constexpr uint32_t kStep = (2 * kTile) >> 4, kdO = kTile >> 4;  // next stage; dO after Q
+            auto along_k = [](int kk) -> uint32_t { return ((kk >> 2) * kBox + (kk & 3) * 32) >> 4; };
+            auto issue_s = [&](int t) -> bool {
+                const int s = t % QS;
+                if (!mbar_wait_warp(smem_u32(&bars->q_full[s]), (t / QS) & 1, p.wc)) return false;
                 tc_fence_after();
-                if (!issue_dp(i + 1)) break;
+                if (leader) {
+#pragma unroll
+                    for (int kk = 0; kk < HD / 16; ++kk)
+                        mma_ss(uS, k_k + along_k(kk), q_k + s * kStep + along_k(kk), id_kk, kk > 0 ? 1u : 0u);
+                    mma_commit(smem_u32(&bars->s_full));
+                }
+                return true;
+            };
+            auto issue_dp = [&](int t) -> bool {
+                const int s = t % QS;
+                if (!mbar_wait_warp(smem_u32(&bars->do_full[s]), (t / QS) & 1, p.wc)) return false;
+                tc_fence_after();
+                if (leader) {
+#pragma unroll
+                    for (int kk = 0; kk < HD / 16; ++kk)
+                        mma_ss(udP, v_k + along_k(kk), q_k + s * kStep + kdO + along_k(kk), id_kk, kk > 0 ? 1u : 0u);
+                    mma_commit(smem_u32(&bars->dp_full));
+                }
+                return true;
+            };
+            bool ok = mbar_wait_warp(smem_u32(&bars->kv_full), 0, p.wc) && issue_s(0);
+            if (ok) ok = issue_dp(0);
+            for (int i = 0; i < nt && ok; ++i) {
+                const int s = i % QS;
+                // dV += P^T dO: P^T (bf16 pairs) in TMEM columns [0,32) for
+                // queries 0..63 and [64,96) for queries 64..127
+                if (!mbar_wait_warp(smem_u32(&bars->p_ready), i & 1, p.wc)) break;
+                tc_fence_after();
+                if (leader) {
+#pragma unroll
+                    for (int kk = 0; kk < BT / 16; ++kk)
+                        mma_ts(udV, uS + (kk < 4 ? kk * 8 : 64 + (kk - 4) * 8), q_mn + s * kStep + kdO + kk * (2048 >> 4),
+                               id_kmn, (i > 0 || kk > 0) ? 1u : 0u);
+                    // dO_i (read by dP_i and dV_i only) is free once dV_i completes
+                    if (i + QS < nt) mma_commit(smem_u32(&bars->do_empty[s]));
+                }
+                if (i + 1 < nt && !issue_s(i + 1)) break;
+                // dK += dS^T Q (A = dS^T, K-major view of the dS smem tile)
+                if (!mbar_wait_warp(smem_u32(&bars->ds_ready), i & 1, p.wc)) break;
+                tc_fence_after();
+                if (leader) {
+#pragma unroll
+                    for (int kk = 0; kk < BT / 16; ++kk)
+                        mma_ss(udK, ds_k + along_k(kk), q_mn + s * kStep + kk * (2048 >> 4), id_kmn,
+                               (i > 0 || kk > 0) ? 1u : 0u);
+                    // Q_i (and its statistics) are free once dK_i completes
+                    if (i + QS < nt) mma_commit(smem_u32(&bars->q_empty[s]));
+                    if constexpr (HD == 128) {
+                        // dQ_i^T = K^T dS^T (A = K, MN-major; B = the dS tile,
+                        // MN-major) -> DP columns, head dimension in TMEM lanes,
+                        // queries in columns
+#pragma unroll
+                        for (int kk = 0; kk < BT / 16; ++kk)
+                            mma_ss(udP, k_mn + kk * (2048 >> 4), ds_mn + kk * (2048 >> 4), id_dqt, kk > 0 ? 1u : 0u);
+                    } else {
+                        // dQ_i = dS K (A = dS, MN-major view of the same tile) -> DP columns
+#pragma unroll
+                        for (int kk = 0; kk < BT / 16; ++kk)
+                            mma_ss(udP, ds_mn + kk * (2048 >> 4), k_mn + kk * (2048 >> 4), id_mnmn, kk > 0 ? 1u : 0u);
+                    }
+                    mma_commit(smem_u32(&bars->dq_full));
+                }
+                if (i + 1 < nt) {
+                    if (!mbar_wait_warp(smem_u32(&bars->dq_free), i & 1, p.wc)) break;
+                    tc_fence_after();
+                    if (!issue_dp(i + 1)) break;
+                }
             }
+            if (ok && leader) mma_commit(smem_u32(&bars->acc_done));
+            // every MMA issued above completes before TMEM is freed (error paths)
+            if (leader) mma_commit(smem_u32(&bars->drain));
+            mbar_wait_warp(smem_u32(&bars->drain), 0, p.wc);
         }
-        if (ok && leader) mma_commit(smem_u32(&bars->acc_done));
-        // every MMA issued above completes before TMEM is freed (error paths)
-        if (leader) mma_commit(smem_u32(&bars->drain));
-        mbar_wait_warp(smem_u32(&bars->drain), 0, p.wc);
-    } else if (warp >= 4) {
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
         // ---------------- compute: two warpgroups split the 128 query columns
         // of S^T/dP^T (64 each) and the HD columns of dQ_i, dK, dV (HD/2 each)
         const int wg = (warp - 4) >> 2;       // 0: first half, 1: second half
@@ -367,31 +373,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool full = kt < qt && (qbase + g.P - 1 - kbase < p.W || kbase + g.P <= p.sinks);
             const int first = kpos - qbase - cbase;
             const int last = kpos < p.sinks ? 0x7fffffff : kpos - qbase + p.W - 1 - cbase;
+            uint32_t rr[2][32];
+            tmem_ld32(tS + lane_off + cbase, rr[0]);
+            tmem_ld32(tS + lane_off + cbase + 32, rr[1]);
+            tmem_ld_wait(rr[0]);
+            tmem_ld_wait(rr[1]);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t rr[32];
-                tmem_ld32(tS + lane_off + cbase + c * 32, rr);
-                tmem_ld_wait(rr);
-                uint32_t pk[16];
-                const uint32_t kept = !key_valid ? 0u : full ? ~0u : kept_bits(32 * c, last, first, 0);
+            for (int u = 0; u < 32; u += 2) {
+                // four row statistics per 16-byte shared-memory load
+                const float4 l4 = *reinterpret_cast<const float4 *>(sL + 2 * u);
+                const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
+                float e[4];
 #pragma unroll
-                for (int u = 0; u < 16; u += 2) {
-                    // four row statistics per 16-byte shared-memory load
-                    const float4 l4 = *reinterpret_cast<const float4 *>(sL + c * 32 + 2 * u);
-                    const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
-                    float e[4];
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) e[h] = ex2(fmaf(__uint_as_float(rr[2 * u + h]), cl2, -lv[h]));
-#pragma unroll
-                    for (int h = 0; h < 4; ++h)
-                        if (!(kept & (1u << (2 * u + h)))) e[h] = 0.f;
-                    pk[u] = pack_bf16x2(e[0], e[1]);
-                    pk[u + 1] = pack_bf16x2(e[2], e[3]);
-                    pkP[c * 16 + u] = pk[u];
-                    pkP[c * 16 + u + 1] = pk[u + 1];
-                }
-                tmem_st16(tS + lane_off + pbase + c * 16, pk);
+                for (int h = 0; h < 4; ++h)
+                    e[h] = ex2(fmaf(__uint_as_float(rr[u / 16][2 * u % 32 + h]), cl2, -lv[h]));
+                pkP[u] = pack_bf16x2(e[0], e[1]);
+                pkP[u + 1] = pack_bf16x2(e[2], e[3]);
             }
+            if (!full || !key_valid) {
+                // clear the pairs that are not kept (whatever their exp gave)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const uint32_t kept = key_valid ? kept_bits(32 * c, last, first, 0) : 0u;
+#pragma unroll
+                    for (int u = 0; u < 16; ++u)
+                        pkP[16 * c + u] &= (kept & (1u << (2 * u)) ? 0x0000ffffu : 0u) |
+                                           (kept & (2u << (2 * u)) ? 0xffff0000u : 0u);
+                }
+            }
+            tmem_st32(tS + lane_off + pbase, pkP);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -399,16 +409,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             return true;
         };
 
-        // warpgroup 1, lane 0: stage whose dQ bulk reduce still reads shared
-        // memory (-1: none); the wait for it is deferred to the next tile
-        int pending = -1;
-        auto release_pending = [&]() {
-            if (pending >= 0) {
-                bulk_wait_group_read0();
-                mbar_arrive(smem_u32(&bars->do_empty[pending]));
-                pending = -1;
-            }
-        };
         if (ok) ok = compute_p(0);
         for (int i = 0; i < nt && ok; ++i) {
             // ---- dS = P * (dP - Delta) -> smem (A operand of dQ and dK)
@@ -418,115 +418,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             const float *sD = stat_ptr(i) + 128;
+            uint32_t rr[2][32];
+            tmem_ld32(tdP + lane_off + cbase, rr[0]);
+            tmem_ld32(tdP + lane_off + cbase + 32, rr[1]);
+            tmem_ld_wait(rr[0]);
+            tmem_ld_wait(rr[1]);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t rr[32];
-                tmem_ld32(tdP + lane_off + cbase + c * 32, rr);
-                tmem_ld_wait(rr);
+            for (int v = 0; v < 8; ++v) {
+                uint32_t w[4];
+                // eight Delta values in two 16-byte loads
+                const float4 d0 = *reinterpret_cast<const float4 *>(sD + 8 * v);
+                const float4 d1 = *reinterpret_cast<const float4 *>(sD + 8 * v + 4);
+                const uint64_t dd[4] = {f2(d0.x, d0.y), f2(d0.z, d0.w), f2(d1.x, d1.y), f2(d1.z, d1.w)};
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    uint32_t w[4];
-                    // the chunk's eight Delta values in two 16-byte loads
-                    const float4 d0 = *reinterpret_cast<const float4 *>(sD + c * 32 + 8 * v);
-                    const float4 d1 = *reinterpret_cast<const float4 *>(sD + c * 32 + 8 * v + 4);
-                    const uint64_t dd[4] = {f2(d0.x, d0.y), f2(d0.z, d0.w), f2(d1.x, d1.y), f2(d1.z, d1.w)};
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        const int u = v * 4 + h;  // pair index within the chunk
-                        __nv_bfloat162 pv = *reinterpret_cast<__nv_bfloat162 *>(&pkP[c * 16 + u]);
-                        const float2 pf = __bfloat1622float2(pv);
-                        // dS = P * (dP - Delta), two at a time
-                        const float2 ds = f2_split(mul2(f2(pf.x, pf.y), sub2(f2(__uint_as_float(rr[2 * u]),
-                                                                                  __uint_as_float(rr[2 * u + 1])), dd[h])));
-                        w[h] = pack_bf16x2(ds.x, ds.y);
-                    }
-                    const int chunk = c * 4 + v;
-                    *reinterpret_cast<uint4 *>(sDS + ((chunk ^ (row & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int h = 0; h < 4; ++h) {
+                    const int u = v * 4 + h;  // pair of query columns
+                    const uint32_t *x = &rr[u / 16][2 * u % 32];
+                    __nv_bfloat162 pv = *reinterpret_cast<__nv_bfloat162 *>(&pkP[u]);
+                    const float2 pf = __bfloat1622float2(pv);
+                    // dS = P * (dP - Delta), two at a time
+                    const float2 ds = f2_split(
+                        mul2(f2(pf.x, pf.y), sub2(f2(__uint_as_float(x[0]), __uint_as_float(x[1])), dd[h])));
+                    w[h] = pack_bf16x2(ds.x, ds.y);
                 }
+                *reinterpret_cast<uint4 *>(sDS + ((v ^ (row & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
             fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bars->ds_ready));
-            // the previous tile's dQ reduce has had dS_i's time to read its
-            // staging: return that dO buffer to the producer now
-            if (wg == 1 && lane == 0) release_pending();
             // ---- P of the next tile while the tensor core runs dQ_i / dK_i
-            if (i + 1 < nt && !compute_p(i + 1)) {
-                ok = false;
-                break;
-            }
-            // ---- dQ_i readout -> fp32 accumulator
-            if (!mbar_wait(smem_u32(&bars->dq_full), i & 1, p.wc)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            // dQ_i -> fp32 accumulator (the two forms are described at the
-            // top of this file).
-            const int s = i % QS;
-            // first row of this (query head, query tile) in the accumulator
-            const int64_t qrow = ((bh * G + i / cnt) * g.nt + a_lo + i % cnt) * BT;
-            if constexpr (HD == 128) {
-                // dQ_i^T: lane = head-dimension column, TMEM column = query;
-                // this warp's 32 dimensions of the warpgroup's 64 queries.
-                // One reduction per query covers a whole 128-byte line of the
-                // accumulator across the warp.
-                uint32_t q0[32], q1[32];
-                tmem_ld32(tdP + lane_off + cbase, q0);
-                tmem_ld32(tdP + lane_off + cbase + 32, q1);
-                tmem_ld_wait(q0);
-                tmem_ld_wait(q1);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars->dq_free));
-                float *dst = p.dq_acc + (qrow + cbase) * HD + quarter * 32 + lane;
-#pragma unroll
-                for (int c = 0; c < 32; ++c) red_add_f32(dst + c * HD, __uint_as_float(q0[c]));
-#pragma unroll
-                for (int c = 0; c < 32; ++c) red_add_f32(dst + (32 + c) * HD, __uint_as_float(q1[c]));
-            } else {
-                // HD = 64: split over two paths so neither the TMA engine nor
-                // the load/store unit carries all of it: warpgroup 0 adds its 32
-                // columns with vector reductions; warpgroup 1 stages its 32
-                // columns in the dO_i buffer (dead once dV_i, covered by
-                // dq_full, is done) as one 128-byte-swizzled box and each warp
-                // bulk-reduces its own 32 rows, then returns the buffer.
-                uint32_t q0[32];
-                tmem_ld32(tdP + lane_off + dbase, q0);
-                tmem_ld_wait(q0);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars->dq_free));
-                if (wg == 0) {
-                    float *dst = p.dq_acc + (qrow + row) * HD + dbase;
-#pragma unroll
-                    for (int v = 0; v < 8; ++v)
-                        red_add_v4(dst + 4 * v, __uint_as_float(q0[4 * v]), __uint_as_float(q0[4 * v + 1]),
-                                   __uint_as_float(q0[4 * v + 2]), __uint_as_float(q0[4 * v + 3]));
-                } else {
-                    const uint32_t stage = sbase + kQOff + s * 2 * kTile + kTile;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t addr = stage + row * 128 + ((j ^ (row & 7)) * 16);
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(q0[4 * j]),
-                                     "r"(q0[4 * j + 1]), "r"(q0[4 * j + 2]), "r"(q0[4 * j + 3])
-                                     : "memory");
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        const uint32_t wofs = (uint32_t)quarter * 32 * 128;
-                        const int r0 = (a_lo + i % cnt) * BT + quarter * 32;
-                        tma_reduce_add_4d(&tmdQ, stage + wofs, dbase, r0, 0, (int)(bh * G) + i / cnt);
-                        bulk_commit_group();
-                        pending = s;
-                    }
-                }
-            }
+            if (i + 1 < nt && !compute_p(i + 1)) ok = false;
         }
-        if (wg == 1 && lane == 0) release_pending();
-        if (lane == 0) bulk_wait_group0();
         if (ok) {
             ok = mbar_wait(smem_u32(&bars->acc_done), 0, p.wc);
             tc_fence_after();
@@ -571,6 +494,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
+        }
+    } else {
+        // ---------------- dQ_i out of tensor memory into the fp32 accumulator
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+        const int quarter = warp & 3;
+        const int row = quarter * 32 + lane;  // TMEM lane
+        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        // Accumulator tile in groups of four columns of dQ_i as it lies in
+        // tensor memory: [column / 4][lane][4], so a reduction instruction of
+        // the warp covers 512 whole bytes.  HD = 128: lane = dimension,
+        // column = query; HD = 64: lane = query, column = dimension.
+        constexpr int kCols = HD == 128 ? BT : HD;
+        for (int i = 0; i < nt; ++i) {
+            if (!mbar_wait(smem_u32(&bars->dq_full), i & 1, p.wc)) break;
+            tc_fence_after();
+            uint32_t q[kCols / 32][32];
+#pragma unroll
+            for (int c = 0; c < kCols / 32; ++c) tmem_ld32(tdP + lane_off + 32 * c, q[c]);
+#pragma unroll
+            for (int c = 0; c < kCols / 32; ++c) tmem_ld_wait(q[c]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->dq_free));
+            float *dst = p.dq_acc + ((bh * G + i / cnt) * g.nt + a_lo + i % cnt) * BT * HD + row * 4;
+#pragma unroll
+            for (int c = 0; c < kCols / 32; ++c)
+#pragma unroll
+                for (int u = 0; u < 32; u += 4)
+                    red_add_v4(dst + (8 * c + u / 4) * BT * 4, __uint_as_float(q[c][u]), __uint_as_float(q[c][u + 1]),
+                               __uint_as_float(q[c][u + 2]), __uint_as_float(q[c][u + 3]));
         }
     }
     tc_fence_before();
@@ -623,29 +576,45 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// dQ = bf16(scale * accumulator) from tile order to the placement's rows:
-// HD/8 threads a row, 8 elements each.
+// dQ = bf16(scale * accumulator) from tile order to the placement's rows.
+// HD = 128: a warp takes 4 rows, stored [dimension][4]; lane l has dimensions
+// 4l .. 4l+3 of each.  HD = 64: a thread takes a row, stored [D / 4][row][4].
 template <int HD>
 __global__ void __launch_bounds__(256)
     window_post_kernel(const float *__restrict__ dq_acc, __nv_bfloat16 *__restrict__ dq, const PosGeom g,
                        int64_t padded_rows, float scale) {
-    constexpr int T = HD / 8;
-    const int64_t stride = (int64_t)gridDim.x * blockDim.x / T;
+    constexpr int T = HD == 128 ? 32 : 1, kRows = HD == 128 ? 4 : 1;
+    const int64_t stride = (int64_t)gridDim.x * blockDim.x / T * kRows;
     const int part = threadIdx.x % T;
-    for (int64_t pr = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / T; pr < padded_rows; pr += stride) {
+    for (int64_t pr = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / T * kRows; pr < padded_rows; pr += stride) {
         const int64_t blk = pr >> 7;
         const int r = (int)(pr & 127);
         const int64_t bh = blk / g.nt;
         const int t = (int)(blk - bh * g.nt);
-        if (!tile_has(g, t, r)) continue;
-        const float4 *src = reinterpret_cast<const float4 *>(dq_acc + pr * HD) + 2 * part;
-        const float4 x = src[0], y = src[1];
-        uint4 w;
-        w.x = pack_bf16x2(x.x * scale, x.y * scale);
-        w.y = pack_bf16x2(x.z * scale, x.w * scale);
-        w.z = pack_bf16x2(y.x * scale, y.y * scale);
-        w.w = pack_bf16x2(y.z * scale, y.w * scale);
-        reinterpret_cast<uint4 *>(dq + (bh * g.S + tile_row(g, t, r)) * HD)[part] = w;
+        if (!tile_has(g, t, r)) continue;  // later rows of the four lie behind it too
+        const float4 *src = reinterpret_cast<const float4 *>(dq_acc + blk * BT * HD);
+        if constexpr (HD == 128) {
+            float v[4][4];
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const float4 x = src[r / 4 * HD + 4 * part + d];
+                v[0][d] = x.x, v[1][d] = x.y, v[2][d] = x.z, v[3][d] = x.w;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (tile_has(g, t, r + q))
+                    reinterpret_cast<uint2 *>(dq + (bh * g.S + tile_row(g, t, r + q)) * HD)[part] =
+                        make_uint2(pack_bf16x2(v[q][0] * scale, v[q][1] * scale),
+                                   pack_bf16x2(v[q][2] * scale, v[q][3] * scale));
+        } else {
+            uint4 *dst = reinterpret_cast<uint4 *>(dq + (bh * g.S + tile_row(g, t, r)) * HD);
+#pragma unroll
+            for (int d = 0; d < HD / 4; d += 2) {
+                const float4 x = src[d * BT + r], y = src[(d + 1) * BT + r];
+                dst[d / 2] = make_uint4(pack_bf16x2(x.x * scale, x.y * scale), pack_bf16x2(x.z * scale, x.w * scale),
+                                        pack_bf16x2(y.x * scale, y.y * scale), pack_bf16x2(y.z * scale, y.w * scale));
+            }
+        }
     }
 }
 
@@ -728,18 +697,17 @@ int launch_window_bwd_hd(const void *q, const void *k, const void *v, const void
     p.dk = static_cast<__nv_bfloat16 *>(dk);
     p.dv = static_cast<__nv_bfloat16 *>(dv);
     p.wc = device_wait_ctl();
-    const int64_t bh = a.B * a.H, bh_kv = a.B * a.Hkv, rows = (int64_t)p.g.nt * BT;
-    CUtensorMap mq, mk, mv, mdo, mdq;
+    const int64_t bh = a.B * a.H, bh_kv = a.B * a.Hkv;
+    CUtensorMap mq, mk, mv, mdo;
     int st;
     if ((st = make_pos_map(&mq, q, a.D, p.g, bh)) || (st = make_pos_map(&mk, k, a.D, p.g, bh_kv)) ||
-        (st = make_pos_map(&mv, v, a.D, p.g, bh_kv)) || (st = make_pos_map(&mdo, dO, a.D, p.g, bh)) ||
-        (st = make_f32_map(&mdq, dq_acc, a.D, rows, 1, bh, rows * a.D, rows * a.D, 32)))
+        (st = make_pos_map(&mv, v, a.D, p.g, bh_kv)) || (st = make_pos_map(&mdo, dO, a.D, p.g, bh)))
         return st;
     const int blocks = device_sm_count() * 8;
     window_pre_kernel<HD><<<blocks, 256, 0, stream>>>((const __nv_bfloat16 *)o, (const __nv_bfloat16 *)dO, lse, stats,
                                                       dq_acc, p.g, plan.padded_rows);
     if ((st = cuda_status(cudaGetLastError()))) return st;
-    tc_window_bwd_kernel<HD><<<(unsigned)(p.units * bh_kv), kThreads, kSmemBytes, stream>>>(mq, mk, mv, mdo, mdq, p);
+    tc_window_bwd_kernel<HD><<<(unsigned)(p.units * bh_kv), kThreads, kSmemBytes, stream>>>(mq, mk, mv, mdo, p);
     if ((st = cuda_status(cudaGetLastError()))) return st;
     window_post_kernel<HD><<<blocks, 256, 0, stream>>>(dq_acc, (__nv_bfloat16 *)dq, p.g, plan.padded_rows, a.scale);
     if ((st = cuda_status(cudaGetLastError())) || p.slots == 0) return st;
