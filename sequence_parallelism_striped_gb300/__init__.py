@@ -11,6 +11,7 @@ are CUDA tensors [B, H, S, D], contiguous, bf16 or fp32.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -446,6 +447,9 @@ def striped_attn_bwd_varlen(q, k, v, o, lse, dO, cu_seqlens, N: int, layout: int
 
 
 # ------------------------------------------------------------------ argument checks
+_raw_stream = torch._C._cuda_getCurrentRawStream  # a current_stream() object costs as much as a launch
+
+
 def _rank(t, name: str, n: int):
     """A CUDA tensor of n dimensions (before its shape is read)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -457,53 +461,46 @@ def _rank(t, name: str, n: int):
 def _need(t, name: str, shape, dtype, dev: int) -> int:
     """Address of a tensor argument that has the shape, type, device and
     layout that the call needs."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _buffer(t, name: str, dev: int):
     """Address and bytes of a workspace."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
+    _rank(t, name, 1)
     return _need(t, name, t.shape, t.dtype, dev), t.numel() * t.element_size()
 
 
-class _on:
-    """Make a call on the device of its tensors, whichever is current, and on
-    the given stream or that device's current one.  What is allocated inside
-    belongs to that stream, so it is not handed out again before the call's
-    kernels are done with it."""
-
-    __slots__ = ("dev", "stream", "guard")
+class _elsewhere:
+    """Make a call on the given stream, or on the device of its tensors where
+    another is current.  What is allocated inside belongs to that stream, so
+    it is not handed out again before the call's kernels are done with it."""
 
     def __init__(self, dev: int, stream):
         if stream is not None and stream.device.index != dev:
             raise ValueError(f"stream is on {stream.device}, tensors are on cuda:{dev}")
-        self.dev = dev
-        self.stream = stream
-        self.guard = None
+        self.guard = torch.cuda.device(dev) if stream is None else torch.cuda.stream(stream)
 
-    def __enter__(self) -> int:
-        if self.stream is not None:
-            self.guard = torch.cuda.stream(self.stream)
-        elif torch.cuda.current_device() != self.dev:
-            self.guard = torch.cuda.device(self.dev)
-        if self.guard is not None:
-            self.guard.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+    def __enter__(self):
+        return self.guard.__enter__()
 
     def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+        return self.guard.__exit__(*exc)
+
+
+def _here(dev: int, stream) -> bool:
+    return stream is None and torch.cuda.current_device() == dev
 
 
 # ------------------------------------------------------------------ window attention
@@ -514,17 +511,20 @@ def striped_attn_window_fwd(q, k, v, N: int, window: int, sinks: int = 0, layout
     (o, lse)."""
     _rank(q, "q", 4)
     _rank(k, "k", 4)
-    B, H, S, D = q.shape
-    Hkv, dt, dev = k.shape[1], q.dtype, q.get_device()
+    dev = q.get_device()
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream):
+            return striped_attn_window_fwd(q, k, v, N, window, sinks, layout, scale, out, lse_out)
+    qs = B, H, S, D = q.shape
+    Hkv, dt = k.shape[1], q.dtype
     kv = (B, Hkv, S, D)
-    with _on(dev, stream) as st:
-        o = torch.empty_like(q) if out is None else out
-        lse = torch.empty((B, H, S), dtype=torch.float32, device=q.device) if lse_out is None else lse_out
-        _check(load().striped_attn_window_fwd(
-            _need(q, "q", q.shape, dt, dev), _need(k, "k", kv, dt, dev), _need(v, "v", kv, dt, dev),
-            _need(o, "out", q.shape, dt, dev), _need(lse, "lse_out", (B, H, S), torch.float32, dev), B, H, Hkv, S, D,
-            N, layout, _dtype_code(q), int(window), int(sinks), 1.0 / D ** 0.5 if scale is None else float(scale), st),
-            "striped_attn_window_fwd")
+    o = torch.empty_like(q) if out is None else out
+    lse = torch.empty((B, H, S), dtype=torch.float32, device=q.device) if lse_out is None else lse_out
+    _check(load().striped_attn_window_fwd(
+        _need(q, "q", qs, dt, dev), _need(k, "k", kv, dt, dev), _need(v, "v", kv, dt, dev),
+        _need(o, "out", qs, dt, dev), _need(lse, "lse_out", (B, H, S), torch.float32, dev), B, H, Hkv, S, D, N, layout,
+        _dtype_code(q), window, sinks, 1.0 / D ** 0.5 if scale is None else scale, _raw_stream(dev)),
+        "striped_attn_window_fwd")
     return o, lse
 
 
@@ -542,21 +542,24 @@ def striped_attn_window_bwd(q, k, v, o, lse, dO, N: int, window: int, sinks: int
     """Backward of striped_attn_window_fwd; returns (dq, dk, dv)."""
     _rank(q, "q", 4)
     _rank(k, "k", 4)
-    B, H, S, D = q.shape
-    Hkv, dt, dev = k.shape[1], q.dtype, q.get_device()
-    qs, kv = q.shape, (B, Hkv, S, D)
-    with _on(dev, stream) as st:
-        dq = torch.empty_like(q) if dq is None else dq
-        dk = torch.empty_like(k) if dk is None else dk
-        dv = torch.empty_like(v) if dv is None else dv
-        ws = new_window_workspace(q, k, N, window, sinks, layout) if workspace is None else workspace
-        wp, wn = _buffer(ws, "workspace", dev)
-        _check(load().striped_attn_window_bwd(
-            _need(q, "q", qs, dt, dev), _need(k, "k", kv, dt, dev), _need(v, "v", kv, dt, dev),
-            _need(o, "o", qs, dt, dev), _need(lse, "lse", (B, H, S), torch.float32, dev),
-            _need(dO, "dO", qs, dt, dev), _need(dq, "dq", qs, dt, dev), _need(dk, "dk", kv, dt, dev),
-            _need(dv, "dv", kv, dt, dev), wp, wn, B, H, Hkv, S, D, N, layout, _dtype_code(q), int(window), int(sinks),
-            1.0 / D ** 0.5 if scale is None else float(scale), st), "striped_attn_window_bwd")
+    dev = q.get_device()
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream):
+            return striped_attn_window_bwd(q, k, v, o, lse, dO, N, window, sinks, layout, scale, workspace, dq, dk, dv)
+    qs = B, H, S, D = q.shape
+    Hkv, dt = k.shape[1], q.dtype
+    kv = (B, Hkv, S, D)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    ws = new_window_workspace(q, k, N, window, sinks, layout) if workspace is None else workspace
+    wp, wn = _buffer(ws, "workspace", dev)
+    _check(load().striped_attn_window_bwd(
+        _need(q, "q", qs, dt, dev), _need(k, "k", kv, dt, dev), _need(v, "v", kv, dt, dev), _need(o, "o", qs, dt, dev),
+        _need(lse, "lse", (B, H, S), torch.float32, dev), _need(dO, "dO", qs, dt, dev), _need(dq, "dq", qs, dt, dev),
+        _need(dk, "dk", kv, dt, dev), _need(dv, "dv", kv, dt, dev), wp, wn, B, H, Hkv, S, D, N, layout,
+        _dtype_code(q), window, sinks, 1.0 / D ** 0.5 if scale is None else scale, _raw_stream(dev)),
+        "striped_attn_window_bwd")
     return dq, dk, dv
 
 
@@ -573,12 +576,21 @@ def _decode_sizes(q, k_prompt, k_tail):
     return B, Bp, H, Hkv, T, P, C, D
 
 
+@functools.lru_cache(maxsize=256)
+def _decode_workspace_size(dev: int, *args) -> int:
+    """Depends on the sizes and on the device's multiprocessors only."""
+    return int(load().striped_attn_decode_workspace_size(*args))
+
+
 def new_decode_workspace(q, k_prompt, k_tail, N: int = 1, layout: int = STRIPED, window: int = 0,
                          sinks: int = 0) -> torch.Tensor:
     """Workspace of striped_attn_decode for these tensors and arguments."""
     n = _decode_sizes(q, k_prompt, k_tail)
-    with _on(q.get_device(), None):
-        need = int(load().striped_attn_decode_workspace_size(*n, N, layout, _dtype_code(q), int(window), int(sinks)))
+    dev = q.get_device()
+    if not _here(dev, None):
+        with _elsewhere(dev, None):
+            return new_decode_workspace(q, k_prompt, k_tail, N, layout, window, sinks)
+    need = _decode_workspace_size(dev, *n, N, layout, _dtype_code(q), window, sinks)
     return torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
 
 
@@ -591,26 +603,28 @@ def striped_attn_decode(q, k_prompt, v_prompt, k_tail, v_tail, tail_lens, N: int
     on the device) rows are written.  window 0: full attention.  Returns
     (o [B,H,T,D], lse [B,H,T])."""
     n = B, Bp, H, Hkv, T, P, C, D = _decode_sizes(q, k_prompt, k_tail)
-    dt, dev, code = q.dtype, q.get_device(), _dtype_code(q)
-    window, sinks = int(window), int(sinks)
+    dev = q.get_device()
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream):
+            return striped_attn_decode(q, k_prompt, v_prompt, k_tail, v_tail, tail_lens, N, layout, window, sinks,
+                                       scale, workspace, out, lse_out)
+    dt, code = q.dtype, _dtype_code(q)
     kp = vp = None
     if k_prompt is not None:
         kp = _need(k_prompt, "k_prompt", (Bp, Hkv, P, D), dt, dev)
         vp = _need(v_prompt, "v_prompt", (Bp, Hkv, P, D), dt, dev)
     tail = (B, Hkv, C, D)
-    with _on(dev, stream) as st:
-        o = torch.empty_like(q) if out is None else out
-        lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device) if lse_out is None else lse_out
-        if workspace is None:
-            need = int(load().striped_attn_decode_workspace_size(*n, N, layout, code, window, sinks))
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-        wp, wn = _buffer(workspace, "workspace", dev)
-        _check(load().striped_attn_decode(
-            _need(q, "q", q.shape, dt, dev), kp, vp, _need(k_tail, "k_tail", tail, dt, dev),
-            _need(v_tail, "v_tail", tail, dt, dev), _need(tail_lens, "tail_lens", (B,), torch.int32, dev),
-            _need(o, "out", q.shape, dt, dev), _need(lse, "lse_out", (B, H, T), torch.float32, dev), wp, wn, *n, N,
-            layout, code, window, sinks, 1.0 / D ** 0.5 if scale is None else float(scale), st),
-            "striped_attn_decode")
+    o = torch.empty_like(q) if out is None else out
+    lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device) if lse_out is None else lse_out
+    if workspace is None:
+        workspace = new_decode_workspace(q, k_prompt, k_tail, N, layout, window, sinks)
+    wp, wn = _buffer(workspace, "workspace", dev)
+    _check(load().striped_attn_decode(
+        _need(q, "q", q.shape, dt, dev), kp, vp, _need(k_tail, "k_tail", tail, dt, dev),
+        _need(v_tail, "v_tail", tail, dt, dev), _need(tail_lens, "tail_lens", (B,), torch.int32, dev),
+        _need(o, "out", q.shape, dt, dev), _need(lse, "lse_out", (B, H, T), torch.float32, dev), wp, wn, *n, N,
+        layout, code, window, sinks, 1.0 / D ** 0.5 if scale is None else scale, _raw_stream(dev)),
+        "striped_attn_decode")
     return o, lse
 
 
@@ -633,19 +647,23 @@ def striped_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, N: int = 1, layout:
     _rank(q, "q", 4)
     _rank(k, "k", 4)
     _rank(inv_freq, "inv_freq", 1)
-    B, H, S, D = q.shape
-    Hkv, dt, dev = k.shape[1], q.dtype, q.get_device()
-    qs, ks, half, f32 = q.shape, (B, Hkv, S, D), inv_freq.shape[0], torch.float32
-    with _on(dev, stream) as st:
-        yq = torch.empty_like(q) if q_out is None else q_out
-        yk = torch.empty_like(k) if k_out is None else k_out
-        _check(load().striped_qk_norm_rope(
-            _need(q, "q", qs, dt, dev), _need(k, "k", ks, dt, dev), _need(yq, "q_out", qs, dt, dev),
-            _need(yk, "k_out", ks, dt, dev), _need(q_weight, "q_weight", (D,), f32, dev),
-            _need(k_weight, "k_weight", (D,), f32, dev), _need(inv_freq, "inv_freq", (half,), torch.float64, dev),
-            None if positions is None else _need(positions, "positions", (B, S), torch.int64, dev), B, H, Hkv, S, D,
-            2 * half, 1 if interleaved else 0, N, layout, -1 if stripe is None else int(stripe), float(eps),
-            _dtype_code(q), st), "striped_qk_norm_rope")
+    dev = q.get_device()
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream):
+            return striped_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, N, layout, stripe, positions, eps,
+                                        interleaved, q_out, k_out)
+    qs = B, H, S, D = q.shape
+    Hkv, dt = k.shape[1], q.dtype
+    ks, half, f32 = (B, Hkv, S, D), inv_freq.shape[0], torch.float32
+    yq = torch.empty_like(q) if q_out is None else q_out
+    yk = torch.empty_like(k) if k_out is None else k_out
+    _check(load().striped_qk_norm_rope(
+        _need(q, "q", qs, dt, dev), _need(k, "k", ks, dt, dev), _need(yq, "q_out", qs, dt, dev),
+        _need(yk, "k_out", ks, dt, dev), _need(q_weight, "q_weight", (D,), f32, dev),
+        _need(k_weight, "k_weight", (D,), f32, dev), _need(inv_freq, "inv_freq", (half,), torch.float64, dev),
+        None if positions is None else _need(positions, "positions", (B, S), torch.int64, dev), B, H, Hkv, S, D,
+        2 * half, 1 if interleaved else 0, N, layout, -1 if stripe is None else stripe, eps, _dtype_code(q),
+        _raw_stream(dev)), "striped_qk_norm_rope")
     return yq, yk
 
 
@@ -666,25 +684,29 @@ def striped_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, inv_freq,
     _rank(q, "q", 4)
     _rank(k, "k", 4)
     _rank(inv_freq, "inv_freq", 1)
-    B, H, S, D = q.shape
-    Hkv, dt, dev = k.shape[1], q.dtype, q.get_device()
-    qs, ks, half, f32 = q.shape, (B, Hkv, S, D), inv_freq.shape[0], torch.float32
-    with _on(dev, stream) as st:
-        dq = torch.empty_like(q) if dq is None else dq
-        dk = torch.empty_like(k) if dk is None else dk
-        dqw = torch.empty_like(q_weight) if dq_weight is None else dq_weight
-        dkw = torch.empty_like(k_weight) if dk_weight is None else dk_weight
-        ws = qk_norm_rope_workspace(q, k) if workspace is None else workspace
-        wp, wn = _buffer(ws, "workspace", dev)
-        _check(load().striped_qk_norm_rope_bwd(
-            _need(q, "q", qs, dt, dev), _need(k, "k", ks, dt, dev), _need(dq_out, "dq_out", qs, dt, dev),
-            _need(dk_out, "dk_out", ks, dt, dev), _need(dq, "dq", qs, dt, dev), _need(dk, "dk", ks, dt, dev),
-            _need(dqw, "dq_weight", (D,), f32, dev), _need(dkw, "dk_weight", (D,), f32, dev),
-            _need(q_weight, "q_weight", (D,), f32, dev), _need(k_weight, "k_weight", (D,), f32, dev),
-            _need(inv_freq, "inv_freq", (half,), torch.float64, dev),
-            None if positions is None else _need(positions, "positions", (B, S), torch.int64, dev), wp, wn, B, H,
-            Hkv, S, D, 2 * half, 1 if interleaved else 0, N, layout, -1 if stripe is None else int(stripe),
-            float(eps), _dtype_code(q), st), "striped_qk_norm_rope_bwd")
+    dev = q.get_device()
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream):
+            return striped_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, inv_freq, N, layout, stripe,
+                                            positions, eps, interleaved, workspace, dq, dk, dq_weight, dk_weight)
+    qs = B, H, S, D = q.shape
+    Hkv, dt = k.shape[1], q.dtype
+    ks, half, f32 = (B, Hkv, S, D), inv_freq.shape[0], torch.float32
+    qw, kw = _need(q_weight, "q_weight", (D,), f32, dev), _need(k_weight, "k_weight", (D,), f32, dev)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dqw = torch.empty_like(q_weight) if dq_weight is None else dq_weight
+    dkw = torch.empty_like(k_weight) if dk_weight is None else dk_weight
+    ws = qk_norm_rope_workspace(q, k) if workspace is None else workspace
+    wp, wn = _buffer(ws, "workspace", dev)
+    _check(load().striped_qk_norm_rope_bwd(
+        _need(q, "q", qs, dt, dev), _need(k, "k", ks, dt, dev), _need(dq_out, "dq_out", qs, dt, dev),
+        _need(dk_out, "dk_out", ks, dt, dev), _need(dq, "dq", qs, dt, dev), _need(dk, "dk", ks, dt, dev),
+        _need(dqw, "dq_weight", (D,), f32, dev), _need(dkw, "dk_weight", (D,), f32, dev), qw, kw,
+        _need(inv_freq, "inv_freq", (half,), torch.float64, dev),
+        None if positions is None else _need(positions, "positions", (B, S), torch.int64, dev), wp, wn, B, H, Hkv, S,
+        D, 2 * half, 1 if interleaved else 0, N, layout, -1 if stripe is None else stripe, eps, _dtype_code(q),
+        _raw_stream(dev)), "striped_qk_norm_rope_bwd")
     return dq, dk, dqw, dkw
 
 
