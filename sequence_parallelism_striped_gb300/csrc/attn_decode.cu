@@ -16,10 +16,12 @@
 //    prompt is read once for them (more than 128 rows: once per 128, from L2
 //    while it is there);
 //  * one CTA per multiprocessor, and all (item, key tile) pairs of the call
-//    are cut into equal contiguous shares, one per CTA, whatever the lengths
-//    (an item is a row tile of one key/value head: of a prompt or of a
-//    tail).  A CTA's loads run ahead of the arithmetic across item
-//    boundaries, so they never pause for a prologue or an epilogue;
+//    are cut into contiguous shares of equal cost, one per CTA, whatever the
+//    lengths (an item is a row tile of one key/value head: of a prompt or of
+//    a tail; beginning one costs as much as a few tiles, so that a CTA with
+//    many short tails gets fewer tiles).  A CTA's loads run ahead of the
+//    arithmetic across item boundaries, so they never pause for a prologue or
+//    an epilogue;
 //  * each stretch of an item in a CTA (a segment) leaves unnormalised fp32
 //    partial results, and a second kernel joins the segments of every row
 //    in a fixed order.
@@ -82,7 +84,8 @@ struct DecParams {
     const int32_t *lens;
     __nv_bfloat16 *o;
     float *lse;
-    int32_t *cum;         // [entries + 1] key tiles before each entry (over one key/value head), then the spans' copy
+    int over;             // what beginning an item costs, in key tiles
+    int32_t *cum;         // [entries + 1] cost of the entries before each one (over one key/value head)
     float *part_o[2], *part_ml[2];  // prompt and tail slots: [slot][rows][D], [slot][rows][m, l]
     int slot_rows[2];
     WaitCtl wc;
@@ -130,27 +133,32 @@ __device__ Span entry_span(const DecParams &p, int e) {
 // Share of CTA c of `parts`: tiles [share(c), share(c + 1)).
 __device__ __forceinline__ int share(int64_t total, int c, int parts) { return (int)(total * c / parts); }
 
-// One stretch of an item inside a CTA's share.
+// One stretch of an item inside a CTA's share [x, x1) of the costs; every item
+// costs `over` and then one per key tile.
 struct Segment {
-    int e, hkv, t0, t1, nt;  // entry, key/value head, tiles t0 .. t1-1 of the entry's nt
+    int e, hkv, t0, t1, nt;  // entry, key/value head, tiles t0 .. t1-1 of the entry's nt (none if t1 <= t0)
+    int next;                // where the next segment begins
     Span s;
 };
 
 __device__ __forceinline__ Segment segment_at(const int *cum, const int *lo, const int *ns, int entries, int hkv_n,
-                                              int x, int x1) {
+                                              int over, int x, int x1) {
     int a = 0, b = entries - 1;  // last entry that begins at or below x (entries without tiles are passed over)
     while (a < b) {
         const int m = (a + b + 1) >> 1;
-        if ((int64_t)cum[m] * hkv_n <= x) a = m;
+        if (cum[m] * hkv_n <= x) a = m;
         else b = m - 1;
     }
     Segment s;
     s.e = a;
-    s.nt = cum[a + 1] - cum[a];
+    const int cost = cum[a + 1] - cum[a];
     const int in = x - cum[a] * hkv_n;
-    s.hkv = in / s.nt;
-    s.t0 = in - s.hkv * s.nt;
-    s.t1 = min(s.nt, s.t0 + x1 - x);
+    s.hkv = in / cost;
+    s.nt = cost - over;
+    const int off = in - s.hkv * cost;
+    s.t0 = max(0, off - over);
+    s.t1 = min(s.nt, off + (x1 - x) - over);
+    s.next = min(x1, x + cost - off);
     s.s = Span{ns[a], lo[a], s.nt};
     return s;
 }
@@ -207,7 +215,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
             const Span s = entry_span(p, e);
             lo_of[e] = s.lo;
             ns_of[e] = s.ns;
-            cum[e + 1] = sum += s.n;
+            cum[e + 1] = sum += s.n > 0 ? s.n + p.over : 0;
         }
         int run = sum;
 #pragma unroll
@@ -236,12 +244,18 @@ __global__ void __launch_bounds__(kDThreads, 1)
     const uint32_t tmem = bars->tmem_slot;
     const uint32_t tS0 = tmem, tS1 = tmem + 128, tO = tmem + 256, tQ = tmem + 256 + HD;
     const int64_t total = (int64_t)cum[p.entries] * p.Hkv;
-    // no more shares than tiles: every CTA below `parts` has at least one, so
-    // the segments of an item are those of consecutive CTAs
+    // no more shares than costs: the segments of an item are those of
+    // consecutive CTAs
     const int parts = (int)min((int64_t)gridDim.x, total), cta = blockIdx.x;
     const int x0 = cta < parts ? share(total, cta, parts) : 0;
     const int x1 = cta < parts ? share(total, cta + 1, parts) : 0;
-    const int nx = x1 - x0;  // key tiles of this CTA
+    auto segment = [&](int x) { return segment_at(cum, lo_of, ns_of, p.entries, p.Hkv, p.over, x, x1); };
+    int nx = 0;  // key tiles of this CTA
+    for (int x = x0; x < x1;) {
+        const Segment sg = segment(x);
+        nx += max(0, sg.t1 - sg.t0);
+        x = sg.next;
+    }
 
     if (warp == 0 && lane == 0 && nx > 0) {
         // ---------------- TMA producer
@@ -250,8 +264,9 @@ __global__ void __launch_bounds__(kDThreads, 1)
         const bool skip_first = p.wc.inject == kInjectFwdSkipKV;
         int j = 0;
         bool ok = true;
-        while (j < nx && ok) {
-            const Segment sg = segment_at(cum, lo_of, ns_of, p.entries, p.Hkv, x0 + j, x1);
+        for (int x = x0; x < x1 && ok;) {
+            const Segment sg = segment(x);
+            x = sg.next;
             const bool tail = sg.e >= p.ep;
             const int head = (tail ? (sg.e - p.ep) / p.nrt_t : sg.e / p.nrt_p) * p.Hkv + sg.hkv;
             const CUtensorMap *mk = tail ? &tmKt : &tmKp, *mv = tail ? &tmVt : &tmVp;
@@ -303,11 +318,13 @@ __global__ void __launch_bounds__(kDThreads, 1)
         };
         bool ok = true;
         int j = 0;
-        for (int seg = 0; j < nx && ok; ++seg) {
-            const Segment sg = segment_at(cum, lo_of, ns_of, p.entries, p.Hkv, x0 + j, x1);
+        for (int x = x0, seg = 0; x < x1 && ok;) {
+            const Segment sg = segment(x);
+            x = sg.next;
+            if (sg.t1 <= sg.t0) continue;
             const int j1 = j + sg.t1 - sg.t0;
             const int first = j;
-            ok = mbar_wait_warp(smem_u32(&bars->q_full), seg & 1, p.wc);
+            ok = mbar_wait_warp(smem_u32(&bars->q_full), seg++ & 1, p.wc);
             tc_fence_after();
             if (ok) ok = issue_s(j);
             if (ok && j + 1 < j1) ok = issue_s(j + 1);
@@ -341,8 +358,10 @@ __global__ void __launch_bounds__(kDThreads, 1)
         const int per = p.G * p.T;
         int j = 0;
         bool ok = true;
-        while (j < nx && ok) {
-            const Segment sg = segment_at(cum, lo_of, ns_of, p.entries, p.Hkv, x0 + j, x1);
+        for (int x = x0; x < x1 && ok;) {
+            const Segment sg = segment(x);
+            x = sg.next;
+            if (sg.t1 <= sg.t0) continue;
             const bool tail = sg.e >= p.ep;
             // this thread's query row: request b, head h, token t
             int grp, rt, rows;
@@ -550,75 +569,105 @@ __global__ void __launch_bounds__(kDThreads, 1)
 }
 
 // o and lse of every row from its segments: those of its prompt's row tile,
-// then those of its tail's, in order.  One warp per row.
+// then those of its tail's.  One block per row; warp w takes every fourth
+// segment from the w-th on, eight loads in flight, and the four are added in
+// order.
 template <int HD>
-__global__ void __launch_bounds__(128, 8) decode_join_kernel(const DecParams p, int grid) {
+__global__ void __launch_bounds__(128) decode_join_kernel(const DecParams p, int grid) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int E = HD / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);  // (b, h, t)
-    if (row >= (int64_t)p.B * p.H * p.T) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = blockIdx.x;  // (b, h, t)
     const int t = (int)(row % p.T);
     const int64_t bh = row / p.T;
     const int b = (int)(bh / p.H), h = (int)(bh % p.H), hkv = h / p.G;
     const int64_t total = (int64_t)p.cum[p.entries] * p.Hkv, parts = min((int64_t)grid, total);
-    float m = -INFINITY, l = 0.f, acc[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] = 0.f;
+    // first slot and count of the row's segments: prompt, tail
+    int64_t at[2];
+    int n[2];
 #pragma unroll
     for (int tail = 0; tail < 2; ++tail) {
-        if (!tail && p.ep == 0) continue;
         const int in = (h % p.G) * p.T + t;
         const int r = tail ? in : (b % p.R) * p.G * p.T + in;
         const int e = (tail ? p.ep + b * p.nrt_t : b / p.R * p.nrt_p) + r / DT;
-        const int n = p.cum[e + 1] - p.cum[e];
-        if (n == 0) continue;
-        const int64_t first = (int64_t)p.cum[e] * p.Hkv + (int64_t)hkv * n;
-        const int c0 = (int)(((first + 1) * parts - 1) / total), c1 = (int)(((first + n) * parts - 1) / total);
-        const int item = (tail ? e - p.ep : e) * p.Hkv + hkv;
-        for (int c = c0; c <= c1; c += 32) {
-            // 32 segments at a time: their statistics one per lane
-            const int k = min(32, c1 - c + 1);
-            const int64_t at = (int64_t)(item + c + lane) * p.slot_rows[tail] + r % DT;
-            float2 ml = make_float2(-INFINITY, 0.f);
-            if (lane < k) ml = *reinterpret_cast<const float2 *>(p.part_ml[tail] + 2 * at);
-            float top = ml.x;
+        n[tail] = 0;
+        at[tail] = 0;
+        if (!tail && p.ep == 0) continue;
+        const int cost = p.cum[e + 1] - p.cum[e];
+        if (cost == 0) continue;
+        const int64_t first = (int64_t)p.cum[e] * p.Hkv + (int64_t)hkv * cost + p.over;  // its tile 0
+        const int64_t last = first + cost - p.over - 1;
+        const int c0 = (int)(((first + 1) * parts - 1) / total), c1 = (int)(((last + 1) * parts - 1) / total);
+        n[tail] = c1 - c0 + 1;
+        at[tail] = (int64_t)((tail ? e - p.ep : e) * p.Hkv + hkv + c0) * p.slot_rows[tail] + r % DT;
+    }
+    float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
-            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float m_new = fmaxf(m, top);
-            if (m_new == -INFINITY) continue;
-            const float old = ex2(m - m_new), w = ex2(ml.x - m_new);
-            float lw = ml.y * w;
+    for (int i = 0; i < E; ++i) acc[i] = 0.f;
+    const int all = n[0] + n[1];
+    constexpr int U = 8;
+    for (int s0 = warp; s0 < all; s0 += 4 * U) {
+        float2 ml[U];
+        float v[U][E];
 #pragma unroll
-            for (int o = 16; o; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
-            l = l * old + lw;
-            m = m_new;
-#pragma unroll
-            for (int i = 0; i < E; ++i) acc[i] *= old;
-            const float *src = p.part_o[tail] + ((int64_t)(item + c) * p.slot_rows[tail] + r % DT) * HD + lane * E;
-            const int64_t step = (int64_t)p.slot_rows[tail] * HD;
-#pragma unroll 4
-            for (int i = 0; i < k; ++i) {
-                const float wi = __shfl_sync(0xffffffffu, w, i);
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + 4 * u, tail = s >= n[0];
+            ml[u] = make_float2(-INFINITY, 0.f);
+            if (s < all) {
+                const int64_t slot = at[tail] + (int64_t)(s - (tail ? n[0] : 0)) * p.slot_rows[tail];
+                ml[u] = *reinterpret_cast<const float2 *>(p.part_ml[tail] + 2 * slot);
+                const float *src = p.part_o[tail] + slot * HD + lane * E;
                 if constexpr (E == 4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(src + i * step);
-                    acc[0] = fmaf(v.x, wi, acc[0]), acc[1] = fmaf(v.y, wi, acc[1]);
-                    acc[2] = fmaf(v.z, wi, acc[2]), acc[3] = fmaf(v.w, wi, acc[3]);
+                    const float4 x = *reinterpret_cast<const float4 *>(src);
+                    v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][3] = x.w;
                 } else {
-                    const float2 v = *reinterpret_cast<const float2 *>(src + i * step);
-                    acc[0] = fmaf(v.x, wi, acc[0]), acc[1] = fmaf(v.y, wi, acc[1]);
+                    const float2 x = *reinterpret_cast<const float2 *>(src);
+                    v[u][0] = x.x, v[u][1] = x.y;
                 }
             }
         }
+        float m_new = m;
+#pragma unroll
+        for (int u = 0; u < U; ++u) m_new = fmaxf(m_new, ml[u].x);
+        if (m_new == -INFINITY) continue;
+        const float old = ex2(m - m_new);
+        l *= old;
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] *= old;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (ml[u].x == -INFINITY) continue;  // no key kept, or no segment
+            const float w = ex2(ml[u].x - m_new);
+            l = fmaf(ml[u].y, w, l);
+#pragma unroll
+            for (int i = 0; i < E; ++i) acc[i] = fmaf(v[u][i], w, acc[i]);
+        }
+        m = m_new;
+    }
+    __shared__ float sm[4], sl[4], sa[4][HD];
+    if (lane == 0) sm[warp] = m, sl[warp] = l;
+#pragma unroll
+    for (int i = 0; i < E; ++i) sa[warp][lane * E + i] = acc[i];
+    __syncthreads();
+    m = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+    float w[4];
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = sm[i] == -INFINITY ? 0.f : ex2(sm[i] - m);
+        l = fmaf(sl[i], w[i], l);
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    if (lane == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-    __nv_bfloat16 *dst = p.o + row * HD + lane * E;
-    if constexpr (E == 4)
-        *reinterpret_cast<uint2 *>(dst) =
-            make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-    else
-        *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    if (threadIdx.x == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    if (threadIdx.x < HD / 2) {
+        float o2[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int d = 2 * threadIdx.x + k;
+            o2[k] = ((sa[0][d] * w[0] + sa[1][d] * w[1]) + (sa[2][d] * w[2] + sa[3][d] * w[3])) * inv;
+        }
+        reinterpret_cast<uint32_t *>(p.o + row * HD)[threadIdx.x] = pack_bf16x2(o2[0], o2[1]);
+    }
 }
 
 struct DecPlan {
@@ -646,7 +695,11 @@ bool decode_plan(DecPlan *plan, const DecodeArgs &a) {
     const int64_t nrt_p = (rows_p + DT - 1) / DT, nrt_t = (per + DT - 1) / DT;
     const int64_t ep = a.P > 0 ? a.Bp * nrt_p : 0, entries = ep + a.B * nrt_t;
     if (entries > kMaxEntries) return false;
-    const int64_t tiles = (ep * (a.P > 0 ? p.g.nt : 0) + a.B * nrt_t * ((a.C + DT - 1) / DT)) * a.Hkv;
+    // a segment of one tile takes about 2.8 us, a further tile 1.35 us at
+    // D = 128 and half of that at D = 64
+    p.over = a.D == 128 ? 1 : 3;
+    const int64_t tiles =
+        (ep * (a.P > 0 ? p.g.nt + p.over : 0) + a.B * nrt_t * ((a.C + DT - 1) / DT + p.over)) * a.Hkv;
     if (tiles > (1ll << 30)) return false;
     p.rows_p = (int)rows_p;
     p.rows_t = (int)per;
@@ -710,7 +763,7 @@ int launch_decode_hd(const void *q, const void *kp, const void *vp, const void *
     tc_decode_kernel<HD><<<plan.parts, kDThreads, DecCfg<HD>::kSmemBytes, stream>>>(mkp, mvp, mkt, mvt, p);
     if ((st = cuda_status(cudaGetLastError()))) return st;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((a.B * a.H * a.T + 3) / 4));
+    cfg.gridDim = dim3((unsigned)(a.B * a.H * a.T));
     cfg.blockDim = dim3(128);
     cfg.stream = stream;
     cudaLaunchAttribute at{};
