@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
                 const int kt = tt < sg.s.ns ? tt : sg.s.lo + tt - sg.s.ns;
                 const int kbase = kt * tile_w;
                 // a tail tile with rows that were never written: clear V there
-                const int written = tail ? len_of(p, grp) - kbase : DT;
+                const int written = tail ? len - kbase : DT;
                 if (written < DT) {
                     const int s = j % NS;
                     if (!mbar_wait(smem_u32(&bars->kv_full[s]), (j / NS) & 1, p.wc)) {
@@ -697,7 +697,7 @@ bool decode_plan(DecPlan *plan, const DecodeArgs &a) {
     if (entries > kMaxEntries) return false;
     // a segment of one tile takes about 2.8 us, a further tile 1.35 us at
     // D = 128 and half of that at D = 64
-    p.over = a.D == 128 ? 1 : 3;
+    p.over = a.D == 128 ? 2 : 4;
     const int64_t tiles =
         (ep * (a.P > 0 ? p.g.nt + p.over : 0) + a.B * nrt_t * ((a.C + DT - 1) / DT + p.over)) * a.Hkv;
     if (tiles > (1ll << 30)) return false;

@@ -86,6 +86,24 @@ def test_decode(layout, B, Bp, H, Hkv, T, P, C, D, N, W, ns, lens):
         within(go, o, tol, "o")
 
 
+@pytest.mark.parametrize("D,B,H", [(128, 2, 8), (64, 20, 32)])
+def test_long_segments_with_a_growing_maximum(D, B, H):
+    """Many tiles per multiprocessor, and scores that keep growing with the
+    position, so that the running maximum moves again and again; all four
+    warps of the row tile at work, or one of them."""
+    Hkv, P, C, N = 4, 40000, 200, 8
+    q, kp, vp, kt, vt, lens = _make(B, 1, H, Hkv, 1, P, C, D, None, 7)
+    pos = positions(P, N, sp.STRIPED)
+    grow = (0.2 + 6.0 * pos.double() / P)[None, None, :, None]
+    kp = (kp.double().abs() * q[:1, :Hkv].double().sign() * grow).to(torch.bfloat16)
+    o, lse, tol = _reference(q, kp, vp, kt, vt, lens, pos, 0, 0, D ** -0.5)
+    go, gl = sp.striped_attn_decode(*_gpu(q, kp, vp, kt, vt, lens), N)
+    assert sp.check_error() == 0
+    within(gl, lse, 4 * LSE_TOL, "lse")  # scores up to a few hundred
+    # a score s is off by up to 2^-20 |s| in fp32 sums: its weight by that
+    within(go, o, tol + 2.0 ** -11 * vp.double().abs().max(), "o")
+
+
 def test_lengths_outside_the_tail_are_clamped():
     q, kp, vp, kt, vt, _ = _make(2, 1, 2, 1, 1, 64, 20, 64, [0, 0], 1)
     a = sp.striped_attn_decode(*_gpu(q, kp, vp, kt, vt, torch.tensor([-5, 1 << 30], dtype=torch.int32)), 4)
