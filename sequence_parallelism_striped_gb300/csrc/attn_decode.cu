@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
     __syncthreads();
     tc_fence_after();
     // the joining kernel may be set up now (it waits for this grid's results)
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    let_next_begin();
     const uint32_t tmem = bars->tmem_slot;
     const uint32_t tS0 = tmem, tS1 = tmem + 128, tO = tmem + 256, tQ = tmem + 256 + HD;
     const int64_t total = (int64_t)cum[p.entries] * p.Hkv;
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
 // order.
 template <int HD>
 __global__ void __launch_bounds__(128) decode_join_kernel(const DecParams p, int grid) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_previous();
     constexpr int E = HD / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = blockIdx.x;  // (b, h, t)
@@ -762,16 +762,7 @@ int launch_decode_hd(const void *q, const void *kp, const void *vp, const void *
     }
     tc_decode_kernel<HD><<<plan.parts, kDThreads, DecCfg<HD>::kSmemBytes, stream>>>(mkp, mvp, mkt, mvt, p);
     if ((st = cuda_status(cudaGetLastError()))) return st;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(a.B * a.H * a.T));
-    cfg.blockDim = dim3(128);
-    cfg.stream = stream;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, decode_join_kernel<HD>, (const DecParams)p, plan.parts));
+    return launch_after(decode_join_kernel<HD>, dim3((unsigned)(a.B * a.H * a.T)), 128, 0, stream, p, plan.parts);
 }
 
 }  // namespace

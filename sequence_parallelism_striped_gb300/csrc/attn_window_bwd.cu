@@ -174,6 +174,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    let_next_begin();
+    wait_for_previous();  // statistics and the cleared accumulator
     const uint32_t tmem = bars->tmem_slot;
     const uint32_t tS = tmem, tdP = tmem + 128, tdV = tmem + 256, tdK = tmem + 256 + HD;
 
@@ -535,44 +537,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// One warp per row of the padded tiles; lanes cover HD/32 elements each.
+// Four rows of the padded tiles per warp, eight lanes each: HD/8 elements a
+// lane in 16-byte vectors that the eight lanes read side by side.
 template <int HD>
 __global__ void __launch_bounds__(256)
     window_pre_kernel(const __nv_bfloat16 *__restrict__ o, const __nv_bfloat16 *__restrict__ dO,
                       const float *__restrict__ lse, float *__restrict__ stats, float *__restrict__ dq_acc,
                       const PosGeom g, int64_t padded_rows) {
-    constexpr int E = HD / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t nwarps = (int64_t)gridDim.x * (blockDim.x >> 5);
-    for (int64_t pr = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); pr < padded_rows; pr += nwarps) {
+    constexpr int V = HD / 64;  // 16-byte vectors of a lane
+    const int lane = threadIdx.x & 31, sub = lane & 7;
+    const int64_t stride = (int64_t)gridDim.x * (blockDim.x >> 3);
+    let_next_begin();
+    for (int64_t pr = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 3; pr < padded_rows; pr += stride) {
         const int64_t blk = pr >> 7;  // bh * nt + t
         const int r = (int)(pr & 127);
         const int64_t bh = blk / g.nt;
         const int t = (int)(blk - bh * g.nt);
-        float *st = stats + (blk << 8) + r;
         const bool real = tile_has(g, t, r);
-        float sum = 0.f;
         const int64_t row = bh * g.S + (real ? tile_row(g, t, r) : 0);
-        if (real) {
-            const __nv_bfloat162 *a = reinterpret_cast<const __nv_bfloat162 *>(o + row * HD + lane * E);
-            const __nv_bfloat162 *b = reinterpret_cast<const __nv_bfloat162 *>(dO + row * HD + lane * E);
+        uint4 x[V], y[V];
+        float ls = 0.f;
 #pragma unroll
-            for (int i = 0; i < E / 2; ++i) {
-                const float2 x = __bfloat1622float2(a[i]), y = __bfloat1622float2(b[i]);
-                sum = fmaf(x.x, y.x, sum);
-                sum = fmaf(x.y, y.y, sum);
+        for (int v = 0; v < V; ++v) {
+            x[v] = y[v] = make_uint4(0u, 0u, 0u, 0u);
+            if (real) {
+                x[v] = reinterpret_cast<const uint4 *>(o + row * HD)[8 * v + sub];
+                y[v] = reinterpret_cast<const uint4 *>(dO + row * HD)[8 * v + sub];
+            }
+        }
+        if (real && sub == 0) ls = lse[row];
+        float4 *z = reinterpret_cast<float4 *>(dq_acc + pr * HD) + sub;
+#pragma unroll
+        for (int v = 0; v < HD / 32; ++v) z[8 * v] = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const __nv_bfloat162 *a = reinterpret_cast<const __nv_bfloat162 *>(&x[v]);
+            const __nv_bfloat162 *b = reinterpret_cast<const __nv_bfloat162 *>(&y[v]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 c = __bfloat1622float2(a[i]), d = __bfloat1622float2(b[i]);
+                sum = fmaf(c.x, d.x, sum);
+                sum = fmaf(c.y, d.y, sum);
             }
         }
 #pragma unroll
-        for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        if (lane == 0) {
-            st[0] = real ? lse[row] * 1.4426950408889634f : INFINITY;
+        for (int off = 4; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        if (sub == 0) {
+            float *st = stats + (blk << 8) + r;
+            st[0] = real ? ls * 1.4426950408889634f : INFINITY;
             st[128] = sum;
         }
-        if constexpr (HD == 128)
-            *reinterpret_cast<float4 *>(dq_acc + pr * HD + lane * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
-        else
-            *reinterpret_cast<float2 *>(dq_acc + pr * HD + lane * 2) = make_float2(0.f, 0.f);
     }
 }
 
@@ -581,11 +596,13 @@ __global__ void __launch_bounds__(256)
 // 4l .. 4l+3 of each.  HD = 64: a thread takes a row, stored [D / 4][row][4].
 template <int HD>
 __global__ void __launch_bounds__(256)
-    window_post_kernel(const float *__restrict__ dq_acc, __nv_bfloat16 *__restrict__ dq, const PosGeom g,
+    window_post_kernel(const float *dq_acc, __nv_bfloat16 *dq, const PosGeom g,
                        int64_t padded_rows, float scale) {
     constexpr int T = HD == 128 ? 32 : 1, kRows = HD == 128 ? 4 : 1;
     const int64_t stride = (int64_t)gridDim.x * blockDim.x / T * kRows;
     const int part = threadIdx.x % T;
+    let_next_begin();
+    wait_for_previous();
     for (int64_t pr = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / T * kRows; pr < padded_rows; pr += stride) {
         const int64_t blk = pr >> 7;
         const int r = (int)(pr & 127);
@@ -623,6 +640,7 @@ __global__ void __launch_bounds__(256)
 template <int HD>
 __global__ void __launch_bounds__(8 * HD / 4)
     window_sink_kernel(const WinBwdParams p) {
+    wait_for_previous();  // and with it for the kernel before, which that one waited for
     const PosGeom &g = p.g;
     const int64_t bh = blockIdx.y / p.nst;
     const int kt = blockIdx.y % p.nst;
@@ -707,12 +725,13 @@ int launch_window_bwd_hd(const void *q, const void *k, const void *v, const void
     window_pre_kernel<HD><<<blocks, 256, 0, stream>>>((const __nv_bfloat16 *)o, (const __nv_bfloat16 *)dO, lse, stats,
                                                       dq_acc, p.g, plan.padded_rows);
     if ((st = cuda_status(cudaGetLastError()))) return st;
-    tc_window_bwd_kernel<HD><<<(unsigned)(p.units * bh_kv), kThreads, kSmemBytes, stream>>>(mq, mk, mv, mdo, p);
-    if ((st = cuda_status(cudaGetLastError()))) return st;
-    window_post_kernel<HD><<<blocks, 256, 0, stream>>>(dq_acc, (__nv_bfloat16 *)dq, p.g, plan.padded_rows, a.scale);
-    if ((st = cuda_status(cudaGetLastError())) || p.slots == 0) return st;
-    window_sink_kernel<HD><<<dim3(BT / 8, (unsigned)(bh_kv * p.nst)), 8 * HD / 4, 0, stream>>>(p);
-    return cuda_status(cudaGetLastError());
+    if ((st = launch_after(tc_window_bwd_kernel<HD>, dim3((unsigned)(p.units * bh_kv)), kThreads, kSmemBytes, stream, mq,
+                           mk, mv, mdo, p)))
+        return st;
+    st = launch_after(window_post_kernel<HD>, dim3((unsigned)blocks), 256, 0, stream, dq_acc, (__nv_bfloat16 *)dq, p.g,
+                      plan.padded_rows, a.scale);
+    if (st || p.slots == 0) return st;
+    return launch_after(window_sink_kernel<HD>, dim3(BT / 8, (unsigned)(bh_kv * p.nst)), 8 * HD / 4, 0, stream, p);
 }
 
 }  // namespace

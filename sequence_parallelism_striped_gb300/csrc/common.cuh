@@ -242,6 +242,14 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const W
 }
 
 // --------------------------------------------------------------------------
+// a kernel that follows another one on its stream (launch_after, internal.h)
+// --------------------------------------------------------------------------
+// The next kernel's blocks may be set up from now on.
+__device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// What the kernels before this one wrote is there from now on.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// --------------------------------------------------------------------------
 // TMA
 // --------------------------------------------------------------------------
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *m) {

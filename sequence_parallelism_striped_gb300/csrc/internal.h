@@ -16,6 +16,24 @@ namespace striped {
 // maps it to a status code.
 int cuda_status(cudaError_t err);
 
+// Launch a kernel whose blocks may be set up while the one before it on the
+// stream still runs; it calls wait_for_previous() before it reads what that
+// one wrote or writes what that one reads.
+template <typename... P, typename... A>
+int launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...));
+}
+
 // A status computed once per device, under a lock: kernel attributes (the
 // dynamic shared-memory opt-in) are per device, so a process that launches
 // on several GPUs sets them on each.

@@ -288,7 +288,10 @@ __global__ void __launch_bounds__(kRopeThreads, kBwd ? 4 : 7) norm_rope_kernel(c
             }
         }
     }
-    if constexpr (kBwd) rope_dw<VN, TP>(ln, p);
+    if constexpr (kBwd) {
+        let_next_begin();
+        rope_dw<VN, TP>(ln, p);
+    }
 }
 
 // The streamed form: a unit is kRows consecutive rows of one batch entry, one
@@ -389,14 +392,18 @@ __global__ void __launch_bounds__(kRopeThreads + 32, kBwd ? 3 : 4) norm_rope_str
             }
         }
     }
-    if constexpr (kBwd) rope_dw<VN, TP>(ln, p);
+    if constexpr (kBwd) {
+        let_next_begin();
+        rope_dw<VN, TP>(ln, p);
+    }
 }
 
 // dw = sum of the blocks' shares, in a fixed order.  One block per 8 columns
 // of one weight: 32 threads a column, each adding every 32nd share.
 __global__ void __launch_bounds__(256)
-    norm_rope_dw_kernel(const float *__restrict__ parts, float *__restrict__ dqw, float *__restrict__ dkw, int nq,
+    norm_rope_dw_kernel(const float *parts, float *dqw, float *dkw, int nq,
                         int nk, int D) {
+    wait_for_previous();
     const int which = blockIdx.y;
     const int col = blockIdx.x * 8 + threadIdx.x % 8, part = threadIdx.x / 8;
     const float *src = parts + (which ? (int64_t)nq * D : 0);
@@ -526,9 +533,8 @@ int launch_norm_rope(const RopeArgs &a, cudaStream_t stream) {
     st = a.dtype == STRIPED_BF16 ? launch_t<__nv_bfloat16, true>(p, g, tp, stream)
                                  : launch_t<float, true>(p, g, tp, stream);
     if (st != STRIPED_OK) return st;
-    norm_rope_dw_kernel<<<dim3((unsigned)((a.D + 7) / 8), 2), 256, 0, stream>>>(
-        p.parts, a.dq_weight, a.dk_weight, g.gx * g.cq, g.gx * g.ck, (int)a.D);
-    return cuda_status(cudaGetLastError());
+    return launch_after(norm_rope_dw_kernel, dim3((unsigned)((a.D + 7) / 8), 2), 256, 0, stream, p.parts, a.dq_weight,
+                        a.dk_weight, g.gx * g.cq, g.gx * g.ck, (int)a.D);
 }
 
 }  // namespace striped
