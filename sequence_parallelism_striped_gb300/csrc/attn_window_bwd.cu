@@ -5,7 +5,9 @@
 // t <= query p and (p - t < W or t < sinks)) and Delta_p = <dO_p, O_p>:
 //   dV = P^T dO,  dP = dO V^T,  dS = P * (dP - Delta),
 //   dK = scale * dS^T Q,  dQ = scale * dS K.
-// P and dS are rounded to bf16 as tensor-core operands; every sum is fp32.
+// P and dS are rounded to bf16 as tensor-core operands, dS from the unrounded
+// P (from the rounded one dQ and dK would be 2.9e-3 off instead of 2.4e-3, of
+// which the rounding of the results alone is 1.7e-3); every sum is fp32.
 //
 // Kernels:
 //   window_pre   per query tile of consecutive positions (window.cuh) the
@@ -361,9 +363,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto stat_ptr = [&](int i) -> const float * {
             return reinterpret_cast<const float *>(smem + kStatOff + (i % QS) * kStatBytes) + cbase;
         };
-        // P^T of tile t (index i): kept in registers (bf16 pairs) for dS and
-        // written to TMEM as the A operand of dV += P^T dO
-        uint32_t pkP[32];
+        // P^T of the tile: kept in registers, unrounded, for dS; rounded to
+        // bf16 into TMEM as the A operand of dV += P^T dO
+        uint32_t P[2][32];
         auto compute_p = [&](int i) -> bool {
             if (!mbar_wait(smem_u32(&bars->q_full[i % QS]), (i / QS) & 1, p.wc)) return false;
             if (!mbar_wait(smem_u32(&bars->s_full), i & 1, p.wc)) return false;
@@ -375,22 +377,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool full = kt < qt && (qbase + g.P - 1 - kbase < p.W || kbase + g.P <= p.sinks);
             const int first = kpos - qbase - cbase;
             const int last = kpos < p.sinks ? 0x7fffffff : kpos - qbase + p.W - 1 - cbase;
-            uint32_t rr[2][32];
-            tmem_ld32(tS + lane_off + cbase, rr[0]);
-            tmem_ld32(tS + lane_off + cbase + 32, rr[1]);
-            tmem_ld_wait(rr[0]);
-            tmem_ld_wait(rr[1]);
+            tmem_ld32(tS + lane_off + cbase, P[0]);
+            tmem_ld32(tS + lane_off + cbase + 32, P[1]);
+            tmem_ld_wait(P[0]);
+            tmem_ld_wait(P[1]);
 #pragma unroll
-            for (int u = 0; u < 32; u += 2) {
+            for (int u = 0; u < 64; u += 4) {
                 // four row statistics per 16-byte shared-memory load
-                const float4 l4 = *reinterpret_cast<const float4 *>(sL + 2 * u);
+                const float4 l4 = *reinterpret_cast<const float4 *>(sL + u);
                 const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
-                float e[4];
 #pragma unroll
-                for (int h = 0; h < 4; ++h)
-                    e[h] = ex2(fmaf(__uint_as_float(rr[u / 16][2 * u % 32 + h]), cl2, -lv[h]));
-                pkP[u] = pack_bf16x2(e[0], e[1]);
-                pkP[u + 1] = pack_bf16x2(e[2], e[3]);
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t &s1 = P[u / 32][u % 32 + h];
+                    s1 = __float_as_uint(ex2(fmaf(__uint_as_float(s1), cl2, -lv[h])));
+                }
             }
             if (!full || !key_valid) {
                 // clear the pairs that are not kept (whatever their exp gave)
@@ -398,12 +398,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < 2; ++c) {
                     const uint32_t kept = key_valid ? kept_bits(32 * c, last, first, 0) : 0u;
 #pragma unroll
-                    for (int u = 0; u < 16; ++u)
-                        pkP[16 * c + u] &= (kept & (1u << (2 * u)) ? 0x0000ffffu : 0u) |
-                                           (kept & (2u << (2 * u)) ? 0xffff0000u : 0u);
+                    for (int u = 0; u < 32; ++u)
+                        if (!(kept & (1u << u))) P[c][u] = 0u;
                 }
             }
-            tmem_st32(tS + lane_off + pbase, pkP);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int u = 0; u < 16; ++u)
+                    pk[u] = pack_bf16x2(__uint_as_float(P[c][2 * u]), __uint_as_float(P[c][2 * u + 1]));
+                tmem_st16(tS + lane_off + pbase + 16 * c, pk);
+            }
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -420,30 +426,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             const float *sD = stat_ptr(i) + 128;
-            uint32_t rr[2][32];
-            tmem_ld32(tdP + lane_off + cbase, rr[0]);
-            tmem_ld32(tdP + lane_off + cbase + 32, rr[1]);
-            tmem_ld_wait(rr[0]);
-            tmem_ld_wait(rr[1]);
 #pragma unroll
-            for (int v = 0; v < 8; ++v) {
-                uint32_t w[4];
-                // eight Delta values in two 16-byte loads
-                const float4 d0 = *reinterpret_cast<const float4 *>(sD + 8 * v);
-                const float4 d1 = *reinterpret_cast<const float4 *>(sD + 8 * v + 4);
-                const uint64_t dd[4] = {f2(d0.x, d0.y), f2(d0.z, d0.w), f2(d1.x, d1.y), f2(d1.z, d1.w)};
+            for (int c = 0; c < 2; ++c) {
+                uint32_t rr[32];
+                tmem_ld32(tdP + lane_off + cbase + 32 * c, rr);
+                tmem_ld_wait(rr);
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const int u = v * 4 + h;  // pair of query columns
-                    const uint32_t *x = &rr[u / 16][2 * u % 32];
-                    __nv_bfloat162 pv = *reinterpret_cast<__nv_bfloat162 *>(&pkP[u]);
-                    const float2 pf = __bfloat1622float2(pv);
-                    // dS = P * (dP - Delta), two at a time
-                    const float2 ds = f2_split(
-                        mul2(f2(pf.x, pf.y), sub2(f2(__uint_as_float(x[0]), __uint_as_float(x[1])), dd[h])));
-                    w[h] = pack_bf16x2(ds.x, ds.y);
+                for (int v = 0; v < 4; ++v) {
+                    uint32_t w[4];
+                    // eight Delta values in two 16-byte loads
+                    const float4 d0 = *reinterpret_cast<const float4 *>(sD + 32 * c + 8 * v);
+                    const float4 d1 = *reinterpret_cast<const float4 *>(sD + 32 * c + 8 * v + 4);
+                    const uint64_t dd[4] = {f2(d0.x, d0.y), f2(d0.z, d0.w), f2(d1.x, d1.y), f2(d1.z, d1.w)};
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const int u = 8 * v + 2 * h;  // query columns u, u + 1
+                        // dS = P * (dP - Delta), two at a time
+                        const float2 ds = f2_split(
+                            mul2(f2(__uint_as_float(P[c][u]), __uint_as_float(P[c][u + 1])),
+                                 sub2(f2(__uint_as_float(rr[u]), __uint_as_float(rr[u + 1])), dd[h])));
+                        w[h] = pack_bf16x2(ds.x, ds.y);
+                    }
+                    *reinterpret_cast<uint4 *>(sDS + (((4 * c + v) ^ (row & 7)) * 16)) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                *reinterpret_cast<uint4 *>(sDS + ((v ^ (row & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
             fence_proxy_async_smem();
             tc_fence_before();

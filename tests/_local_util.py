@@ -64,7 +64,7 @@ def window_reference(q, k, v, pos, window, sinks, scale, dO=None, o_given=None):
             ds = p * (dp - delta)
             # fp32 error of dP - Delta: sums of up to 128 products, twice
             soft = p * (2.0 ** -16 * (do.abs() @ v[b, g].abs().T + delta.abs()))
-            mag = 2.05 * BF * ds.abs() + soft
+            mag = 1.02 * BF * ds.abs() + soft
             r["dq"][b, h] = scale * ds @ k[b, g]
             r["dq_tol"][b, h] = scale * mag @ k[b, g].abs()
             r["dk"][b, g] += scale * ds.T @ q[b, h]
