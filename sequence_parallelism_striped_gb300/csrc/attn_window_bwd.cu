@@ -80,6 +80,7 @@ struct WinBwdParams {
     float *dq_acc;       // [BH][nt] tiles of fp32: HD = 128 [query / 4][D][4], HD = 64 [D / 4][query][4]
     float *parts;        // [BHkv][nst][slots][dK 128 D | dV 128 D] fp32
     __nv_bfloat16 *dk, *dv;
+    bool wide;  // dk and dv are 32-byte aligned
     WaitCtl wc;  // status word, wait bound, test hook
 };
 
@@ -485,20 +486,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (shared_tile) {
                     float *acc = part + (which ? 0 : BT * HD) + c * 32;
 #pragma unroll
-                    for (int u = 0; u < 32; u += 4)
-                        *reinterpret_cast<float4 *>(acc + u) =
-                            make_float4(__uint_as_float(rr[u]) * mul, __uint_as_float(rr[u + 1]) * mul,
-                                        __uint_as_float(rr[u + 2]) * mul, __uint_as_float(rr[u + 3]) * mul);
-                } else if (key_valid) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(outp + krow + c * 32);
+                    for (int u = 0; u < 32; u += 8) {
+                        uint32_t f8[8];
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        uint4 w;
-                        w.x = pack_bf16x2(__uint_as_float(rr[8 * v + 0]) * mul, __uint_as_float(rr[8 * v + 1]) * mul);
-                        w.y = pack_bf16x2(__uint_as_float(rr[8 * v + 2]) * mul, __uint_as_float(rr[8 * v + 3]) * mul);
-                        w.z = pack_bf16x2(__uint_as_float(rr[8 * v + 4]) * mul, __uint_as_float(rr[8 * v + 5]) * mul);
-                        w.w = pack_bf16x2(__uint_as_float(rr[8 * v + 6]) * mul, __uint_as_float(rr[8 * v + 7]) * mul);
-                        dst[v] = w;
+                        for (int i = 0; i < 8; ++i) f8[i] = __float_as_uint(__uint_as_float(rr[u + i]) * mul);
+                        st_global_32(acc + u, f8, true);  // the workspace is 256-byte aligned
+                    }
+                } else if (key_valid) {
+                    __nv_bfloat16 *dst = outp + krow + c * 32;
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        uint32_t o8[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            o8[i] = pack_bf16x2(__uint_as_float(rr[16 * v + 2 * i]) * mul,
+                                                __uint_as_float(rr[16 * v + 2 * i + 1]) * mul);
+                        st_global_32(dst + 16 * v, o8, p.wide);
                     }
                 }
             }
@@ -720,6 +723,7 @@ int launch_window_bwd_hd(const void *q, const void *k, const void *v, const void
     p.parts = reinterpret_cast<float *>(ws + plan.dq_bytes + plan.stat_bytes);
     p.dk = static_cast<__nv_bfloat16 *>(dk);
     p.dv = static_cast<__nv_bfloat16 *>(dv);
+    p.wide = ((reinterpret_cast<uintptr_t>(dk) | reinterpret_cast<uintptr_t>(dv)) & 31u) == 0;
     p.wc = device_wait_ctl();
     const int64_t bh = a.B * a.H, bh_kv = a.B * a.Hkv;
     CUtensorMap mq, mk, mv, mdo;

@@ -77,6 +77,7 @@ struct WinParams {
     float scale;
     __nv_bfloat16 *o;
     float *lse;
+    bool wide;    // o is 32-byte aligned
     WaitCtl wc;
 };
 
@@ -407,15 +408,15 @@ __global__ void __launch_bounds__(kWThreads, 1)
                 tmem_ld32(tO + c * 32, rr);
                 tmem_ld_wait(rr);
                 if (!valid) continue;
-                uint4 *dst = reinterpret_cast<uint4 *>(p.o + row * HD + c * 32);
+                __nv_bfloat16 *dst = p.o + row * HD + c * 32;
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    uint4 o4;
-                    o4.x = pack_bf16x2(__uint_as_float(rr[8 * v + 0]) * inv_l, __uint_as_float(rr[8 * v + 1]) * inv_l);
-                    o4.y = pack_bf16x2(__uint_as_float(rr[8 * v + 2]) * inv_l, __uint_as_float(rr[8 * v + 3]) * inv_l);
-                    o4.z = pack_bf16x2(__uint_as_float(rr[8 * v + 4]) * inv_l, __uint_as_float(rr[8 * v + 5]) * inv_l);
-                    o4.w = pack_bf16x2(__uint_as_float(rr[8 * v + 6]) * inv_l, __uint_as_float(rr[8 * v + 7]) * inv_l);
-                    dst[v] = o4;
+                for (int v = 0; v < 2; ++v) {
+                    uint32_t o8[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        o8[i] = pack_bf16x2(__uint_as_float(rr[16 * v + 2 * i]) * inv_l,
+                                            __uint_as_float(rr[16 * v + 2 * i + 1]) * inv_l);
+                    st_global_32(dst + 16 * v, o8, p.wide);
                 }
             }
             tc_fence_before();  // O is read out before the next item's first P is announced
@@ -457,6 +458,7 @@ int launch_tc_window_fwd(const void *q, const void *k, const void *v, void *o, f
     p.scale = a.scale;
     p.o = static_cast<__nv_bfloat16 *>(o);
     p.lse = lse;
+    p.wide = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
     p.wc = device_wait_ctl();
     const int sms = device_sm_count();
     const int64_t items = (int64_t)p.npair * a.B * a.H;

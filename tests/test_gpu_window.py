@@ -147,6 +147,25 @@ def test_run_to_run_stream_and_graph():
     assert sp.check_error() == 0
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_results_at_16_byte_addresses(D):
+    """Results that start 16 bytes past a 32-byte boundary: the same values."""
+    B, H, Hkv, S, N, W, ns = 1, 2, 1, 600, 4, 100, 3
+    q, k, v, do = (t.to(DEV) for t in _make(B, H, Hkv, S, D, 8))
+
+    def off(t):  # an uninitialised tensor like t, 16 bytes into its storage
+        return torch.empty(t.numel() + 8, dtype=t.dtype, device=DEV)[8:].view(t.shape)
+
+    o, lse = sp.striped_attn_window_fwd(q, k, v, N, W, ns)
+    o2, lse2 = sp.striped_attn_window_fwd(q, k, v, N, W, ns, out=off(o))
+    assert o2.data_ptr() % 32 == 16 and torch.equal(o, o2) and torch.equal(lse, lse2)
+    want = sp.striped_attn_window_bwd(q, k, v, o, lse, do, N, W, ns)
+    got = sp.striped_attn_window_bwd(q, k, v, o, lse, do, N, W, ns, dq=off(q), dk=off(k), dv=off(v))
+    assert torch.equal(want[1], got[1]) and torch.equal(want[2], got[2])
+    # dQ is summed by atomics: a bf16 rounding apart at most
+    assert float((want[0].float() - got[0].float()).abs().max()) <= 2.0 ** -7 * float(want[0].float().abs().max())
+
+
 def test_a_missing_tile_times_out():
     """The bounded waits end, report and leave the device usable."""
     q, k, v, do = (t.to(DEV) for t in _make(1, 2, 2, 512, 128, 4))
