@@ -482,6 +482,16 @@ def _buffer(t, name: str, dev: int):
     return _need(t, name, t.shape, t.dtype, dev), t.numel() * t.element_size()
 
 
+def _work(t, size, dev: int, *args):
+    """Address, bytes and tensor of a workspace: the caller's, or a new one of
+    size(dev, *args) bytes."""
+    if t is None:
+        t = torch.empty(max(size(dev, *args), 256), dtype=torch.uint8, device=dev)
+        return t.data_ptr(), t.shape[0], t
+    p, n = _buffer(t, "workspace", dev)
+    return p, n, t
+
+
 class _elsewhere:
     """Make a call on the given stream, or on the device of its tensors where
     another is current.  What is allocated inside belongs to that stream, so
@@ -528,12 +538,16 @@ def striped_attn_window_fwd(q, k, v, N: int, window: int, sinks: int = 0, layout
     return o, lse
 
 
+@functools.lru_cache(maxsize=256)
+def _window_workspace_size(dev: int, *args) -> int:
+    return int(load().striped_attn_window_workspace_size(*args))
+
+
 def new_window_workspace(q, k, N: int, window: int, sinks: int = 0, layout: int = STRIPED) -> torch.Tensor:
     """Workspace of striped_attn_window_bwd for these tensors and arguments."""
     B, H, S, D = q.shape
-    n = int(load().striped_attn_window_workspace_size(B, H, k.shape[1], S, D, N, layout, _dtype_code(q), int(window),
-                                                      int(sinks)))
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+    return _work(None, _window_workspace_size, q.get_device(), B, H, k.shape[1], S, D, N, layout, _dtype_code(q),
+                 window, sinks)[2]
 
 
 def striped_attn_window_bwd(q, k, v, o, lse, dO, N: int, window: int, sinks: int = 0, layout: int = STRIPED,
@@ -552,14 +566,13 @@ def striped_attn_window_bwd(q, k, v, o, lse, dO, N: int, window: int, sinks: int
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
-    ws = new_window_workspace(q, k, N, window, sinks, layout) if workspace is None else workspace
-    wp, wn = _buffer(ws, "workspace", dev)
+    code = _dtype_code(q)
+    wp, wn, workspace = _work(workspace, _window_workspace_size, dev, B, H, Hkv, S, D, N, layout, code, window, sinks)
     _check(load().striped_attn_window_bwd(
         _need(q, "q", qs, dt, dev), _need(k, "k", kv, dt, dev), _need(v, "v", kv, dt, dev), _need(o, "o", qs, dt, dev),
         _need(lse, "lse", (B, H, S), torch.float32, dev), _need(dO, "dO", qs, dt, dev), _need(dq, "dq", qs, dt, dev),
-        _need(dk, "dk", kv, dt, dev), _need(dv, "dv", kv, dt, dev), wp, wn, B, H, Hkv, S, D, N, layout,
-        _dtype_code(q), window, sinks, 1.0 / D ** 0.5 if scale is None else scale, _raw_stream(dev)),
-        "striped_attn_window_bwd")
+        _need(dk, "dk", kv, dt, dev), _need(dv, "dv", kv, dt, dev), wp, wn, B, H, Hkv, S, D, N, layout, code, window,
+        sinks, 1.0 / D ** 0.5 if scale is None else scale, _raw_stream(dev)), "striped_attn_window_bwd")
     return dq, dk, dv
 
 
@@ -590,8 +603,7 @@ def new_decode_workspace(q, k_prompt, k_tail, N: int = 1, layout: int = STRIPED,
     if not _here(dev, None):
         with _elsewhere(dev, None):
             return new_decode_workspace(q, k_prompt, k_tail, N, layout, window, sinks)
-    need = _decode_workspace_size(dev, *n, N, layout, _dtype_code(q), window, sinks)
-    return torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    return _work(None, _decode_workspace_size, dev, *n, N, layout, _dtype_code(q), window, sinks)[2]
 
 
 def striped_attn_decode(q, k_prompt, v_prompt, k_tail, v_tail, tail_lens, N: int = 1, layout: int = STRIPED,
@@ -616,9 +628,7 @@ def striped_attn_decode(q, k_prompt, v_prompt, k_tail, v_tail, tail_lens, N: int
     tail = (B, Hkv, C, D)
     o = torch.empty_like(q) if out is None else out
     lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device) if lse_out is None else lse_out
-    if workspace is None:
-        workspace = new_decode_workspace(q, k_prompt, k_tail, N, layout, window, sinks)
-    wp, wn = _buffer(workspace, "workspace", dev)
+    wp, wn, workspace = _work(workspace, _decode_workspace_size, dev, *n, N, layout, code, window, sinks)
     _check(load().striped_attn_decode(
         _need(q, "q", q.shape, dt, dev), kp, vp, _need(k_tail, "k_tail", tail, dt, dev),
         _need(v_tail, "v_tail", tail, dt, dev), _need(tail_lens, "tail_lens", (B,), torch.int32, dev),
@@ -667,11 +677,15 @@ def striped_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, N: int = 1, layout:
     return yq, yk
 
 
+@functools.lru_cache(maxsize=256)
+def _rope_workspace_size(dev: int, *args) -> int:
+    return int(load().striped_qk_norm_rope_workspace_size(*args))
+
+
 def qk_norm_rope_workspace(q, k) -> torch.Tensor:
     """Workspace of striped_qk_norm_rope_bwd for these q and k."""
     B, H, S, D = q.shape
-    n = int(load().striped_qk_norm_rope_workspace_size(B, H, k.shape[1], S, D, _dtype_code(q)))
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+    return _work(None, _rope_workspace_size, q.get_device(), B, H, k.shape[1], S, D, _dtype_code(q))[2]
 
 
 def striped_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, inv_freq, N: int = 1, layout: int = STRIPED,
@@ -697,15 +711,15 @@ def striped_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, inv_freq,
     dk = torch.empty_like(k) if dk is None else dk
     dqw = torch.empty_like(q_weight) if dq_weight is None else dq_weight
     dkw = torch.empty_like(k_weight) if dk_weight is None else dk_weight
-    ws = qk_norm_rope_workspace(q, k) if workspace is None else workspace
-    wp, wn = _buffer(ws, "workspace", dev)
+    code = _dtype_code(q)
+    wp, wn, workspace = _work(workspace, _rope_workspace_size, dev, B, H, Hkv, S, D, code)
     _check(load().striped_qk_norm_rope_bwd(
         _need(q, "q", qs, dt, dev), _need(k, "k", ks, dt, dev), _need(dq_out, "dq_out", qs, dt, dev),
         _need(dk_out, "dk_out", ks, dt, dev), _need(dq, "dq", qs, dt, dev), _need(dk, "dk", ks, dt, dev),
         _need(dqw, "dq_weight", (D,), f32, dev), _need(dkw, "dk_weight", (D,), f32, dev), qw, kw,
         _need(inv_freq, "inv_freq", (half,), torch.float64, dev),
         None if positions is None else _need(positions, "positions", (B, S), torch.int64, dev), wp, wn, B, H, Hkv, S,
-        D, 2 * half, 1 if interleaved else 0, N, layout, -1 if stripe is None else stripe, eps, _dtype_code(q),
+        D, 2 * half, 1 if interleaved else 0, N, layout, -1 if stripe is None else stripe, eps, code,
         _raw_stream(dev)), "striped_qk_norm_rope_bwd")
     return dq, dk, dqw, dkw
 
