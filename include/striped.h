@@ -325,6 +325,8 @@ int ring_bwd_finish(const float *acc, void *out, int64_t n, int dtype, float mul
  * kernels work on tiles of consecutive positions, not on the per-round tiles
  * of the ring, so there is no tile_stats.  K and V must be finite in every
  * row: a tile multiplies the weight 0 of a pair that is not kept with its V.
+ * scale must be a normal number in (0, 1e38], and no result may overlap
+ * another tensor of the call: else STRIPED_ERR_INVALID_ARG.
  */
 int striped_attn_window_fwd(const void *q, const void *k, const void *v, void *o, float *lse, int64_t B, int64_t H,
                             int64_t Hkv, int64_t S, int64_t D, int N, int layout, int dtype, int64_t window,
@@ -342,7 +344,10 @@ size_t striped_attn_window_workspace_size(int64_t B, int64_t H, int64_t Hkv, int
  * overwritten; a shared key/value head gets the sum over its query heads).
  * workspace: 256-byte aligned, its contents on entry are ignored.  dK and dV
  * are the same from run to run; dQ is accumulated with fp32 atomics (a few
- * fp32 ulps before it is rounded).
+ * fp32 ulps before it is rounded).  The dO of a row that does not count
+ * (padding) must be 0.  Calls that may overlap (other streams, graphs
+ * replayed side by side) each need their own workspace; no result may overlap
+ * it or another tensor.
  */
 int striped_attn_window_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
                             const void *dO, void *dq, void *dk, void *dv, void *workspace, size_t ws_bytes, int64_t B,
@@ -363,20 +368,22 @@ int striped_attn_window_bwd(const void *q, const void *k, const void *v, const v
  *              0 .. len-1 of request b hold positions P .. P+len-1, the new
  *              tokens' own keys among them (the T last).  Rows from len on
  *              are never used, whatever they hold; a length outside 0..C is
- *              taken as the nearer end.
+ *              taken as the nearer end.  The rows before len, and the
+ *              prompt's, must be finite.
  * Token t stands at position P + len - T + t and keeps the keys at or before
  * it; with window > 0 only those less than `window` before it or among the
  * first `sinks` positions (window = 0: all).  A token before position 0
  * (len + P < T) keeps none: o = 0, lse = -infinity.
  * bf16 with D == 64 or 128, at most 128 stripes in the striped placement,
- * zig-zag as for striped_attn_fwd, P + C <= 2^31 - 256; with g = H/Hkv * T
+ * zig-zag as for striped_attn_fwd, P + C + T <= 2^31 - 256; with g = H/Hkv * T
  * rows a request, Bp * ceil(B/Bp * g / 128) (P > 0) + B * ceil(g / 128)
  * <= 2048: else STRIPED_ERR_UNSUPPORTED (split the batch).
  * Segments are joined in a fixed order: results are the same from run to run
  * (on the same kind of GPU).  workspace: 256-byte aligned, >=
  * striped_attn_decode_workspace_size() bytes, contents ignored; calls that
  * may overlap (other streams, graphs replayed side by side) each need their
- * own.
+ * own.  scale is bounded as for striped_attn_window_fwd, and no result may
+ * overlap another tensor or the workspace.
  */
 int striped_attn_decode(const void *q, const void *k_prompt, const void *v_prompt, const void *k_tail,
                         const void *v_tail, const int32_t *tail_lens, void *o, float *lse, void *workspace,
@@ -401,9 +408,11 @@ size_t striped_attn_decode_workspace_size(int64_t B, int64_t Bp, int64_t H, int6
  * for the pairs (a, b) = (j, j + rotary_dim/2), or (2j, 2j + 1) with
  * interleaved != 0, j < rotary_dim/2; elements from rotary_dim on are not
  * rotated (rotary_dim = 0: norm only, inv_freq may be NULL).  Angles are
- * reduced in 64 bits, so they stay exact at far positions.
+ * reduced in 64 bits, so they stay exact at far positions (inv_freq finite).
+ * Squares and their sums are fp32: |x| below 1e18, and eps > 0 wherever a row
+ * may be all 0.
  *  q, q_out: [B,H,S,D], k, k_out: [B,Hkv,S,D] `dtype`; H and Hkv are any
- *            counts >= 1.  q_out may be q and k_out may be k (in place); any
+ *            counts up to 65536.  q_out may be q and k_out may be k (in place); any
  *            other overlap of a result with another tensor is
  *            STRIPED_ERR_INVALID_ARG.
  *  q_weight, k_weight: [D] fp32.  inv_freq: [rotary_dim/2] fp64.
@@ -432,7 +441,8 @@ size_t striped_qk_norm_rope_workspace_size(int64_t B, int64_t H, int64_t Hkv, in
  *     dx = r h - x r^3 mean(h x),  r = 1 / sqrt(mean(x^2) + eps).
  * dq may be q or dq_out, dk may be k or dk_out (in place).  Sums in a fixed
  * order: results are the same from run to run.  workspace: 16-byte aligned,
- * >= striped_qk_norm_rope_workspace_size() bytes, its contents are ignored.
+ * >= striped_qk_norm_rope_workspace_size() bytes, its contents are ignored;
+ * calls that may overlap each need their own.
  */
 int striped_qk_norm_rope_bwd(const void *q, const void *k, const void *dq_out, const void *dk_out, void *dq, void *dk,
                              float *dq_weight, float *dk_weight, const float *q_weight, const float *k_weight,

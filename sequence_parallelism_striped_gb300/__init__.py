@@ -447,7 +447,8 @@ def striped_attn_bwd_varlen(q, k, v, o, lse, dO, cu_seqlens, N: int, layout: int
 
 
 # ------------------------------------------------------------------ argument checks
-_raw_stream = torch._C._cuda_getCurrentRawStream  # a current_stream() object costs as much as a launch
+# a current_stream() object costs as much as a launch
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # None: torch without CUDA
 
 
 def _rank(t, name: str, n: int):

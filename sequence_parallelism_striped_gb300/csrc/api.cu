@@ -574,11 +574,43 @@ int ring_round_fwd(const void *q_d, const void *k_e, const void *v_e, float *o_a
 }
 
 // ---------------------------------------------------------------- window attention
+// A call's buffers.  Results must lie apart from one another and from every
+// input; with `in_place`, results 0 and 1 may be one of the inputs 0 .. 3 of
+// their own parity (q and k, or their cotangents) as a whole.
+struct Range {
+    const void *p;
+    int64_t n;
+};
+static bool overlap(const Range &a, const Range &b) {
+    const char *x = (const char *)a.p, *y = (const char *)b.p;
+    return x && y && x < y + b.n && y < x + a.n;
+}
+static bool results_overlap(const Range *out, int no, const Range *in, int ni, bool in_place = false) {
+    for (int i = 0; i < no; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return true;
+        for (int j = 0; j < ni; ++j) {
+            if (in_place && i < 2 && j < 4 && j % 2 == i && out[i].p == in[j].p) continue;
+            if (overlap(out[i], in[j])) return true;
+        }
+    }
+    return false;
+}
+
+// Rows of D <= 256 elements that no GPU holds, and whose byte counts still
+// fit 64 bits.
+constexpr int64_t kMaxRows = 1ll << 40;
+
+// The running maximum is taken over unscaled scores, and a masked score of
+// -infinity times the scale has to stay that.
+static bool valid_scale(float scale) { return scale >= 1.17549435e-38f && scale <= 1e38f; }
+
 static int check_window(const WindowArgs &a, int dtype) {
-    if (a.Hkv < 1 || a.H < 1 || a.H % a.Hkv != 0 || a.window < 1 || a.sinks < 0) return STRIPED_ERR_INVALID_ARG;
+    if (a.Hkv < 1 || a.H < 1 || a.H % a.Hkv != 0 || a.window < 1 || a.sinks < 0 || !valid_scale(a.scale))
+        return STRIPED_ERR_INVALID_ARG;
     const int st = check_attn(a.B, a.H, a.S, a.D, a.N, a.layout, dtype);
     if (st) return st;
-    if (dtype != STRIPED_BF16 || a.sinks > kMaxSinks || a.S > kMaxPositions) return STRIPED_ERR_UNSUPPORTED;
+    if (a.B * a.H * a.S > kMaxRows || dtype != STRIPED_BF16 || a.sinks > kMaxSinks || a.S > kMaxPositions) return STRIPED_ERR_UNSUPPORTED;
     if (a.layout == STRIPED_LAYOUT_STRIPED && a.N > 128) return STRIPED_ERR_UNSUPPORTED;
     return STRIPED_OK;
 }
@@ -591,6 +623,9 @@ int striped_attn_window_fwd(const void *q, const void *k, const void *v, void *o
     const int st = check_window(a, dtype);
     if (st) return st;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse)) return STRIPED_ERR_ALIGN;
+    const int64_t nq = B * H * S * D * 2, nk = B * Hkv * S * D * 2;
+    const Range out[2] = {{o, nq}, {lse, B * H * S * 4}}, in[3] = {{q, nq}, {k, nk}, {v, nk}};
+    if (results_overlap(out, 2, in, 3)) return STRIPED_ERR_INVALID_ARG;
     return launch_tc_window_fwd(q, k, v, o, lse, a, (cudaStream_t)stream);
 }
 
@@ -616,13 +651,17 @@ int striped_attn_window_bwd(const void *q, const void *k, const void *v, const v
     const void *ptrs[9] = {q, k, v, o, lse, dO, dq, dk, dv};
     for (const void *p : ptrs)
         if (!aligned16(p)) return STRIPED_ERR_ALIGN;
+    const int64_t nq = B * H * S * D * 2, nk = B * Hkv * S * D * 2;
+    const Range out[4] = {{dq, nq}, {dk, nk}, {dv, nk}, {workspace, (int64_t)need}};
+    const Range in[6] = {{q, nq}, {k, nk}, {v, nk}, {o, nq}, {lse, B * H * S * 4}, {dO, nq}};
+    if (results_overlap(out, 4, in, 6)) return STRIPED_ERR_INVALID_ARG;
     return launch_tc_window_bwd(q, k, v, o, lse, dO, dq, dk, dv, workspace, a, (cudaStream_t)stream);
 }
 
 // ---------------------------------------------------------------- decoding
 static int check_decode(const DecodeArgs &a, int dtype) {
     if (a.B < 1 || a.H < 1 || a.Hkv < 1 || a.H % a.Hkv != 0 || a.T < 1 || a.P < 0 || a.C < 1 || a.window < 0 ||
-        a.sinks < 0)
+        a.sinks < 0 || !valid_scale(a.scale))
         return STRIPED_ERR_INVALID_ARG;
     if (dtype != STRIPED_BF16) return dtype == STRIPED_FP32 ? STRIPED_ERR_UNSUPPORTED : STRIPED_ERR_INVALID_ARG;
     if (a.D != 64 && a.D != 128) return a.D < 1 ? STRIPED_ERR_INVALID_ARG : STRIPED_ERR_UNSUPPORTED;
@@ -633,8 +672,10 @@ static int check_decode(const DecodeArgs &a, int dtype) {
         if (a.layout == STRIPED_LAYOUT_STRIPED && a.N > 128) return STRIPED_ERR_UNSUPPORTED;
     }
     const int64_t limit = 1ll << 30;  // counts that the kernels hold in 32 bits
-    if (a.P > kMaxPositions || a.C > kMaxPositions || a.P + a.C > kMaxPositions) return STRIPED_ERR_UNSUPPORTED;
-    if (a.B > limit || a.H > limit || a.T > limit || a.B * a.H > limit || a.B * a.H * a.T > limit)
+    if (a.P > kMaxPositions || a.C > kMaxPositions || a.T > limit || a.P + a.C + a.T > kMaxPositions)
+        return STRIPED_ERR_UNSUPPORTED;
+    if (a.B > limit || a.H > limit || a.B * a.H > limit || a.B * a.H * a.T > limit ||
+        a.B * a.Hkv * (a.P + a.C) > kMaxRows)
         return STRIPED_ERR_UNSUPPORTED;
     return decode_workspace(a) == 0 ? STRIPED_ERR_UNSUPPORTED : STRIPED_OK;
 }
@@ -656,37 +697,36 @@ int striped_attn_decode(const void *q, const void *k_prompt, const void *v_promp
     const DecodeArgs a{B, Bp, H, Hkv, T, P, C, D, N, layout, window, sinks, scale};
     const int st = check_decode(a, dtype);
     if (st) return st;
-    if (!workspace || ws_bytes < decode_workspace(a)) return STRIPED_ERR_WORKSPACE;
+    const size_t need = decode_workspace(a);
+    if (!workspace || ws_bytes < need) return STRIPED_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return STRIPED_ERR_ALIGN;
     const void *ptrs[5] = {q, k_tail, v_tail, o, lse};
     for (const void *p : ptrs)
         if (!aligned16(p)) return STRIPED_ERR_ALIGN;
     if (P > 0 && (!aligned16(k_prompt) || !aligned16(v_prompt))) return STRIPED_ERR_ALIGN;
     if ((reinterpret_cast<uintptr_t>(tail_lens) & 3u) != 0) return STRIPED_ERR_ALIGN;
+    const int64_t nq = B * H * T * D * 2, np = P > 0 ? Bp * Hkv * P * D * 2 : 0, nt = B * Hkv * C * D * 2;
+    const Range out[3] = {{o, nq}, {lse, B * H * T * 4}, {workspace, (int64_t)need}};
+    const Range in[6] = {{q, nq}, {k_prompt, np}, {v_prompt, np}, {k_tail, nt}, {v_tail, nt}, {tail_lens, B * 4}};
+    if (results_overlap(out, 3, in, 6)) return STRIPED_ERR_INVALID_ARG;
     return launch_tc_decode(q, k_prompt, v_prompt, k_tail, v_tail, tail_lens, o, lse, workspace, a,
                             (cudaStream_t)stream);
 }
 
 // ---------------------------------------------------------------- norm and rotation
-// Two buffers may be the same one (`alias`: results over their own inputs)
-// but must not overlap in any other way.
-static bool overlap(const void *a, int64_t na, const void *b, int64_t nb, bool alias) {
-    if (!a || !b || (alias && a == b && na == nb)) return false;
-    const char *x = (const char *)a, *y = (const char *)b;
-    return x < y + nb && y < x + na;
-}
+constexpr int64_t kMaxRopeHeads = 1 << 16;  // a block row of the grid per eight of them, for both tensors
 
 static int check_rope(const RopeArgs &a) {
     if (!a.q || !a.k || !a.q_res || !a.k_res || !a.q_weight || !a.k_weight) return STRIPED_ERR_INVALID_ARG;
     if (a.rot < 0 || a.rot > a.D || (a.rot > 0 && !a.inv_freq)) return STRIPED_ERR_INVALID_ARG;
     if (!(a.eps >= 0.f)) return STRIPED_ERR_INVALID_ARG;
-    if (a.H < 1 || a.Hkv < 1 || !valid_layout(a.layout)) return STRIPED_ERR_INVALID_ARG;
+    if (a.H < 1 || a.Hkv < 1) return STRIPED_ERR_INVALID_ARG;
     // one stripe's rows: S is the stripe's length and any S fits
     const bool placed = !a.positions && a.stripe < 0;
     int st = check_sizes(a.B, a.H > a.Hkv ? a.H : a.Hkv, a.S, a.D, placed ? a.N : 1);
     if (st) return st;
     if (!a.positions) {
-        if (a.N < 1 || a.stripe < -1 || a.stripe >= a.N) return STRIPED_ERR_INVALID_ARG;
+        if (!valid_layout(a.layout) || a.N < 1 || a.stripe < -1 || a.stripe >= a.N) return STRIPED_ERR_INVALID_ARG;
         if (a.layout == STRIPED_LAYOUT_ZIGZAG && (placed ? a.S % (2 * (int64_t)a.N) : a.S % 2) != 0)
             return STRIPED_ERR_INVALID_ARG;
     }
@@ -695,6 +735,8 @@ static int check_rope(const RopeArgs &a) {
     else if (a.dtype == STRIPED_FP32) unit = 8, es = 4;
     else return STRIPED_ERR_INVALID_ARG;
     if (a.D > 256 || a.D % unit != 0 || a.rot % unit != 0) return STRIPED_ERR_UNSUPPORTED;
+    if (a.H > kMaxRopeHeads || a.Hkv > kMaxRopeHeads || a.B * (a.H > a.Hkv ? a.H : a.Hkv) * a.S > kMaxRows)
+        return STRIPED_ERR_UNSUPPORTED;
     const void *ptrs[6] = {a.q, a.k, a.q_res, a.k_res, a.dq_out, a.dk_out};
     for (const void *p : ptrs)
         if (!aligned16(p)) return STRIPED_ERR_ALIGN;
@@ -703,16 +745,13 @@ static int check_rope(const RopeArgs &a) {
         if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return STRIPED_ERR_ALIGN;
     if (((reinterpret_cast<uintptr_t>(a.inv_freq) | reinterpret_cast<uintptr_t>(a.positions)) & 7u) != 0)
         return STRIPED_ERR_ALIGN;
-    const int64_t nq = a.B * a.H * a.S * a.D * es, nk = a.B * a.Hkv * a.S * a.D * es;
-    if (overlap(a.q_res, nq, a.k_res, nk, false)) return STRIPED_ERR_INVALID_ARG;
-    for (int r = 0; r < 2; ++r) {
-        const void *res = r ? a.k_res : a.q_res;
-        const int64_t n = r ? nk : nq;
-        if (overlap(res, n, a.q, nq, !r) || overlap(res, n, a.k, nk, r) || overlap(res, n, a.dq_out, nq, !r) ||
-            overlap(res, n, a.dk_out, nk, r))
-            return STRIPED_ERR_INVALID_ARG;
-    }
-    return STRIPED_OK;
+    const int64_t nq = a.B * a.H * a.S * a.D * es, nk = a.B * a.Hkv * a.S * a.D * es, nw = a.D * 4;
+    const Range out[5] = {{a.q_res, nq}, {a.k_res, nk}, {a.dq_weight, nw}, {a.dk_weight, nw},
+                          {a.workspace, (int64_t)a.ws_bytes}};
+    const Range in[8] = {{a.q, nq},          {a.k, nk},        {a.dq_out, nq},         {a.dk_out, nk},
+                         {a.q_weight, nw},   {a.k_weight, nw}, {a.inv_freq, a.rot * 4ll},  // rot / 2 of 8 bytes
+                         {a.positions, a.B * a.S * 8}};
+    return results_overlap(out, 5, in, 8, true) ? STRIPED_ERR_INVALID_ARG : STRIPED_OK;
 }
 
 int striped_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out, const float *q_weight,
@@ -732,7 +771,7 @@ int striped_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out,
 
 size_t striped_qk_norm_rope_workspace_size(int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t D, int dtype) {
     if (check_sizes(B, H, S, D, 1) || Hkv < 1 || (dtype != STRIPED_BF16 && dtype != STRIPED_FP32)) return 0;
-    if (D > 256 || D % (dtype == STRIPED_BF16 ? 16 : 8) != 0) return 0;
+    if (D > 256 || D % (dtype == STRIPED_BF16 ? 16 : 8) != 0 || H > kMaxRopeHeads || Hkv > kMaxRopeHeads) return 0;
     return align256(rope_bwd_workspace(B, H, Hkv, S, D, dtype));
 }
 
@@ -746,13 +785,13 @@ int striped_qk_norm_rope_bwd(const void *q, const void *k, const void *dq_out, c
     a.q = q, a.k = k, a.dq_out = dq_out, a.dk_out = dk_out, a.q_res = dq, a.k_res = dk;
     a.q_weight = q_weight, a.k_weight = k_weight, a.inv_freq = inv_freq, a.positions = positions;
     a.dq_weight = dq_weight, a.dk_weight = dk_weight, a.workspace = workspace;
+    a.ws_bytes = striped_qk_norm_rope_workspace_size(B, H, Hkv, S, D, dtype);
     a.B = B, a.H = H, a.Hkv = Hkv, a.S = S, a.D = D;
     a.rot = rotary_dim, a.interleaved = interleaved, a.N = N, a.layout = layout, a.stripe = stripe;
     a.eps = eps, a.dtype = dtype;
     const int st = check_rope(a);
     if (st) return st;
-    if (!workspace || ws_bytes < striped_qk_norm_rope_workspace_size(B, H, Hkv, S, D, dtype))
-        return STRIPED_ERR_WORKSPACE;
+    if (!workspace || ws_bytes < a.ws_bytes) return STRIPED_ERR_WORKSPACE;
     if (!aligned16(workspace)) return STRIPED_ERR_ALIGN;
     return launch_norm_rope(a, (cudaStream_t)stream);
 }

@@ -187,6 +187,7 @@ struct RopeArgs {
     const int64_t *positions;
     float *dq_weight, *dk_weight;
     void *workspace;
+    size_t ws_bytes;
     int64_t B, H, Hkv, S, D;
     int rot, interleaved, N, layout, stripe;
     float eps;

@@ -510,7 +510,7 @@ int launch_norm_rope(const RopeArgs &a, cudaStream_t stream) {
     p.positions = a.positions;
     p.rows = a.B * a.S;
     p.S = a.S;
-    p.L = a.stripe >= 0 ? a.S : a.S / a.N;
+    p.L = a.positions || a.stripe >= 0 ? a.S : a.S / a.N;
     p.D = (int)a.D;
     p.rot = a.rot;
     p.interleaved = a.interleaved;
@@ -522,7 +522,6 @@ int launch_norm_rope(const RopeArgs &a, cudaStream_t stream) {
     p.wc = device_wait_ctl();
     const int tp = rope_tp(a.D, a.dtype);
     const RopeGrid g = rope_grid(a.B, a.S, a.H, a.Hkv, tp, a.dq_out != nullptr);
-    if (g.cq + g.ck > 65535) return STRIPED_ERR_UNSUPPORTED;
     p.hc = g.hc;
     p.t[0].chunks = g.cq;
     p.t[1].chunks = g.ck;

@@ -182,3 +182,14 @@ def test_wrapper_refusals():
         sp.striped_qk_norm_rope(q, q.clone(), w, w, f, N=3)
     with pytest.raises(sp.StripedError):
         sp.striped_qk_norm_rope(q, q.clone(), w, w, f, k_out=q)
+
+
+def test_given_positions_ignore_the_placement():
+    B, H, Hkv, S, D = 1, 2, 1, 6, 64
+    q, k, qw, kw, dq, dk = (t.to(DEV) for t in _make(B, H, Hkv, S, D, torch.bfloat16, 9))
+    f = sp.rope_frequencies(D, 1e4, DEV)
+    pos = torch.arange(S, device=DEV)[None]
+    want = sp.striped_qk_norm_rope(q, k, qw, kw, f) + sp.striped_qk_norm_rope_bwd(q, k, dq, dk, qw, kw, f)
+    odd = dict(N=0, layout=9, stripe=77, positions=pos)
+    got = sp.striped_qk_norm_rope(q, k, qw, kw, f, **odd) + sp.striped_qk_norm_rope_bwd(q, k, dq, dk, qw, kw, f, **odd)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))

@@ -200,3 +200,73 @@ def test_wrapper_refusals():
         sp.striped_attn_window_fwd(q, k, k, 4, 0)
     with pytest.raises(sp.StripedError):
         sp.striped_attn_window_fwd(q, k, k, 4, 10, 1025)
+
+
+@pytest.mark.parametrize("layout,N,D", [(sp.STRIPED, 4, 128), (sp.CONTIGUOUS, 1, 64)])
+def test_padded_rows_do_not_reach_the_real_ones(layout, N, D):
+    """Rows behind the last token of a padded sequence may hold anything
+    finite: the real rows are those of the short sequence, and with dO = 0
+    there the padding's dK and dV are 0."""
+    B, H, Hkv, S, real, W, ns = 1, 2, 1, 512, 300, 70, 2
+    q, k, v, do = _make(B, H, Hkv, real, D, 11)
+    scale = D ** -0.5
+
+    def padded(t, fill):
+        return torch.cat([t, torch.full((B, t.shape[1], S - real, D), fill, dtype=t.dtype)], 2)
+
+    def place(t):
+        t = t.to(DEV)
+        return sp.striped_permute(t, N) if layout == sp.STRIPED else t
+
+    def back(t):
+        return sp.striped_unpermute(t, N) if layout == sp.STRIPED else t
+
+    args = [place(padded(t, fill)) for t, fill in ((q, 300.0), (k, -200.0), (v, 1e30))]
+    o, lse = sp.striped_attn_window_fwd(*args, N, W, ns, layout)
+    r = window_reference(q, k, v, torch.arange(real), W, ns, scale, do, back(o)[:, :, :real].cpu())
+    within(back(o)[:, :, :real], r["o"], r["o_tol"], "o")
+    dq, dk, dv = sp.striped_attn_window_bwd(*args, o, lse, place(padded(do, 0.0)), N, W, ns, layout)
+    for name, t in (("dk", dk), ("dv", dv)):
+        within(back(t)[:, :, :real], r[name], r[name + "_tol"], name)
+        assert not back(t)[:, :, real:].any()
+    within(back(dq)[:, :, :real], r["dq"], r["dq_tol"], "dq")
+    assert sp.check_error() == 0
+
+
+def test_calls_side_by_side():
+    """Two threads on streams of their own: every call has its own workspace,
+    and kernels that share a multiprocessor wait for its tensor memory."""
+    import threading
+
+    jobs = []
+    for D, seed in ((128, 21), (64, 22)):
+        q, k, v, do = (t.to(DEV) for t in _make(1, 4, 2, 1500, D, seed))
+        w, f = torch.ones(D, device=DEV), sp.rope_frequencies(D, 1e4, DEV)
+        kt, vt = (t[:, :, :200].expand(3, -1, -1, -1).contiguous() for t in (k, v))
+        lens = torch.tensor([1, 77, 200], dtype=torch.int32, device=DEV)
+        new = q[:, :, :1].expand(3, -1, -1, -1).contiguous()
+
+        def run(q=q, k=k, v=v, do=do, w=w, f=f, kt=kt, vt=vt, lens=lens, new=new):
+            a, b = sp.striped_qk_norm_rope(q, k, w, w, f, 4)
+            o, lse = sp.striped_attn_window_fwd(a, b, v, 4, 200, 2)
+            _, dk, dv = sp.striped_attn_window_bwd(a, b, v, o, lse, do, 4, 200, 2)
+            g = sp.striped_qk_norm_rope_bwd(q, k, o, dk, w, w, f, 4)
+            return (a, b, o, lse, dk, dv) + g + sp.striped_attn_decode(new, b, v, kt, vt, lens, 4)
+
+        jobs.append((run, run()))
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(run, want):
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            got = [run() for _ in range(10)]
+        side.synchronize()
+        bad.extend(i for g in got for i, (x, y) in enumerate(zip(g, want)) if not torch.equal(x, y))
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad and sp.check_error() == 0

@@ -217,3 +217,72 @@ def test_decode_workspace_size():
     assert size(4, 3, 4, 2, 1, 256, 16, 64, 4, 0, 0, 0, 0) == 0
     assert size(4, 2, 4, 2, 1, 256, 16, 64, 4, 0, 1, 0, 0) == 0
     assert size(4, 1, 4, 2, 1, 0, 16, 64, 4, 0, 0, 0, 0) > 0  # no prompt: N and layout are not looked at
+
+
+# ------------------------------------------------------------------ scales, overlapping buffers, ignored arguments
+BAD_SCALES = [0.0, -0.1, float("nan"), float("inf"), 1e-40, 2e38]
+
+
+@pytest.mark.parametrize("scale", BAD_SCALES)
+def test_scale_refusals(scale):
+    lib, s = sp.load(), ctypes.c_float(scale)
+    assert lib.striped_attn_window_fwd(*A[:5], 1, 4, 2, 256, 64, 4, 0, 0, 10, 0, s, None) == INVALID
+    assert lib.striped_attn_window_bwd(*A[:10], 1 << 40, 1, 4, 2, 256, 64, 4, 0, 0, 10, 0, s, None) == INVALID
+    assert lib.striped_attn_decode(*A[:9], 1 << 40, 4, 2, 4, 2, 1, 256, 16, 64, 4, 0, 0, 0, 0, s, None) == INVALID
+
+
+# results and the workspace over every other tensor, at the last byte of it or of themselves
+Q, KV, LSE = 4 * 256 * 64 * 2, 2 * 256 * 64 * 2, 4 * 256 * 4  # bytes at B 1, H 4, Hkv 2, S 256, D 64
+
+
+@pytest.mark.parametrize("res,at", [
+    (3, A[0]), (3, A[1]), (3, A[2] + KV - 16), (3, A[0] - Q + 16), (3, A[4] - Q + 16), (4, A[0] + 32),
+    (4, A[1] + KV - 16), (4, A[2] - LSE + 16)])
+def test_window_overlap_refusals(res, at):
+    a = A[:5]
+    a[res] = at
+    assert sp.load().striped_attn_window_fwd(*a, 1, 4, 2, 256, 64, 4, 0, 0, 10, 0, ctypes.c_float(0.1),
+                                             None) == INVALID
+
+
+@pytest.mark.parametrize("res,at", [
+    (6, A[0]), (6, A[5]), (6, A[7]), (7, A[1]), (7, A[8] + KV - 16), (8, A[2]), (8, A[4]), (8, A[3] - KV + 16),
+    (9, A[0]), (9, A[6]), (9, A[8] + KV - 256)])
+def test_window_backward_overlap_refusals(res, at):
+    a = A[:10]
+    a[res] = at
+    assert sp.load().striped_attn_window_bwd(*a, 1 << 40, 1, 4, 2, 256, 64, 4, 0, 0, 10, 4, ctypes.c_float(0.1),
+                                             None) == INVALID
+
+
+@pytest.mark.parametrize("kw", [
+    dict(o=A[0]), dict(o=A[1]), dict(o=A[5] - 16), dict(lse=A[3]), dict(lse=A[6] + 16), dict(ws=A[4]), dict(ws=A[7]),
+    dict(vt=A[8])])
+def test_decode_overlap_refusals(kw):
+    assert _decode(sp.load(), **kw) == INVALID
+
+
+def test_norm_rope_overlap_refusals():
+    lib = sp.load()
+    assert _rope(lib, yq=A[4]) == INVALID and _rope(lib, yk=A[5]) == INVALID and _rope(lib, pos=A[2]) == INVALID
+    need = lib.striped_qk_norm_rope_workspace_size(1, 4, 2, 64, 64, 0)
+
+    def call(dq=A[6], dw=A[8], ws=A[12]):
+        return lib.striped_qk_norm_rope_bwd(A[0], A[1], A[2], A[3], dq, A[7], dw, A[9], A[10], A[11], A[13], None, ws,
+                                            need, 1, 4, 2, 64, 64, 64, 0, 4, 0, -1, ctypes.c_float(1e-6), 0, None)
+
+    assert call(dq=A[1]) == INVALID and call(dq=A[3]) == INVALID and call(dq=A[9]) == INVALID
+    assert call(dw=A[9] + 252) == INVALID and call(dw=A[10]) == INVALID and call(dw=A[0]) == INVALID
+    assert call(ws=A[0]) == INVALID and call(ws=A[9]) == INVALID and call(ws=A[13]) == INVALID
+
+
+def test_sizes_that_no_gpu_holds():
+    """Byte counts past 64 bits, and heads past the grid."""
+    lib = sp.load()
+    assert _window(lib, B=2 ** 20, H=2 ** 11, Hkv=2 ** 11, S=2 ** 30) == UNSUPPORTED
+    assert lib.striped_attn_window_workspace_size(2 ** 20, 2 ** 11, 2 ** 11, 2 ** 30, 64, 4, 0, 0, 10, 4) == 0
+    assert _decode(lib, B=1, Bp=1, H=2 ** 30, Hkv=2 ** 30, P=2 ** 30) == UNSUPPORTED
+    assert _decode(lib, P=2 ** 30, C=2 ** 30 - 256, T=1) == UNSUPPORTED
+    assert _rope(lib, H=65537) == UNSUPPORTED and _rope(lib, Hkv=65537) == UNSUPPORTED
+    assert lib.striped_qk_norm_rope_workspace_size(1, 65537, 2, 64, 64, 0) == 0
+    assert _rope(lib, B=2 ** 15, H=2 ** 16, S=2 ** 31) == UNSUPPORTED
