@@ -217,3 +217,29 @@ def test_wrapper_refusals():
     with pytest.raises(sp.StripedError):
         sp.striped_attn_decode(q, kp, vp, kt, vt, lens, 4,
                                workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
+
+
+@pytest.fixture
+def emptied_cache():
+    """The memory of a large test goes back to the device."""
+    yield
+    torch.cuda.empty_cache()
+
+
+def test_offsets_past_32_bits(emptied_cache):
+    """More than 2^31 elements of prompt and of tails: the last key/value head
+    of the last request is what it is alone."""
+    B, H, Hkv, P, C, D, N = 2, 64, 32, 1 << 20, 1 << 19, 128, 8
+    g = torch.Generator(device=DEV).manual_seed(6)
+    mk = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device=DEV).normal_(generator=g)  # noqa: E731
+    q, kp, vp, kt, vt = mk(B, H, 1, D), mk(1, Hkv, P, D), mk(1, Hkv, P, D), mk(B, Hkv, C, D), mk(B, Hkv, C, D)
+    lens = torch.tensor([5, C], dtype=torch.int32, device=DEV)
+    last = [q[1:, -2:], kp[:, -1:], vp[:, -1:], kt[1:, -1:], vt[1:, -1:], lens[1:]]
+    last = [t.contiguous() for t in last]
+    for W, ns in ((0, 0), (C + 1000, 9)):
+        o, lse = sp.striped_attn_decode(q, kp, vp, kt, vt, lens, N, sp.STRIPED, W, ns)
+        o1, lse1 = sp.striped_attn_decode(*last, N, sp.STRIPED, W, ns)
+        # cut into other segments: their sums are rounded in another order
+        assert float((lse[1:, -2:] - lse1).abs().max()) <= LSE_TOL
+        assert float((o[1:, -2:].float() - o1.float()).abs().max()) <= 2.0 ** -7 * float(o1.float().abs().max())
+    assert sp.check_error() == 0

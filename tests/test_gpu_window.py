@@ -270,3 +270,36 @@ def test_calls_side_by_side():
     for t in threads:
         t.join()
     assert not bad and sp.check_error() == 0
+
+
+@pytest.fixture
+def emptied_cache():
+    """The memory of a large test goes back to the device."""
+    yield
+    torch.cuda.empty_cache()
+
+
+def test_offsets_past_32_bits(emptied_cache):
+    """More than 2^31 elements a tensor: the last head is what it is alone."""
+    S, D, N, W, ns = 1 << 19, 128, 8, 100, 3
+    H = (1 << 31) // (S * D) + 1
+    g = torch.Generator(device=DEV).manual_seed(5)
+    q, k, v, do = (torch.empty(1, H, S, D, dtype=torch.bfloat16, device=DEV).normal_(generator=g) for _ in range(4))
+    w, f = torch.ones(D, device=DEV), sp.rope_frequencies(D, 1e4, DEV)
+    one = [t[:, -1:].contiguous() for t in (q, k, v, do)]
+    a, b = sp.striped_qk_norm_rope(q, k, w, w, f, N)
+    a1, b1 = sp.striped_qk_norm_rope(one[0], one[1], w, w, f, N)
+    assert torch.equal(a[:, -1:], a1) and torch.equal(b[:, -1:], b1)
+    o, lse = sp.striped_attn_window_fwd(a, b, v, N, W, ns)
+    o1, lse1 = sp.striped_attn_window_fwd(a1, b1, one[2], N, W, ns)
+    assert torch.equal(o[:, -1:], o1) and torch.equal(lse[:, -1:], lse1)
+    grads = sp.striped_attn_window_bwd(a, b, v, o, lse, do, N, W, ns)
+    grads1 = sp.striped_attn_window_bwd(a1, b1, one[2], o1, lse1, one[3], N, W, ns)
+    assert torch.equal(grads[1][:, -1:], grads1[1]) and torch.equal(grads[2][:, -1:], grads1[2])
+    # dQ is summed by atomics: a bf16 rounding apart at most
+    off = (grads[0][:, -1:].float() - grads1[0].float()).abs().max()
+    assert float(off) <= 2.0 ** -7 * float(grads1[0].float().abs().max())
+    dx = sp.striped_qk_norm_rope_bwd(q, k, grads[1], grads[2], w, w, f, N)
+    dx1 = sp.striped_qk_norm_rope_bwd(one[0], one[1], grads1[1], grads1[2], w, w, f, N)
+    assert torch.equal(dx[0][:, -1:], dx1[0]) and torch.equal(dx[1][:, -1:], dx1[1])
+    assert sp.check_error() == 0
