@@ -474,9 +474,9 @@ __global__ void __launch_bounds__(kDThreads, 1)
                     }
                     float mx8[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) mx8[i] = sv[i];
+                    for (int i = 0; i < 8; ++i) mx8[i] = fmaxf(sv[i], sv[8 + i]);
 #pragma unroll
-                    for (int c = 8; c < DT; c += 16)
+                    for (int c = 16; c < DT; c += 16)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) mx8[i] = fmax3(mx8[i], sv[c + i], sv[c + 8 + i]);
                     const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),

@@ -318,9 +318,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // latency)
                 float mx8[8];
 #pragma unroll
-                for (int t = 0; t < 8; ++t) mx8[t] = sv[t];
+                for (int t = 0; t < 8; ++t) mx8[t] = fmaxf(sv[t], sv[8 + t]);
 #pragma unroll
-                for (int c = 8; c < BN; c += 16)
+                for (int c = 16; c < BN; c += 16)
 #pragma unroll
                     for (int t = 0; t < 8; ++t) mx8[t] = fmax3(mx8[t], sv[c + t], sv[c + 8 + t]);
                 const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
