@@ -24,8 +24,12 @@
 //
 // The main kernel has the pipeline of the full attention's backward: warp 0 =
 // TMA producer (K, V once; then Q_i with its statistics, 2 stages), warp 2 =
-// TMA producer of dO_i, warp 1 = TMEM allocator + MMA issuer, warps 4..11 =
-// two compute warpgroups; thread t owns key row t of S^T and dP^T.
+// TMA producer of dO_i, warp 1 = TMEM allocator + MMA issuer (the whole warp
+// waits, one elected lane issues), warps 4..11 = two compute warpgroups; thread
+// t owns key row t of S^T and dP^T.  Warps 12..15 only carry dQ_i from tensor
+// memory to the accumulator, so that the compute warps go on to the next tile;
+// the accumulator is laid out so that a warp's 16-byte reductions are whole
+// lines.
 //   TMEM: S^T [0,128) (P^T bf16 pairs over it), dP^T [128,256) (dQ_i over it
 //   once dS_i is formed), dV [256,256+HD), dK [256+HD,256+2HD).
 //     S^T  = K Q_i^T      SS, both K-major
@@ -38,6 +42,13 @@
 // The accumulator holds whole tiles, so every reduction is unconditional;
 // its order, and with it the last bits of dQ, change from run to run (a few
 // fp32 ulps before the rounding to bf16), dK and dV do not.
+//
+// Bound by the hand-offs and the L2's fp32 reductions (64 KB a tile): tensor
+// pipe 44% active; without the reductions the main kernel would take 0.8 of
+// its time.  Measured (H = 32 + 8, S = 32768, D = 128, window 2048, 16 sinks,
+// zig-zag): 3.09 ms, 870 TFLOP/s of kept pairs, 2.9 us a 128 x 128 tile of one
+// multiprocessor (the full attention's backward: 3.05).  The four kernels
+// follow one another by programmatic launches: 8 us less a call.
 #include <math.h>
 
 #include "common.cuh"

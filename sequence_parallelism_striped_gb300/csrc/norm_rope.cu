@@ -431,6 +431,12 @@ __global__ void __launch_bounds__(256)
 // four rounds of shorter blocks, whose ends overlap (201 us; at S = 8192 they
 // cost 5 us in set-up).  The block count depends on the sizes only, so the
 // backward's shares, and with them dw, do not depend on the device.
+//
+// Rows are streamed through shared memory by bulk copies when a sequence fills
+// at least one block's rows; shorter ones (decoding: one row a request) are
+// read by the threads themselves (64 requests of one token, 40 heads: 2.9 us,
+// streamed 5.8; S = 65536: 246 us forward and 394 backward, streamed 202 and
+// 300).
 struct RopeGrid {
     bool stream;
     int hc, cq, ck, gx;
