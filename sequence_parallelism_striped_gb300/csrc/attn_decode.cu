@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
             const int base_pos = tail ? p.P : 0;                  // position of key 0
             const int qpos = p.P + len - p.T + t - base_pos;      // relative to it, like hi, lo and sk
             const int hi = min(qpos, (tail ? len : p.P) - 1);
-            const int lo = p.W == 0 ? -0x40000000 : qpos - p.W + 1;
+            const int lo = p.W == 0 ? 0 : qpos - p.W + 1;
             const int sk = p.sinks - base_pos;
             if (warp_on) {
                 // Q row -> TMEM as bf16 pairs: the A operand of S = Q K^T.
