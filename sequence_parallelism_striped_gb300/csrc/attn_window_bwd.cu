@@ -95,6 +95,27 @@ struct WinBwdParams {
     WaitCtl wc;  // status word, wait bound, test hook
 };
 
+// mbar_wait and mbar_wait_warp with one place that tries (B = 1, H = 8,
+// S = 8192, window 1024: 158 us with the tries unrolled at every place that
+// waits, 155 with them in a loop of their own, 152 so).
+__device__ __forceinline__ bool bwd_wait(uint32_t bar, uint32_t parity, const WaitCtl &w) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 0u) {
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            else if (now - t0 > w.limit_ns) break;
+        }
+    }
+    record_timeout(w);
+    return false;
+}
+__device__ __forceinline__ bool bwd_wait_warp(uint32_t bar, uint32_t parity, const WaitCtl &w) {
+    return __all_sync(0xffffffffu, bwd_wait(bar, parity, w));
+}
+
 struct Bars {
     uint64_t kv_full;
     uint64_t q_full[QS], q_empty[QS];    // Q_i + statistics of tile i
@@ -216,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int i = 0;
             for (; i < nt; ++i) {
                 const int s = i % QS;
-                if (i >= QS && !mbar_wait(smem_u32(&bars->q_empty[s]), ((i / QS) + 1) & 1, p.wc)) break;
+                if (i >= QS && !bwd_wait(smem_u32(&bars->q_empty[s]), ((i / QS) + 1) & 1, p.wc)) break;
                 if (skip_first && i == 0) continue;
                 const uint32_t fb = smem_u32(&bars->q_full[s]);
                 const uint32_t qdst = sbase + kQOff + s * 2 * kTile;
@@ -231,9 +252,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // K, V and loads [0, i) were issued: wait (bounded) for the last of
             // each stage, so that on an error path none lands after the CTA exits
-            mbar_wait(kb, 0, p.wc);
+            bwd_wait(kb, 0, p.wc);
             for (int t = i > QS ? i - QS : 0; t < i; ++t)
-                if (!(skip_first && t == 0)) mbar_wait(smem_u32(&bars->q_full[t % QS]), (t / QS) & 1, p.wc);
+                if (!(skip_first && t == 0)) bwd_wait(smem_u32(&bars->q_full[t % QS]), (t / QS) & 1, p.wc);
         } else if (warp == 2 && lane == 0 && nt > 0) {
             // ---------------- TMA producer: dO_i (its own stream: the buffer is
             // released at dV_i, or at HD 64 after the dQ_i half staged in it is read)
@@ -241,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int i = 0;
             for (; i < nt; ++i) {
                 const int s = i % QS;
-                if (i >= QS && !mbar_wait(smem_u32(&bars->do_empty[s]), ((i / QS) + 1) & 1, p.wc)) break;
+                if (i >= QS && !bwd_wait(smem_u32(&bars->do_empty[s]), ((i / QS) + 1) & 1, p.wc)) break;
                 const uint32_t fb = smem_u32(&bars->do_full[s]);
                 const uint32_t odst = sbase + kQOff + s * 2 * kTile + kTile;
                 const int bq = (int)(bh * G) + i / cnt;
@@ -252,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_4d(odst + x * kBox, &tmdO, fb, 64 * x, at.c1, at.c2, bq);
             }
             for (int t = i > QS ? i - QS : 0; t < i; ++t)  // in-flight loads, as above
-                mbar_wait(smem_u32(&bars->do_full[t % QS]), (t / QS) & 1, p.wc);
+                bwd_wait(smem_u32(&bars->do_full[t % QS]), (t / QS) & 1, p.wc);
         } else if (warp == 1 && nt > 0) {
             // ---------------- MMA issuer (the whole warp, one lane issues)
             // Per query tile i (TMEM: S = S^T then P^T; DP = dP^T then dQ_i):
@@ -276,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto along_k = [](int kk) -> uint32_t { return ((kk >> 2) * kBox + (kk & 3) * 32) >> 4; };
             auto issue_s = [&](int t) -> bool {
                 const int s = t % QS;
-                if (!mbar_wait_warp(smem_u32(&bars->q_full[s]), (t / QS) & 1, p.wc)) return false;
+                if (!bwd_wait_warp(smem_u32(&bars->q_full[s]), (t / QS) & 1, p.wc)) return false;
                 tc_fence_after();
                 if (leader) {
 #pragma unroll
@@ -288,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             auto issue_dp = [&](int t) -> bool {
                 const int s = t % QS;
-                if (!mbar_wait_warp(smem_u32(&bars->do_full[s]), (t / QS) & 1, p.wc)) return false;
+                if (!bwd_wait_warp(smem_u32(&bars->do_full[s]), (t / QS) & 1, p.wc)) return false;
                 tc_fence_after();
                 if (leader) {
 #pragma unroll
@@ -298,13 +319,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 return true;
             };
-            bool ok = mbar_wait_warp(smem_u32(&bars->kv_full), 0, p.wc) && issue_s(0);
+            bool ok = bwd_wait_warp(smem_u32(&bars->kv_full), 0, p.wc) && issue_s(0);
             if (ok) ok = issue_dp(0);
             for (int i = 0; i < nt && ok; ++i) {
                 const int s = i % QS;
                 // dV += P^T dO: P^T (bf16 pairs) in TMEM columns [0,32) for
                 // queries 0..63 and [64,96) for queries 64..127
-                if (!mbar_wait_warp(smem_u32(&bars->p_ready), i & 1, p.wc)) break;
+                if (!bwd_wait_warp(smem_u32(&bars->p_ready), i & 1, p.wc)) break;
                 tc_fence_after();
                 if (leader) {
 #pragma unroll
@@ -316,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (i + 1 < nt && !issue_s(i + 1)) break;
                 // dK += dS^T Q (A = dS^T, K-major view of the dS smem tile)
-                if (!mbar_wait_warp(smem_u32(&bars->ds_ready), i & 1, p.wc)) break;
+                if (!bwd_wait_warp(smem_u32(&bars->ds_ready), i & 1, p.wc)) break;
                 tc_fence_after();
                 if (leader) {
 #pragma unroll
@@ -341,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma_commit(smem_u32(&bars->dq_full));
                 }
                 if (i + 1 < nt) {
-                    if (!mbar_wait_warp(smem_u32(&bars->dq_free), i & 1, p.wc)) break;
+                    if (!bwd_wait_warp(smem_u32(&bars->dq_free), i & 1, p.wc)) break;
                     tc_fence_after();
                     if (!issue_dp(i + 1)) break;
                 }
@@ -349,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && leader) mma_commit(smem_u32(&bars->acc_done));
             // every MMA issued above completes before TMEM is freed (error paths)
             if (leader) mma_commit(smem_u32(&bars->drain));
-            mbar_wait_warp(smem_u32(&bars->drain), 0, p.wc);
+            bwd_wait_warp(smem_u32(&bars->drain), 0, p.wc);
         }
     } else if (warp < 12) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
@@ -379,8 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // bf16 into TMEM as the A operand of dV += P^T dO
         uint32_t P[2][32];
         auto compute_p = [&](int i) -> bool {
-            if (!mbar_wait(smem_u32(&bars->q_full[i % QS]), (i / QS) & 1, p.wc)) return false;
-            if (!mbar_wait(smem_u32(&bars->s_full), i & 1, p.wc)) return false;
+            if (!bwd_wait(smem_u32(&bars->q_full[i % QS]), (i / QS) & 1, p.wc)) return false;
+            if (!bwd_wait(smem_u32(&bars->s_full), i & 1, p.wc)) return false;
             tc_fence_after();
             const float *sL = stat_ptr(i);
             // keep (query, key) iff key <= query <= key + W - 1, or any later
@@ -432,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) ok = compute_p(0);
         for (int i = 0; i < nt && ok; ++i) {
             // ---- dS = P * (dP - Delta) -> smem (A operand of dQ and dK)
-            if (!mbar_wait(smem_u32(&bars->dp_full), i & 1, p.wc)) {
+            if (!bwd_wait(smem_u32(&bars->dp_full), i & 1, p.wc)) {
                 ok = false;
                 break;
             }
@@ -471,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i + 1 < nt && !compute_p(i + 1)) ok = false;
         }
         if (ok) {
-            ok = mbar_wait(smem_u32(&bars->acc_done), 0, p.wc);
+            ok = bwd_wait(smem_u32(&bars->acc_done), 0, p.wc);
             tc_fence_after();
         }
         // ---------------- epilogue: this warpgroup's columns of dK, dV
@@ -529,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // column = query; HD = 64: lane = query, column = dimension.
         constexpr int kCols = HD == 128 ? BT : HD;
         for (int i = 0; i < nt; ++i) {
-            if (!mbar_wait(smem_u32(&bars->dq_full), i & 1, p.wc)) break;
+            if (!bwd_wait(smem_u32(&bars->dq_full), i & 1, p.wc)) break;
             tc_fence_after();
             uint32_t q[kCols / 32][32];
 #pragma unroll

@@ -227,11 +227,8 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Wait for the phase of parity `parity` to complete; false (and the device
-// status set to STRIPED_ERR_TIMEOUT) if the bound runs out.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const WaitCtl &w) {
-    for (int it = 0; it < 64; ++it)
-        if (mbar_try_wait(bar, parity)) return true;
+// Tries until the time limit, then records the timeout and returns false.
+__device__ __forceinline__ bool mbar_wait_timed(uint32_t bar, uint32_t parity, const WaitCtl &w) {
     const uint64_t t0 = global_timer_ns();
     for (uint32_t it = 0;; ++it) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -239,6 +236,14 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const W
     }
     record_timeout(w);
     return false;
+}
+
+// Wait for the phase of parity `parity` to complete; false (and the device
+// status set to STRIPED_ERR_TIMEOUT) if the bound runs out.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const WaitCtl &w) {
+    for (int it = 0; it < 64; ++it)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait_timed(bar, parity, w);
 }
 
 // --------------------------------------------------------------------------
