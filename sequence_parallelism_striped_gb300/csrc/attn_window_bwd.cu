@@ -46,7 +46,7 @@
 // Bound by the hand-offs and the L2's fp32 reductions (64 KB a tile): tensor
 // pipe 44% active; without the reductions the main kernel would take 0.8 of
 // its time.  Measured (H = 32 + 8, S = 32768, D = 128, window 2048, 16 sinks,
-// zig-zag): 3.09 ms, 870 TFLOP/s of kept pairs, 2.9 us a 128 x 128 tile of one
+// zig-zag): 3.05 ms, 880 TFLOP/s of kept pairs, 2.9 us a 128 x 128 tile of one
 // multiprocessor (the full attention's backward: 3.05).  The four kernels
 // follow one another by programmatic launches: 8 us less a call.
 #include <math.h>

@@ -34,13 +34,13 @@
 // a warp skips the 32-column words that all its rows keep whole.
 //
 // Bound by the chain S -> softmax -> P -> O of a query tile: the tensor pipe is
-// 51% active, DRAM 17%.  Measured (H = 32 + 8, S = 65536, D = 128, N = 8): a
-// 128 x 128 tile takes 0.83 us of a multiprocessor at a window of 16384, the
-// pace of the full attention's two-tile kernel; an item's ends cost 3.8 us, so
-// it is 1.03 us at a window of 1024.  With 4 sinks, whose tile is one of the
-// ten that a query tile issues for eight kept: 1120 us, 980 TFLOP/s of kept
-// pairs.  Slower, same case: 32-column products for the sink tile (1142), two
-// issuing warps, two threads a row, the maximum off the chain.
+// 52% active, DRAM 17%.  Measured (H = 32 + 8, S = 65536, D = 128, N = 8): a
+// 128 x 128 tile takes 0.77 us of a multiprocessor at a window of 16384, 1.00
+// us at 1024, where an item's ends (its first S, its last O) are 20% of it.
+// With 4 sinks, whose tile is one of the ten that a query tile issues for
+// eight kept: 1085 us, 1010 TFLOP/s of kept pairs.  Slower: 32-column products
+// for the sink tile, K and V in places of their own, two issuing warps, two
+// threads a row, the maximum off the chain.
 #include <math.h>
 
 #include "common.cuh"

@@ -243,3 +243,23 @@ def test_offsets_past_32_bits(emptied_cache):
         assert float((lse[1:, -2:] - lse1).abs().max()) <= LSE_TOL
         assert float((o[1:, -2:].float() - o1.float()).abs().max()) <= 2.0 ** -7 * float(o1.float().abs().max())
     assert sp.check_error() == 0
+
+
+ROW_TILES = [
+    # more than 128 rows on a prompt: layout, B, Bp, H, Hkv, T, P, C, D, N, window, sinks
+    (sp.STRIPED, 40, 1, 8, 1, 1, 8192, 20, 64, 8, 0, 0),      # 320 rows
+    (sp.STRIPED, 20, 2, 8, 1, 5, 2048, 20, 128, 4, 0, 0),     # 400 rows on each of two prompts
+    (sp.STRIPED, 33, 1, 16, 2, 1, 6000, 1, 128, 3, 0, 0),     # 264 rows, tails of one row
+    (sp.ZIGZAG, 64, 1, 8, 2, 1, 12288, 30, 128, 4, 6000, 5),  # 256 rows, a window
+    (sp.STRIPED, 10, 1, 8, 1, 13, 4096, 100, 64, 8, 0, 0),    # 1040 rows: nine row tiles
+]
+
+
+@pytest.mark.parametrize("layout,B,Bp,H,Hkv,T,P,C,D,N,W,ns", ROW_TILES)
+def test_several_row_tiles(layout, B, Bp, H, Hkv, T, P, C, D, N, W, ns):
+    q, kp, vp, kt, vt, lens = _make(B, Bp, H, Hkv, T, P, C, D, None, 8)
+    o, lse, tol = _reference(q, kp, vp, kt, vt, lens, positions(P, N, layout), W, ns, D ** -0.5)
+    go, gl = sp.striped_attn_decode(*_gpu(q, kp, vp, kt, vt, lens), N, layout, W, ns)
+    assert sp.check_error() == 0
+    within(gl, lse, LSE_TOL, "lse")
+    within(go, o, tol, "o")
