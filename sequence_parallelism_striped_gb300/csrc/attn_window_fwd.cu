@@ -73,16 +73,24 @@ struct WinCfg {
 // mbar_wait and mbar_wait_warp in little code: the tries are not unrolled at
 // every place that waits, and a warp's first one ends in a uniform branch
 // (S = 65536, window 1024, 4 sinks: 1112 us unrolled, 1075 with the uniform
-// first try, 1063 with both; window 16384: 9.95, 9.51 and 9.27 ms).
+// first try, 1063 with both; window 16384: 9.95, 9.51 and 9.27 ms).  At HD =
+// 64 the timed tries are a function of their own (S = 4096, H = 8: 26.8 us
+// inlined, 25.4 so; at HD = 128 1068 us inlined, 1116 so).
+__device__ __noinline__ bool win_wait_timed(uint32_t bar, uint32_t parity, const WaitCtl w) {
+    return mbar_wait_timed(bar, parity, w);
+}
+template <int HD>
 __device__ __forceinline__ bool win_wait(uint32_t bar, uint32_t parity, const WaitCtl &w) {
 #pragma unroll 1
     for (int it = 0; it < 64; ++it)
         if (mbar_try_wait(bar, parity)) return true;
+    if constexpr (HD == 64) return win_wait_timed(bar, parity, w);
     return mbar_wait_timed(bar, parity, w);
 }
+template <int HD>
 __device__ __forceinline__ bool win_wait_warp(uint32_t bar, uint32_t parity, const WaitCtl &w) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    return __all_sync(0xffffffffu, win_wait(bar, parity, w));
+    return __all_sync(0xffffffffu, win_wait<HD>(bar, parity, w));
 }
 
 struct WinBars {
@@ -195,7 +203,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
             const WinItem w(p, item);
             const int kvh = (int)(w.bh / p.G);
-            if (last_q >= 0 && !win_wait(smem_u32(&bars->q_empty), last_q & 1, p.wc)) break;
+            if (last_q >= 0 && !win_wait<HD>(smem_u32(&bars->q_empty), last_q & 1, p.wc)) break;
             ++last_q;
             mbar_arrive_expect_tx(qbar, (w.has_b ? 2 : 1) * kBoxes * box_bytes);
             for (int x = 0; x < (w.has_b ? 2 : 1); ++x) {
@@ -207,7 +215,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
             }
             for (int t = 0; t < w.nt; ++t, ++j) {
                 const int s = j % NS;
-                if (j >= NS && !win_wait(smem_u32(&bars->kv_empty[s]), ((j / NS) + 1) & 1, p.wc)) {
+                if (j >= NS && !win_wait<HD>(smem_u32(&bars->kv_empty[s]), ((j / NS) + 1) & 1, p.wc)) {
                     ok = false;
                     break;
                 }
@@ -226,9 +234,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
         // loads [0, j) and the last Q were issued: wait (bounded) for the last
         // of each stage, so that on an error path none lands after the CTA has
         // exited
-        if (last_q >= 0) win_wait(qbar, last_q & 1, p.wc);
+        if (last_q >= 0) win_wait<HD>(qbar, last_q & 1, p.wc);
         for (int t = j > NS ? j - NS : 0; t < j; ++t)
-            if (!(skip_first && t == 0)) win_wait(smem_u32(&bars->kv_full[t % NS]), (t / NS) & 1, p.wc);
+            if (!(skip_first && t == 0)) win_wait<HD>(smem_u32(&bars->kv_full[t % NS]), (t / NS) & 1, p.wc);
     } else if (warp == 1) {
         // ---------------- MMA issuer: PV_A(t), S_A(next), PV_B(t), S_B(next)
         constexpr uint32_t idesc_qk = idesc_bf16_f32(WB, WB, false, false);
@@ -247,7 +255,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         int seen = -1;  // last tile whose K and V were waited for
         auto issue_s = [&](int x, int j) -> bool {
             const int s = j % NS;
-            if (j > seen && !win_wait_warp(smem_u32(&bars->kv_full[s]), (j / NS) & 1, p.wc)) return false;
+            if (j > seen && !win_wait_warp<HD>(smem_u32(&bars->kv_full[s]), (j / NS) & 1, p.wc)) return false;
             seen = max(seen, j);
             tc_fence_after();
             if (leader) {
@@ -266,7 +274,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
             const uint64_t vs = dv + (j % NS) * (kStage >> 4);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                if (!win_wait_warp(smem_u32(&bars->p_ready[x][h]), n[x] & 1, p.wc)) return false;
+                if (!win_wait_warp<HD>(smem_u32(&bars->p_ready[x][h]), n[x] & 1, p.wc)) return false;
                 tc_fence_after();
                 if (leader) {
 #pragma unroll
@@ -287,7 +295,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
             const bool more = item + (int)gridDim.x < p.items;
             const int skip = w.skip(p), last_a = w.last(0);
             const int first_b = w.first(1, skip);
-            ok = win_wait_warp(smem_u32(&bars->q_full), it & 1, p.wc);
+            ok = win_wait_warp<HD>(smem_u32(&bars->q_full), it & 1, p.wc);
             tc_fence_after();
             if (ok) ok = issue_s(0, jbase);
             if (ok && w.has_b) ok = issue_s(1, jbase + first_b);
@@ -313,7 +321,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         }
         // every MMA issued above completes before TMEM is freed (error paths)
         if (leader) mma_commit(smem_u32(&bars->drain));
-        win_wait_warp(smem_u32(&bars->drain), 0, p.wc);
+        win_wait_warp<HD>(smem_u32(&bars->drain), 0, p.wc);
     } else if (warp >= 2) {
         // ---------------- softmax + epilogue of one query tile
         const int x = (warp - 2) >> 2;       // group: query tile qa or qa + 1
@@ -331,7 +339,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
             float m_ref = -INFINITY, l = 0.f;
             bool first = true;
             for (int kt = ns > 0 ? 0 : lo; kt <= qt; kt = kt + 1 == ns ? lo : kt + 1) {
-                if (!win_wait(smem_u32(&bars->s_full[x]), n & 1, p.wc)) {
+                if (!win_wait<HD>(smem_u32(&bars->s_full[x]), n & 1, p.wc)) {
                     ok = false;
                     break;
                 }
@@ -422,7 +430,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
                 first = false;
             }
             // ---------------- epilogue
-            if (ok) ok = win_wait(smem_u32(&bars->o_done[x]), m++ & 1, p.wc);
+            if (ok) ok = win_wait<HD>(smem_u32(&bars->o_done[x]), m++ & 1, p.wc);
             tc_fence_after();
             const bool valid = tile_has(g, qt, ri);
             const bool empty = !(l > 0.f) || !ok;
