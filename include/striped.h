@@ -409,8 +409,8 @@ size_t striped_attn_decode_workspace_size(int64_t B, int64_t Bp, int64_t H, int6
  * interleaved != 0, j < rotary_dim/2; elements from rotary_dim on are not
  * rotated (rotary_dim = 0: norm only, inv_freq may be NULL).  Angles are
  * reduced in 64 bits, so they stay exact at far positions (inv_freq finite).
- * Squares and their sums are fp32: |x| below 1e18, and eps > 0 wherever a row
- * may be all 0.
+ * Squares and their sums are fp32: |x| below 1e18, and eps > 0 wherever a
+ * row's root mean square may be below 1e-18 (an all-0 row among them).
  *  q, q_out: [B,H,S,D], k, k_out: [B,Hkv,S,D] `dtype`; H and Hkv are any
  *            counts up to 65536.  q_out may be q and k_out may be k (in place); any
  *            other overlap of a result with another tensor is
@@ -438,7 +438,9 @@ size_t striped_qk_norm_rope_workspace_size(int64_t B, int64_t H, int64_t Hkv, in
  * dq_out and dk_out the cotangents of its outputs.  With g the cotangent
  * turned back by the row's angle and h = g * weight,
  *     d_weight = sum over all rows and heads of g * n   (fp32 [D]),
- *     dx = r h - x r^3 mean(h x),  r = 1 / sqrt(mean(x^2) + eps).
+ *     dx = r (h - n mean(h n)),  r = 1 / sqrt(mean(x^2) + eps).
+ * Sums are fp32: beside the forward's bounds, the sum of |h x| over a row is
+ * below 3e38.
  * dq may be q or dq_out, dk may be k or dk_out (in place).  Sums in a fixed
  * order: results are the same from run to run.  workspace: 16-byte aligned,
  * >= striped_qk_norm_rope_workspace_size() bytes, its contents are ignored;

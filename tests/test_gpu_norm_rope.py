@@ -193,3 +193,24 @@ def test_given_positions_ignore_the_placement():
     odd = dict(N=0, layout=9, stripe=77, positions=pos)
     got = sp.striped_qk_norm_rope(q, k, qw, kw, f, **odd) + sp.striped_qk_norm_rope_bwd(q, k, dq, dk, qw, kw, f, **odd)
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("size,eps", [(1e17, EPS), (1e14, EPS), (1e7, EPS), (1e-14, 0.0), (1e-17, 0.0)])
+def test_rows_far_from_one(size, eps, dtype):
+    """Rows whose squares fit fp32 and the cube of whose 1 / RMS does not."""
+    B, H, Hkv, S, D, N = 1, 3, 1, 40, 128, 4
+    q, k, qw, kw, dq, dk = _make(B, H, Hkv, S, D, torch.float32, 10)
+    rms = lambda x: x.square().mean(-1, keepdim=True).sqrt()  # noqa: E731
+    q, k = ((x / rms(x) * size).to(dtype) for x in (q, k))  # |x| <= sqrt(128) * size at most, 5 * size here
+    dq, dk = dq.to(dtype), dk.to(dtype)
+    f = sp.rope_frequencies(D, 10000.0, "cpu")
+    pos = positions(S, N, sp.STRIPED)[None]
+    d = [t.to(DEV) for t in (q, k, qw, kw, f)]
+    yq, yk = sp.striped_qk_norm_rope(*d, N, eps=eps)
+    gq, gk, gqw, gkw = sp.striped_qk_norm_rope_bwd(d[0], d[1], dq.to(DEV), dk.to(DEV), *d[2:], N, eps=eps)
+    for x, w, g, y, dx, dw in ((q, qw, dq, yq, gq, gqw), (k, kw, dk, yk, gk, gkw)):
+        r = norm_rope_reference(x, w, pos, f, eps, False, g)
+        within(y, r["y"], _rel(dtype) * r["y"].abs() + STEPS * r["y_mag"], "y")
+        within(dx, r["dx"], _rel(dtype) * r["dx"].abs() + STEPS * r["dx_mag"], "dx")
+        within(dw, r["dw"], (128 * F32 + STEPS) * r["dw_mag"], "dw")
