@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
                 const int written = tail ? len - kbase : DT;
                 if (written < DT) {
                     const int s = j % NS;
-                    if (!mbar_wait(smem_u32(&bars->kv_full[s]), (j / NS) & 1, p.wc)) {
+                    if (!mbar_wait_warp(smem_u32(&bars->kv_full[s]), (j / NS) & 1, p.wc)) {
                         ok = false;
                         break;
                     }
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
                 float alpha = 1.f;
                 if (warp_on) {
                     const uint32_t tS = ((j & 1) ? tS1 : tS0) + lane_off;
-                    if (!mbar_wait(smem_u32(&bars->s_full[j & 1]), (j >> 1) & 1, p.wc)) {
+                    if (!mbar_wait_warp(smem_u32(&bars->s_full[j & 1]), (j >> 1) & 1, p.wc)) {
                         ok = false;
                         break;
                     }
@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
                 if (n > 0) {
                     // the previous product must be complete before O is
                     // touched (and before this warp's next arrival)
-                    if (!mbar_wait(smem_u32(&bars->o_done), (j - 1) & 1, p.wc)) {
+                    if (!mbar_wait_warp(smem_u32(&bars->o_done), (j - 1) & 1, p.wc)) {
                         ok = false;
                         break;
                     }
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
                 if (lane == 0) mbar_arrive(smem_u32(&bars->p_ready));
             }
             if (!ok) break;
-            if (!mbar_wait(smem_u32(&bars->o_done), (j - 1) & 1, p.wc)) {
+            if (!mbar_wait_warp(smem_u32(&bars->o_done), (j - 1) & 1, p.wc)) {
                 ok = false;
                 break;
             }

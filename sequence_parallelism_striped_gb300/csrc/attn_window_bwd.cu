@@ -400,8 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // bf16 into TMEM as the A operand of dV += P^T dO
         uint32_t P[2][32];
         auto compute_p = [&](int i) -> bool {
-            if (!bwd_wait(smem_u32(&bars->q_full[i % QS]), (i / QS) & 1, p.wc)) return false;
-            if (!bwd_wait(smem_u32(&bars->s_full), i & 1, p.wc)) return false;
+            if (!mbar_wait_warp(smem_u32(&bars->q_full[i % QS]), (i / QS) & 1, p.wc)) return false;
+            if (!mbar_wait_warp(smem_u32(&bars->s_full), i & 1, p.wc)) return false;
             tc_fence_after();
             const float *sL = stat_ptr(i);
             // keep (query, key) iff key <= query <= key + W - 1, or any later
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) ok = compute_p(0);
         for (int i = 0; i < nt && ok; ++i) {
             // ---- dS = P * (dP - Delta) -> smem (A operand of dQ and dK)
-            if (!bwd_wait(smem_u32(&bars->dp_full), i & 1, p.wc)) {
+            if (!mbar_wait_warp(smem_u32(&bars->dp_full), i & 1, p.wc)) {
                 ok = false;
                 break;
             }
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i + 1 < nt && !compute_p(i + 1)) ok = false;
         }
         if (ok) {
-            ok = bwd_wait(smem_u32(&bars->acc_done), 0, p.wc);
+            ok = mbar_wait_warp(smem_u32(&bars->acc_done), 0, p.wc);
             tc_fence_after();
         }
         // ---------------- epilogue: this warpgroup's columns of dK, dV
@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // column = query; HD = 64: lane = query, column = dimension.
         constexpr int kCols = HD == 128 ? BT : HD;
         for (int i = 0; i < nt; ++i) {
-            if (!bwd_wait(smem_u32(&bars->dq_full), i & 1, p.wc)) break;
+            if (!mbar_wait_warp(smem_u32(&bars->dq_full), i & 1, p.wc)) break;
             tc_fence_after();
             uint32_t q[kCols / 32][32];
 #pragma unroll

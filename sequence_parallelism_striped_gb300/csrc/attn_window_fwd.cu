@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
             float m_ref = -INFINITY, l = 0.f;
             bool first = true;
             for (int kt = ns > 0 ? 0 : lo; kt <= qt; kt = kt + 1 == ns ? lo : kt + 1) {
-                if (!win_wait<HD>(smem_u32(&bars->s_full[x]), n & 1, p.wc)) {
+                if (!mbar_wait_warp(smem_u32(&bars->s_full[x]), n & 1, p.wc)) {
                     ok = false;
                     break;
                 }
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
                 first = false;
             }
             // ---------------- epilogue
-            if (ok) ok = win_wait<HD>(smem_u32(&bars->o_done[x]), m++ & 1, p.wc);
+            if (ok) ok = mbar_wait_warp(smem_u32(&bars->o_done[x]), m++ & 1, p.wc);
             tc_fence_after();
             const bool valid = tile_has(g, qt, ri);
             const bool empty = !(l > 0.f) || !ok;

@@ -263,3 +263,21 @@ def test_several_row_tiles(layout, B, Bp, H, Hkv, T, P, C, D, N, W, ns):
     assert sp.check_error() == 0
     within(gl, lse, LSE_TOL, "lse")
     within(go, o, tol, "o")
+
+
+@pytest.mark.parametrize("B,Bp,H,Hkv,T,P,C,D,N,W,ns", [(40, 1, 8, 1, 1, 2048, 20, 64, 8, 0, 0),
+                                                       (3, 3, 4, 2, 3, 1000, 300, 128, 8, 280, 1),
+                                                       (5, 1, 4, 4, 1, 0, 700, 64, 1, 0, 0)])
+def test_missing_tiles_end_and_leave_the_device_usable(B, Bp, H, Hkv, T, P, C, D, N, W, ns):
+    """Row tiles with one and with four warps at work, tails with unwritten rows."""
+    args = _gpu(*_make(B, Bp, H, Hkv, T, P, C, D, None, 9))
+    want = sp.striped_attn_decode(*args, N, sp.STRIPED, W, ns)
+    assert sp.check_error() == 0
+    try:
+        sp.test_inject(sp.FAULT_FWD_SKIP_KV, 5_000_000)
+        sp.striped_attn_decode(*args, N, sp.STRIPED, W, ns)
+        assert sp.check_error() == -5
+    finally:
+        sp.test_inject(sp.FAULT_NONE, 0)
+    got = sp.striped_attn_decode(*args, N, sp.STRIPED, W, ns)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1]) and sp.check_error() == 0

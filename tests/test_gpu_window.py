@@ -303,3 +303,28 @@ def test_offsets_past_32_bits(emptied_cache):
     dx1 = sp.striped_qk_norm_rope_bwd(one[0], one[1], grads1[1], grads1[2], w, w, f, N)
     assert torch.equal(dx[0][:, -1:], dx1[0]) and torch.equal(dx[1][:, -1:], dx1[1])
     assert sp.check_error() == 0
+
+
+@pytest.mark.parametrize("layout,N,D,W,ns", [(sp.STRIPED, 8, 64, 200, 4), (sp.STRIPED, 3, 128, 1500, 0),
+                                             (sp.CONTIGUOUS, 1, 64, 1, 0), (sp.ZIGZAG, 2, 128, 300, 200)])
+def test_missing_tiles_end_and_leave_the_device_usable(layout, N, D, W, ns):
+    """Every role's waits run out: the calls return, report, and the next ones
+    give what they gave before."""
+    S = 1536 if layout != sp.STRIPED else 1503 // N * N
+    q, k, v, do = (t.to(DEV) for t in _make(2, 4, 2, S, D, 12))
+    o, lse = sp.striped_attn_window_fwd(q, k, v, N, W, ns, layout)
+    grads = sp.striped_attn_window_bwd(q, k, v, o, lse, do, N, W, ns, layout)
+    assert sp.check_error() == 0
+    try:
+        sp.test_inject(sp.FAULT_FWD_SKIP_KV, 5_000_000)
+        sp.striped_attn_window_fwd(q, k, v, N, W, ns, layout)
+        assert sp.check_error() == -5
+        sp.test_inject(sp.FAULT_BWD_SKIP_Q, 5_000_000)
+        sp.striped_attn_window_bwd(q, k, v, o, lse, do, N, W, ns, layout)
+        assert sp.check_error() == -5
+    finally:
+        sp.test_inject(sp.FAULT_NONE, 0)
+    o2, lse2 = sp.striped_attn_window_fwd(q, k, v, N, W, ns, layout)
+    again = sp.striped_attn_window_bwd(q, k, v, o, lse, do, N, W, ns, layout)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and sp.check_error() == 0
+    assert torch.equal(grads[1], again[1]) and torch.equal(grads[2], again[2])
