@@ -427,8 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // written to TMEM as the A operand of dV += P^T dO
         uint32_t pkP[32];
         auto compute_p = [&](const QTileIter &t, int i) -> bool {
-            if (!mbar_wait(smem_u32(&bars->q_full[i % QS]), (i / QS) & 1, p.wc)) return false;
-            if (!mbar_wait(smem_u32(&bars->s_full), i & 1, p.wc)) return false;
+            if (!mbar_wait_warp(smem_u32(&bars->q_full[i % QS]), (i / QS) & 1, p.wc)) return false;
+            if (!mbar_wait_warp(smem_u32(&bars->s_full), i & 1, p.wc)) return false;
             tc_fence_after();
             const float *sL = stat_ptr(i);
             const bool diag = t.has_diag && t.a == t.a_lo;
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) ok = compute_p(cur, 0);
         for (int i = 0; i < nt && ok; ++i) {
             // ---- dS = P * (dP - Delta) -> smem (A operand of dQ and dK)
-            if (!mbar_wait(smem_u32(&bars->dp_full), i & 1, p.wc)) {
+            if (!mbar_wait_warp(smem_u32(&bars->dp_full), i & 1, p.wc)) {
                 ok = false;
                 break;
             }
@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // ---- dQ_i readout -> fp32 accumulator
-            if (!mbar_wait(smem_u32(&bars->dq_full), i & 1, p.wc)) {
+            if (!mbar_wait_warp(smem_u32(&bars->dq_full), i & 1, p.wc)) {
                 ok = false;
                 break;
             }
@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (wg == 1 && lane == 0) release_pending();
         if (lane == 0) bulk_wait_group0();
         if (ok) {
-            ok = mbar_wait(smem_u32(&bars->acc_done), 0, p.wc);
+            ok = mbar_wait_warp(smem_u32(&bars->acc_done), 0, p.wc);
             tc_fence_after();
         }
         // ---------------- epilogue: this warpgroup's columns of dK, dV

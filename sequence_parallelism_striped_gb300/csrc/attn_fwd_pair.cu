@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const int lim_diag = ri + sp.diag_off;
             int n_full = 0, n_part = 0;  // tiles of this round turned into P below
             for (int b = 0; b < ntr; ++b, ++j) {
-                if (!mbar_wait(smem_u32(&bars->s_full[x]), j & 1, p.wc)) {
+                if (!mbar_wait_warp(smem_u32(&bars->s_full[x]), j & 1, p.wc)) {
                     ok = false;
                     break;
                 }
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 m_ref = m_new;
                 if (j > 0) {
                     // PV(j-1) of this group must be complete before O is touched
-                    if (!mbar_wait(smem_u32(&bars->o_done[x]), (j - 1) & 1, p.wc)) {
+                    if (!mbar_wait_warp(smem_u32(&bars->o_done[x]), (j - 1) & 1, p.wc)) {
                         ok = false;
                         break;
                     }
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         // ---------------- epilogue
         if (ok) {
-            ok = mbar_wait(smem_u32(&bars->o_done[x]), (nt - 1) & 1, p.wc);
+            ok = mbar_wait_warp(smem_u32(&bars->o_done[x]), (nt - 1) & 1, p.wc);
             tc_fence_after();
         }
         const int64_t i = (int64_t)a * PB + ri;

@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int n_full = 0, n_part = 0;  // tiles of this round turned into P below
             for (int b = 0; b < ntr; ++b, ++j) {
                 const uint32_t tS = ((j & 1) ? tS1 : tS0) + lane_off;
-                if (!mbar_wait(smem_u32(&bars->s_full[j & 1]), (j >> 1) & 1, p.wc)) {
+                if (!mbar_wait_warp(smem_u32(&bars->s_full[j & 1]), (j >> 1) & 1, p.wc)) {
                     ok = false;
                     break;
                 }
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m_ref = m_new;
                 if (j > 0) {
                     // PV_{j-1} must be complete before O is touched or PV_j issued
-                    if (!mbar_wait(smem_u32(&bars->o_done), (j - 1) & 1, p.wc)) {
+                    if (!mbar_wait_warp(smem_u32(&bars->o_done), (j - 1) & 1, p.wc)) {
                         ok = false;
                         break;
                     }
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // ---------------- epilogue
         if (ok && nt > 0) {
-            ok = mbar_wait(smem_u32(&bars->o_done), (nt - 1) & 1, p.wc);
+            ok = mbar_wait_warp(smem_u32(&bars->o_done), (nt - 1) & 1, p.wc);
             tc_fence_after();
         }
         const int64_t i = (int64_t)ag * BM + ri;

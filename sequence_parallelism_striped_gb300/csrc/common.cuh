@@ -401,7 +401,9 @@ __device__ __forceinline__ bool elect_one() {
 // ends in a uniform branch and the further ones are a function of their own:
 // so the vote costs nothing (window forward, H = 32 + 8, S = 65536, D = 128:
 // 1104 us without a vote, 1102 so, 1113 with mbar_wait inlined and voted on;
-// decoding, 24 requests, window 4096: 33.8, 32.9 and 34.8 us).
+// decoding, 24 requests, window 4096: 33.8, 32.9 and 34.8 us; full attention,
+// H = 8, S = 65536 forward 5.89, 5.83 and 6.00 ms, S = 32768 backward 5.63,
+// 5.58 and 5.70 ms).
 inline __device__ __noinline__ bool mbar_wait_warp_timed(uint32_t bar, uint32_t parity, const WaitCtl w) {
     const uint64_t t0 = global_timer_ns();
 #pragma unroll 1

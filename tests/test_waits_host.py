@@ -68,7 +68,7 @@ __global__ void k(int n) {
 
 
 @pytest.mark.parametrize("name", ["attn_window_fwd.cu", "attn_window_bwd.cu", "attn_decode.cu", "norm_rope.cu",
-                                  "common.cuh"])
+                                  "common.cuh", "attn_fwd_tc.cu", "attn_fwd_pair.cu", "attn_bwd_tc.cu"])
 def test_warps_wait_as_one(name):
     with open(os.path.join(CSRC, name)) as f:
         bad = lane_waits_of_many(f.read())
