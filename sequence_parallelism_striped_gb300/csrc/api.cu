@@ -132,7 +132,9 @@ static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 
 static int check_sizes(int64_t B, int64_t H, int64_t S, int64_t D, int N) {
     if (B < 1 || H < 1 || S < 1 || D < 1 || N < 1) return STRIPED_ERR_INVALID_ARG;
     if (S % N != 0) return STRIPED_ERR_INVALID_ARG;
-    if (S > (1ll << 31) || B * H > (1ll << 31)) return STRIPED_ERR_UNSUPPORTED;
+    // each bounded before the product, which could wrap
+    const int64_t limit = 1ll << 31;
+    if (S > limit || B > limit || H > limit || B * H > limit) return STRIPED_ERR_UNSUPPORTED;
     return STRIPED_OK;
 }
 
@@ -770,8 +772,11 @@ int striped_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out,
 }
 
 size_t striped_qk_norm_rope_workspace_size(int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t D, int dtype) {
-    if (check_sizes(B, H, S, D, 1) || Hkv < 1 || (dtype != STRIPED_BF16 && dtype != STRIPED_FP32)) return 0;
-    if (D > 256 || D % (dtype == STRIPED_BF16 ? 16 : 8) != 0 || H > kMaxRopeHeads || Hkv > kMaxRopeHeads) return 0;
+    const int64_t heads = H > Hkv ? H : Hkv;
+    if (check_sizes(B, heads, S, D, 1) || H < 1 || Hkv < 1 || (dtype != STRIPED_BF16 && dtype != STRIPED_FP32))
+        return 0;
+    if (D > 256 || D % (dtype == STRIPED_BF16 ? 16 : 8) != 0 || heads > kMaxRopeHeads || B * heads * S > kMaxRows)
+        return 0;
     return align256(rope_bwd_workspace(B, H, Hkv, S, D, dtype));
 }
 

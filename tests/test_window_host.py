@@ -286,3 +286,20 @@ def test_sizes_that_no_gpu_holds():
     assert _rope(lib, H=65537) == UNSUPPORTED and _rope(lib, Hkv=65537) == UNSUPPORTED
     assert lib.striped_qk_norm_rope_workspace_size(1, 65537, 2, 64, 64, 0) == 0
     assert _rope(lib, B=2 ** 15, H=2 ** 16, S=2 ** 31) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("B,H", [(2 ** 62, 4), (2 ** 61, 8), (4, 2 ** 62), (2 ** 33, 2 ** 31), (2 ** 40, 2 ** 24)])
+def test_products_of_sizes_that_wrap(B, H):
+    """B * H is 0 (or small) modulo 2^64: refused, not taken for an empty call."""
+    lib = sp.load()
+    assert (B * H) % 2 ** 64 == 0
+    assert _window(lib, B=B, H=H, Hkv=H) == UNSUPPORTED
+    assert lib.striped_attn_window_workspace_size(B, H, H, 256, 64, 4, 0, 0, 10, 4) == 0
+    assert lib.striped_attn_window_bwd(*A[:10], 1 << 40, B, H, H, 256, 64, 4, 0, 0, 10, 4, ctypes.c_float(0.1),
+                                       None) == UNSUPPORTED
+    assert _rope(lib, B=B, H=H, Hkv=H) == UNSUPPORTED and _rope(lib, B=B, H=1, Hkv=H) == UNSUPPORTED
+    assert lib.striped_qk_norm_rope_workspace_size(B, H, H, 64, 64, 0) == 0
+    assert lib.striped_qk_norm_rope_workspace_size(B, 1, H, 64, 64, 0) == 0
+    assert _decode(lib, B=B, Bp=B, H=H, Hkv=H) == UNSUPPORTED
+    assert lib.striped_attn_fwd(*A[:5], B, H, 64, 128, 4, 0, 0, ctypes.c_float(0.1), None, None) == UNSUPPORTED
+    assert lib.striped_permute(A[0], A[1], B, H, 64, 128, 4, 0, None) == UNSUPPORTED
