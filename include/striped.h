@@ -325,6 +325,9 @@ int ring_bwd_finish(const float *acc, void *out, int64_t n, int dtype, float mul
  * kernels work on tiles of consecutive positions, not on the per-round tiles
  * of the ring, so there is no tile_stats.  K and V must be finite in every
  * row: a tile multiplies the weight 0 of a pair that is not kept with its V.
+ * More than 2^40 rows B * H * S, or 2^31 tiles of 65 .. 128 positions over all
+ * heads (16 for a sink tile of the backward), are UNSUPPORTED: no GPU holds
+ * them.
  * scale must be a normal number in (0, 1e38], and no result may overlap
  * another tensor of the call: else STRIPED_ERR_INVALID_ARG.
  */

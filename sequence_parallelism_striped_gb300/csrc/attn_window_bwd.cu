@@ -683,9 +683,10 @@ __global__ void __launch_bounds__(8 * HD / 4)
     window_sink_kernel(const WinBwdParams p) {
     wait_for_previous();  // and with it for the kernel before, which that one waited for
     const PosGeom &g = p.g;
-    const int64_t bh = blockIdx.y / p.nst;
-    const int kt = blockIdx.y % p.nst;
-    const int row = blockIdx.x * 8 + threadIdx.x / (HD / 4), col = threadIdx.x % (HD / 4) * 4;
+    const int tile = blockIdx.x / (BT / 8);
+    const int64_t bh = tile / p.nst;
+    const int kt = tile % p.nst;
+    const int row = blockIdx.x % (BT / 8) * 8 + threadIdx.x / (HD / 4), col = threadIdx.x % (HD / 4) * 4;
     if (!tile_has(g, kt, row)) return;
     const int n = 1 + far_units(g, kt, p.W, p.chunk);
     const float *src = p.parts + ((bh * p.nst + kt) * p.slots * 2 * BT + row) * (int64_t)HD + col;
@@ -724,7 +725,9 @@ bool window_bwd_plan(WinBwdPlan *plan, const WindowArgs &a) {
     int64_t units = g.nt;
     for (int kt = 0; kt < p.nst; ++kt) units += far_units(g, kt, p.W, p.chunk);
     p.slots = units > g.nt ? 1 + far_units(g, 0, p.W, p.chunk) : 0;
-    if (units * a.B * a.Hkv > 0x7fffffffll || (p.slots > 0 && a.B * a.Hkv * p.nst > 65535)) return false;
+    // one-dimensional grids of the units and of the sink tiles' rows
+    const int64_t most_units = 0x7fffffffll / (a.B * a.Hkv);
+    if (units > most_units || (p.slots > 0 && p.nst * (BT / 8) > most_units)) return false;
     p.units = (int)units;
     p.G = (int)(a.H / a.Hkv);
     p.scale = a.scale;
@@ -773,7 +776,7 @@ int launch_window_bwd_hd(const void *q, const void *k, const void *v, const void
     st = launch_after(window_post_kernel<HD>, dim3((unsigned)blocks), 256, 0, stream, dq_acc, (__nv_bfloat16 *)dq, p.g,
                       plan.padded_rows, a.scale);
     if (st || p.slots == 0) return st;
-    return launch_after(window_sink_kernel<HD>, dim3(BT / 8, (unsigned)(bh_kv * p.nst)), 8 * HD / 4, 0, stream, p);
+    return launch_after(window_sink_kernel<HD>, dim3((unsigned)(bh_kv * p.nst * (BT / 8))), 8 * HD / 4, 0, stream, p);
 }
 
 }  // namespace

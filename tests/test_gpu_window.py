@@ -328,3 +328,19 @@ def test_missing_tiles_end_and_leave_the_device_usable(layout, N, D, W, ns):
     again = sp.striped_attn_window_bwd(q, k, v, o, lse, do, N, W, ns, layout)
     assert torch.equal(o, o2) and torch.equal(lse, lse2) and sp.check_error() == 0
     assert torch.equal(grads[1], again[1]) and torch.equal(grads[2], again[2])
+
+
+def test_many_heads_with_sinks(emptied_cache):
+    """More than 65535 sink tiles: the last heads are what they are alone."""
+    B, H, S, D, N, W, ns = 16500, 4, 300, 64, 4, 5, 3
+    g = torch.Generator(device=DEV).manual_seed(13)
+    q, k, v, do = (torch.empty(B, H, S, D, dtype=torch.bfloat16, device=DEV).normal_(generator=g) for _ in range(4))
+    o, lse = sp.striped_attn_window_fwd(q, k, v, N, W, ns)
+    dq, dk, dv = sp.striped_attn_window_bwd(q, k, v, o, lse, do, N, W, ns)
+    last = [t[-2:].contiguous() for t in (q, k, v, o, lse, do)]
+    o1, lse1 = sp.striped_attn_window_fwd(*last[:3], N, W, ns)
+    dq1, dk1, dv1 = sp.striped_attn_window_bwd(*last, N, W, ns)
+    assert torch.equal(o[-2:], o1) and torch.equal(lse[-2:], lse1)
+    assert torch.equal(dk[-2:], dk1) and torch.equal(dv[-2:], dv1) and sp.check_error() == 0
+    # dQ is summed by atomics: a bf16 rounding apart at most
+    assert float((dq[-2:].float() - dq1.float()).abs().max()) <= 2.0 ** -7 * float(dq1.float().abs().max())

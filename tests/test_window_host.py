@@ -303,3 +303,13 @@ def test_products_of_sizes_that_wrap(B, H):
     assert _decode(lib, B=B, Bp=B, H=H, Hkv=H) == UNSUPPORTED
     assert lib.striped_attn_fwd(*A[:5], B, H, 64, 128, 4, 0, 0, ctypes.c_float(0.1), None, None) == UNSUPPORTED
     assert lib.striped_permute(A[0], A[1], B, H, 64, 128, 4, 0, None) == UNSUPPORTED
+
+
+def test_window_backward_takes_what_the_forward_takes():
+    """Many heads with sinks: the sink tiles' shares do not bound the batch."""
+    size = sp.load().striped_attn_window_workspace_size
+    one = size(1, 1, 1, 384, 64, 4, 0, 0, 64, 4)
+    # per head: three tiles of fp32 dQ and statistics, and two fp32 shares of one sink tile's dK and dV
+    assert one == 384 * (64 * 4 + 8) + 2 * 2 * 128 * 64 * 4
+    for B, H in ((8192, 8), (65536, 1), (200000, 4)):
+        assert size(B, H, H, 384, 64, 4, 0, 0, 64, 4) == B * H * one
