@@ -281,3 +281,18 @@ def test_missing_tiles_end_and_leave_the_device_usable(B, Bp, H, Hkv, T, P, C, D
         sp.test_inject(sp.FAULT_NONE, 0)
     got = sp.striped_attn_decode(*args, N, sp.STRIPED, W, ns)
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1]) and sp.check_error() == 0
+
+
+@pytest.mark.parametrize("layout,B,Bp,H,Hkv,T,P,C,D,N,W,ns", [
+    (sp.STRIPED, 1024, 1024, 2, 1, 1, 24, 9, 64, 4, 0, 0),    # 1024 prompts and 1024 tails: the most that a call takes
+    (sp.STRIPED, 2048, 1, 1, 1, 1, 0, 140, 128, 1, 100, 3),   # 2048 tails
+    (sp.CONTIGUOUS, 1000, 2, 1, 1, 2, 300, 3, 64, 1, 64, 0)])
+def test_the_most_requests_of_a_call(layout, B, Bp, H, Hkv, T, P, C, D, N, W, ns):
+    q, kp, vp, kt, vt, lens = _make(B, Bp, H, Hkv, T, P, C, D, None, 15)
+    o, lse, tol = _reference(q, kp, vp, kt, vt, lens, positions(P, N, layout) if P else None, W, ns, D ** -0.5)
+    behind = (torch.arange(C) >= lens[:, None])[:, None, :, None].expand_as(kt)
+    kt[behind], vt[behind] = float("nan"), float("nan")
+    go, gl = sp.striped_attn_decode(*_gpu(q, kp, vp, kt, vt, lens), N, layout, W, ns)
+    assert sp.check_error() == 0
+    within(gl, lse, LSE_TOL, "lse")
+    within(go, o, tol, "o")

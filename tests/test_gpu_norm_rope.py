@@ -214,3 +214,78 @@ def test_rows_far_from_one(size, eps, dtype):
         within(y, r["y"], _rel(dtype) * r["y"].abs() + STEPS * r["y_mag"], "y")
         within(dx, r["dx"], _rel(dtype) * r["dx"].abs() + STEPS * r["dx_mag"], "dx")
         within(dw, r["dw"], (128 * F32 + STEPS) * r["dw_mag"], "dw")
+
+
+MANY_BLOCKS = [
+    # layout, B, H, Hkv, S, D, N, dtype, positions given
+    (sp.STRIPED, 1, 20, 3, 2100, 128, 4, torch.bfloat16, False),   # chunks of eight heads and one of four
+    (sp.STRIPED, 1, 9, 3, 66000, 64, 8, torch.bfloat16, False),    # chunks of eight heads and one of one
+    (sp.ZIGZAG, 1, 20, 3, 65536, 128, 8, torch.bfloat16, False),   # four rounds of blocks
+    (sp.STRIPED, 1, 20, 3, 60000, 64, 5, torch.float32, False),    # the same
+    (sp.CONTIGUOUS, 2, 17, 16, 2000, 96, 1, torch.float32, False),
+    (sp.STRIPED, 700, 17, 3, 4, 128, 1, torch.bfloat16, True),     # rows read one by one
+    (sp.STRIPED, 900, 12, 9, 3, 64, 1, torch.float32, True),
+]
+
+
+@pytest.mark.parametrize("layout,B,H,Hkv,S,D,N,dtype,at", MANY_BLOCKS)
+def test_gradients_of_many_blocks(layout, B, H, Hkv, S, D, N, dtype, at):
+    """Blocks with several heads, a last chunk with fewer, several rounds."""
+    g = torch.Generator(device=DEV).manual_seed(11)
+    mk = lambda h: torch.randn(B, h, S, D, generator=g, device=DEV).to(dtype)  # noqa: E731
+    q, k, dq, dk = mk(H), mk(Hkv), mk(H), mk(Hkv)
+    qw, kw = (1 + 0.3 * torch.randn(D, generator=g, device=DEV) for _ in range(2))
+    f = sp.rope_frequencies(D, 10000.0, DEV)
+    pos = torch.randint(0, 100000, (B, S), generator=g, device=DEV) if at else positions(S, N, layout)[None].to(DEV)
+    ws = sp.qk_norm_rope_workspace(q, k)
+    ws.fill_(255)  # NaN in every share that is not written
+    got = sp.striped_qk_norm_rope_bwd(q, k, dq, dk, qw, kw, f, N, layout, eps=EPS, positions=pos if at else None,
+                                      workspace=ws)
+    assert sp.check_error() == 0
+    for x, w, c, dx, dw in ((q, qw, dq, got[0], got[2]), (k, kw, dk, got[1], got[3])):
+        want, mag = torch.zeros(2, D, dtype=torch.float64, device=DEV)
+        for h in range(x.shape[1]):
+            r = norm_rope_reference(x[:, h:h + 1], w, pos, f, EPS, False, c[:, h:h + 1])
+            tol = _rel(dtype) * r["dx"].abs() + STEPS * r["dx_mag"] + 1e-30
+            assert float(((dx[:, h:h + 1].double() - r["dx"]).abs() / tol).max()) <= 1.0, h
+            want += r["dw"]
+            mag += r["dw_mag"]
+        # a thread adds at most 112 rows one after another, its block 9 such sums, and the last kernel 43 and 32
+        within(dw, want.cpu(), ((196 * F32 + STEPS) * mag + 1e-30).cpu(), "dw")
+
+
+def test_workspace_of_the_caller():
+    B, H, Hkv, S, D = 1, 4, 2, 300, 64
+    q, k, qw, kw, dq, dk = (t.to(DEV) for t in _make(B, H, Hkv, S, D, torch.bfloat16, 12))
+    f = sp.rope_frequencies(D, 1e4, DEV)
+    want = sp.striped_qk_norm_rope_bwd(q, k, dq, dk, qw, kw, f)
+    ws = sp.qk_norm_rope_workspace(q, k)
+    for i in (255, 0):  # contents on entry are ignored
+        ws.fill_(i)
+        got = sp.striped_qk_norm_rope_bwd(q, k, dq, dk, qw, kw, f, workspace=ws)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    with pytest.raises(sp.StripedError):
+        sp.striped_qk_norm_rope_bwd(q, k, dq, dk, qw, kw, f, workspace=ws[:-256])
+    with pytest.raises(sp.StripedError):
+        sp.striped_qk_norm_rope_bwd(q, k, dq, dk, qw, kw, f, workspace=ws[1:])
+    with pytest.raises(ValueError):
+        sp.striped_qk_norm_rope_bwd(q, k, dq, dk, qw, kw, f, workspace=ws[::2])
+    with pytest.raises(TypeError):
+        sp.striped_qk_norm_rope_bwd(q, k, dq, dk, qw, kw, f, workspace=ws.cpu())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("layout", [sp.STRIPED, sp.CONTIGUOUS, sp.ZIGZAG])
+def test_one_stripe_of_a_long_sequence(layout, dtype):
+    """The same for stripes long enough to be streamed."""
+    B, H, Hkv, N, L, D = 2, 9, 3, 3, 250, 128
+    q, k, qw, kw, dq, dk = (t.to(DEV) for t in _make(B, H, Hkv, N * L, D, dtype, 13))
+    f = sp.rope_frequencies(64, 10000.0, DEV)
+    whole = sp.striped_qk_norm_rope(q, k, qw, kw, f, N, layout)
+    whole += sp.striped_qk_norm_rope_bwd(q, k, dq, dk, qw, kw, f, N, layout)[:2]
+    for d in range(N):
+        c = [t[:, :, d * L:(d + 1) * L].contiguous() for t in (q, k, dq, dk)]
+        part = sp.striped_qk_norm_rope(c[0], c[1], qw, kw, f, N, layout, stripe=d)
+        part += sp.striped_qk_norm_rope_bwd(*c, qw, kw, f, N, layout, stripe=d)[:2]
+        for a, b in zip(whole, part):
+            assert torch.equal(a[:, :, d * L:(d + 1) * L], b)

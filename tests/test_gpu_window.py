@@ -344,3 +344,26 @@ def test_many_heads_with_sinks(emptied_cache):
     assert torch.equal(dk[-2:], dk1) and torch.equal(dv[-2:], dv1) and sp.check_error() == 0
     # dQ is summed by atomics: a bf16 rounding apart at most
     assert float((dq[-2:].float() - dq1.float()).abs().max()) <= 2.0 ** -7 * float(dq1.float().abs().max())
+
+
+def test_workspace_of_the_caller():
+    q, k, v, do = (t.to(DEV) for t in _make(1, 4, 2, 1500, 64, 14))
+    N, W, ns = 4, 200, 130
+    o, lse = sp.striped_attn_window_fwd(q, k, v, N, W, ns)
+    want = sp.striped_attn_window_bwd(q, k, v, o, lse, do, N, W, ns)
+    ws = sp.new_window_workspace(q, k, N, W, ns)
+    for i in (255, 0):  # contents on entry are ignored
+        ws.fill_(i)
+        got = sp.striped_attn_window_bwd(q, k, v, o, lse, do, N, W, ns, workspace=ws)
+        assert torch.equal(want[1], got[1]) and torch.equal(want[2], got[2])
+        off = (want[0].float() - got[0].float()).abs().max()
+        assert float(off) <= 2.0 ** -7 * float(want[0].float().abs().max())
+    with pytest.raises(sp.StripedError):
+        sp.striped_attn_window_bwd(q, k, v, o, lse, do, N, W, ns, workspace=ws[:-256])
+    with pytest.raises(sp.StripedError):
+        sp.striped_attn_window_bwd(q, k, v, o, lse, do, N, W, ns, workspace=ws[16:])
+    with pytest.raises(ValueError):
+        sp.striped_attn_window_bwd(q, k, v, o, lse, do, N, W, ns, workspace=ws.view(2, -1))
+    with pytest.raises(TypeError):
+        sp.striped_attn_window_bwd(q, k, v, o, lse, do, N, W, ns, workspace=ws.cpu())
+    assert sp.check_error() == 0
