@@ -478,16 +478,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
                                     if (!(k & (1u << c))) sv[32 * w + c] = -INFINITY;
                         }
                     }
-                    float mx8[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) mx8[i] = fmaxf(sv[i], sv[8 + i]);
-#pragma unroll
-                    for (int c = 16; c < DT; c += 16)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) mx8[i] = fmax3(mx8[i], sv[c + i], sv[c + 8 + i]);
-                    const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
-                                           fmaxf(mx8[6], mx8[7]));
-                    const float m_tile = mx * cl2;
+                    const float m_tile = row_max(sv) * cl2;
                     const bool move = n == 0 || m_tile > m_ref + kDRescale;
                     const float m_new = move ? fmaxf(m_ref, m_tile) : m_ref;
                     alpha = (n == 0 || !move) ? 1.f : ex2(m_ref - m_new);

@@ -313,19 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < BN; ++c)
                         if (c > lim) sv[c] = -INFINITY;
                 }
-                // row max as 8 independent chains of three-input max (a
-                // single chain of 128 dependent max operations would be pure
-                // latency)
-                float mx8[8];
-#pragma unroll
-                for (int t = 0; t < 8; ++t) mx8[t] = fmaxf(sv[t], sv[8 + t]);
-#pragma unroll
-                for (int c = 16; c < BN; c += 16)
-#pragma unroll
-                    for (int t = 0; t < 8; ++t) mx8[t] = fmax3(mx8[t], sv[c + t], sv[c + 8 + t]);
-                const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
-                                       fmaxf(mx8[6], mx8[7]));
-                const float m_tile = mx * cl2;
+                const float m_tile = row_max(sv) * cl2;
                 // lazy rescale: move the reference only when the max grows a lot
                 bool move = (j == 0) ? true : (m_tile > m_ref + kRescaleThreshold);
                 const float m_new = move ? fmaxf(m_ref, m_tile) : m_ref;

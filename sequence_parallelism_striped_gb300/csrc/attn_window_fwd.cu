@@ -377,16 +377,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
                                 if (!(k & (1u << c))) sv[32 * b + c] = -INFINITY;
                     }
                 }
-                float mx8[8];
-#pragma unroll
-                for (int t = 0; t < 8; ++t) mx8[t] = fmaxf(sv[t], sv[8 + t]);
-#pragma unroll
-                for (int c = 16; c < WB; c += 16)
-#pragma unroll
-                    for (int t = 0; t < 8; ++t) mx8[t] = fmax3(mx8[t], sv[c + t], sv[c + 8 + t]);
-                const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
-                                       fmaxf(mx8[6], mx8[7]));
-                const float m_tile = mx * cl2;
+                const float m_tile = row_max(sv) * cl2;
                 const bool move = first || m_tile > m_ref + kWRescale;
                 const float m_new = move ? fmaxf(m_ref, m_tile) : m_ref;
                 const float alpha = (first || !move) ? 1.f : ex2(m_ref - m_new);

@@ -560,6 +560,19 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     return r;
 }
 
+// Maximum of a row's 128 scores, as eight independent chains of three-operand
+// maxima (one chain of 127 would be pure latency).
+__device__ __forceinline__ float row_max(const float (&s)[128]) {
+    float m[8];
+#pragma unroll
+    for (int t = 0; t < 8; ++t) m[t] = fmaxf(s[t], s[8 + t]);
+#pragma unroll
+    for (int c = 16; c < 128; c += 16)
+#pragma unroll
+        for (int t = 0; t < 8; ++t) m[t] = fmax3(m[t], s[c + t], s[c + 8 + t]);
+    return fmax3(fmax3(m[0], m[1], m[2]), fmax3(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
+}
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);  // .x = lo (low half), .y = hi
     return *reinterpret_cast<uint32_t *>(&v);
