@@ -623,6 +623,8 @@ def striped_attn_decode(q, k_prompt, v_prompt, k_tail, v_tail, tail_lens, N: int
                                        scale, workspace, out, lse_out)
     dt, code = q.dtype, _dtype_code(q)
     kp = vp = None
+    if k_prompt is None and v_prompt is not None:
+        raise ValueError("v_prompt without k_prompt")
     if k_prompt is not None:
         kp = _need(k_prompt, "k_prompt", (Bp, Hkv, P, D), dt, dev)
         vp = _need(v_prompt, "v_prompt", (Bp, Hkv, P, D), dt, dev)

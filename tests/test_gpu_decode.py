@@ -296,3 +296,13 @@ def test_the_most_requests_of_a_call(layout, B, Bp, H, Hkv, T, P, C, D, N, W, ns
     assert sp.check_error() == 0
     within(gl, lse, LSE_TOL, "lse")
     within(go, o, tol, "o")
+
+
+def test_half_a_prompt_is_refused():
+    q, kp, vp, kt, vt, lens = _gpu(*_make(4, 2, 4, 2, 1, 256, 16, 64, None, 16))
+    with pytest.raises(ValueError):
+        sp.striped_attn_decode(q, None, vp, kt, vt, lens, 4)
+    with pytest.raises(TypeError):
+        sp.striped_attn_decode(q, kp, None, kt, vt, lens, 4)
+    sp.striped_attn_decode(q, None, None, kt, vt, lens)
+    assert sp.check_error() == 0
