@@ -411,7 +411,8 @@ size_t striped_attn_decode_workspace_size(int64_t B, int64_t Bp, int64_t H, int6
  * for the pairs (a, b) = (j, j + rotary_dim/2), or (2j, 2j + 1) with
  * interleaved != 0, j < rotary_dim/2; elements from rotary_dim on are not
  * rotated (rotary_dim = 0: norm only, inv_freq may be NULL).  Angles are
- * reduced in 64 bits, so they stay exact at far positions (inv_freq finite).
+ * reduced to one turn in 64 bits without loss; the fp64 rounding of inv_freq
+ * (finite) leaves them off by about 2^-53 of p * inv_freq.
  * Squares and their sums are fp32: |x| below 1e18, and eps > 0 wherever a
  * row's root mean square may be below 1e-18 (an all-0 row among them).
  *  q, q_out: [B,H,S,D], k, k_out: [B,Hkv,S,D] `dtype`; H and Hkv are any

@@ -7,6 +7,11 @@ library is missing, every call raises -- there is no fallback.
 
 The functions mirror the C ABI in ``include/striped.h`` (same names).  Tensors
 are CUDA tensors [B, H, S, D], contiguous, bf16 or fp32.
+
+A call with ``stream=`` runs on that stream as any PyTorch operation under
+``torch.cuda.stream`` does: it does not wait for what other streams still write,
+and tensors of another stream that are given up while it runs need
+``record_stream``.
 """
 from __future__ import annotations
 
@@ -545,7 +550,8 @@ def _window_workspace_size(dev: int, *args) -> int:
 
 
 def new_window_workspace(q, k, N: int, window: int, sinks: int = 0, layout: int = STRIPED) -> torch.Tensor:
-    """Workspace of striped_attn_window_bwd for these tensors and arguments."""
+    """Workspace of striped_attn_window_bwd for these tensors and arguments;
+    calls that may overlap each need their own."""
     B, H, S, D = q.shape
     return _work(None, _window_workspace_size, q.get_device(), B, H, k.shape[1], S, D, N, layout, _dtype_code(q),
                  window, sinks)[2]
@@ -598,7 +604,8 @@ def _decode_workspace_size(dev: int, *args) -> int:
 
 def new_decode_workspace(q, k_prompt, k_tail, N: int = 1, layout: int = STRIPED, window: int = 0,
                          sinks: int = 0) -> torch.Tensor:
-    """Workspace of striped_attn_decode for these tensors and arguments."""
+    """Workspace of striped_attn_decode for these tensors and arguments; calls
+    that may overlap (two captured steps among them) each need their own."""
     n = _decode_sizes(q, k_prompt, k_tail)
     dev = q.get_device()
     if not _here(dev, None):
@@ -686,7 +693,8 @@ def _rope_workspace_size(dev: int, *args) -> int:
 
 
 def qk_norm_rope_workspace(q, k) -> torch.Tensor:
-    """Workspace of striped_qk_norm_rope_bwd for these q and k."""
+    """Workspace of striped_qk_norm_rope_bwd for these q and k; calls that may
+    overlap each need their own."""
     B, H, S, D = q.shape
     return _work(None, _rope_workspace_size, q.get_device(), B, H, k.shape[1], S, D, _dtype_code(q))[2]
 

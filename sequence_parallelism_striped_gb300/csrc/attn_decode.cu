@@ -36,11 +36,14 @@
 // masked by selection and their V rows are cleared in shared memory before
 // the product, where a weight of 0 would not hide them.
 //
-// Measured at D = 128, 32 query heads on 8: 32 requests on one prompt of
-// 131072 positions, tails of 1000: 110 us, 5.8 TB/s; 16 requests with prompts
-// of their own of 32768: 310 us, 6.9 TB/s (a copy reaches 6.69); one request
-// on 4096: 11 us, two launches and one tile's chain of load, product, softmax,
-// product and join.
+// P is rounded to bf16 as a tensor-core operand, the row sum adds the
+// unrounded values (attn_window_fwd.cu); partial results are joined in fp32.
+//
+// Measured in a graph at D = 128, 32 query heads on 8: 32 requests on one
+// prompt of 131072 positions, tails of 1000: 110 us, 5.8 TB/s; 16 requests with
+// prompts of their own of 32768: 310 us, 6.9 TB/s (a copy reaches 6.69); one
+// request on 4096: 11 us, two launches and one tile's chain of load, product,
+// softmax, product and join.
 #include <math.h>
 
 #include "common.cuh"

@@ -44,11 +44,15 @@
 // fp32 ulps before the rounding to bf16), dK and dV do not.
 //
 // Bound by the hand-offs and the L2's fp32 reductions (64 KB a tile): tensor
-// pipe 44% active; without the reductions the main kernel would take 0.8 of
+// pipe 45% active; without the reductions the main kernel would take 0.8 of
 // its time.  Measured (H = 32 + 8, S = 32768, D = 128, window 2048, 16 sinks,
-// zig-zag): 3.05 ms, 880 TFLOP/s of kept pairs, 2.9 us a 128 x 128 tile of one
-// multiprocessor (the full attention's backward: 3.05).  The four kernels
-// follow one another by programmatic launches: 8 us less a call.
+// zig-zag): 3.03 ms, 885 TFLOP/s of kept pairs, 2.9 us a 128 x 128 tile of one
+// multiprocessor (the full attention's backward: 3.04); D = 64, H = 32: 2.01
+// ms.  The four kernels follow one another by programmatic launches: 8 us less
+// a call.  A unit takes its key tile against all G query heads, so few
+// key/value heads on a short sequence leave multiprocessors idle: H = 32, S =
+// 2048, window 1024: 116 us on 32 key/value heads, 212 on 4, 782 on 1 (16
+// units); S = 8192 480 on 8, 845 on 1.
 #include <math.h>
 
 #include "common.cuh"
@@ -95,8 +99,8 @@ struct WinBwdParams {
     WaitCtl wc;  // status word, wait bound, test hook
 };
 
-// mbar_wait and mbar_wait_warp with one place that tries (B = 1, H = 8,
-// S = 8192, window 1024: 158 us with the tries unrolled at every place that
+// The producers' and the issuer's waits with one place that tries (B = 1, H =
+// 8, S = 8192, window 1024: 158 us with the tries unrolled at every place that
 // waits, 155 with them in a loop of their own, 152 so).
 __device__ __forceinline__ bool bwd_wait(uint32_t bar, uint32_t parity, const WaitCtl &w) {
     uint64_t t0 = 0;
@@ -257,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(skip_first && t == 0)) bwd_wait(smem_u32(&bars->q_full[t % QS]), (t / QS) & 1, p.wc);
         } else if (warp == 2 && lane == 0 && nt > 0) {
             // ---------------- TMA producer: dO_i (its own stream: the buffer is
-            // released at dV_i, or at HD 64 after the dQ_i half staged in it is read)
+            // released at dV_i, Q_i's at dK_i)
             tma_prefetch_desc(&tmdO);
             int i = 0;
             for (; i < nt; ++i) {

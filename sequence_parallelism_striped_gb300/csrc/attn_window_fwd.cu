@@ -19,26 +19,30 @@
 // the last one's O.
 //   warp 0      TMA producer: Q_A, Q_B of an item, then its K/V tiles
 //   warp 1      TMEM allocator + tcgen05.mma issuer: the whole warp waits and
-//               one elected lane issues (eight MMAs in under 64 clocks; from a
-//               branch of a single thread about 90, longer than they run)
+//               one elected lane issues (a product of 128 x 128 x 16 in less
+//               than the 64 clocks that it runs; from a branch of a single
+//               thread in about 90)
 //   warps 2..5  softmax group A, thread t owns query row t
 //   warps 6..9  softmax group B
 // Tensor memory: S_A [0,128), S_B [128,256), O_A [256,256+HD), O_B
 // [384,384+HD); P is written back over S as bf16 pairs, the A operand of
 // O += P V.  The running max moves lazily (by more than 2^8), which is exact
 // because the final division uses the same reference.  P is rounded to bf16
-// as a tensor-core operand; the row sum adds the unrounded values.
+// as a tensor-core operand (tf32 would run at half the rate, with V converted);
+// the row sum adds the unrounded values, which lse needs.  o is 2.3e-3 off in
+// the root mean square then, 1.6e-3 of it the rounding of o itself.
 //
 // The kept columns of a row in a partly kept tile (the diagonal one, at most
 // two at the window's lower edge, the last sink tile) are a few bit ranges;
 // a warp skips the 32-column words that all its rows keep whole.
 //
 // Bound by the chain S -> softmax -> P -> O of a query tile: the tensor pipe is
-// 52% active, DRAM 17%.  Measured (H = 32 + 8, S = 65536, D = 128, N = 8): a
+// 53% active, DRAM 17%.  Measured (H = 32 + 8, S = 65536, D = 128, N = 8): a
 // 128 x 128 tile takes 0.77 us of a multiprocessor at a window of 16384, 1.00
 // us at 1024, where an item's ends (its first S, its last O) are 20% of it.
 // With 4 sinks, whose tile is one of the ten that a query tile issues for
-// eight kept: 1085 us, 1010 TFLOP/s of kept pairs.  Slower: 32-column products
+// eight kept: 1093 us in a graph (1090 .. 1105 over boxes), 1000 TFLOP/s of
+// kept pairs; D = 64, H = 32: 857 us.  Slower: 32-column products
 // for the sink tile, K and V in places of their own, two issuing warps, two
 // threads a row, the maximum off the chain.
 #include <math.h>
@@ -70,12 +74,14 @@ struct WinCfg {
     static_assert(NS <= kWMaxNS, "barrier array");
 };
 
-// mbar_wait and mbar_wait_warp in little code: the tries are not unrolled at
-// every place that waits, and a warp's first one ends in a uniform branch
-// (S = 65536, window 1024, 4 sinks: 1112 us unrolled, 1075 with the uniform
-// first try, 1063 with both; window 16384: 9.95, 9.51 and 9.27 ms).  At HD =
-// 64 the timed tries are a function of their own (S = 4096, H = 8: 26.8 us
-// inlined, 25.4 so; at HD = 128 1068 us inlined, 1116 so).
+// The producer's and the issuer's waits in little code: the tries are not
+// unrolled at every place that waits, and a warp's first one ends in a uniform
+// branch (S = 65536, window 1024, 4 sinks: 4% off; window 16384: 7%).  At HD =
+// 64 the timed tries are a function of their own, at HD = 128 they are inlined
+// (each side timed in turn with the other, graphs; HD = 64: S = 65536, H = 32
+// 860 us so and 932 inlined, S = 16384, H = 8 67.7 and 73.8, S = 5000 26.7 and
+// 28.7; HD = 128: S = 65536, H = 32 + 8 1105 us inlined and 1152 as a
+// function, S = 8192, H = 8 45.2 and 47.3, window 16384 1187 and 1232).
 __device__ __noinline__ bool win_wait_timed(uint32_t bar, uint32_t parity, const WaitCtl w) {
     return mbar_wait_timed(bar, parity, w);
 }

@@ -13,11 +13,13 @@
 //
 // The position of a row is the one the placement puts there (striped:
 // i*N + d; research.elamur.ai summary page, §Summary "every N-th token"), or
-// given.  Angles: inv_freq is turned once per thread into a 64-bit fraction
+// given.  Angles: inv_freq is turned once per block into a 64-bit fraction
 // of a turn, F = 2^64 * frac(inv_freq / 2 pi); p * F modulo 2^64 is then the
-// exact phase of any position (one integer multiplication, no range
-// reduction that loses bits at far positions), and its top 32 bits go to
-// sincospi, whose error is one ulp of fp32.
+// phase of position p, reduced to one turn without loss by the integer
+// multiplication.  What is left is the rounding of F, in fp64: the angle is
+// off by about 2^-53 of itself, as p * inv_freq in fp64 is (1e-6 at p = 2^33).
+// The top 32 bits of the phase go to sincospi (fp32, an error of one ulp) or
+// to the fast sine (bf16, rope_angles).
 //
 // Bound by HBM (read and write each element once: 2 or 3 element sizes an
 // element).  A group of TP threads owns a row; each thread holds two 16-byte
@@ -25,8 +27,9 @@
 // exchange is the sum for the mean.  The angles of a row are computed once
 // and serve every head of the block's chunk.  Rows are brought in by bulk
 // copies well ahead of the arithmetic (see the streamed form below).
-// Measured at B = 1, H = 32 + 8, S = 65536, D = 128, bf16: 202 us forward
-// (6.66 TB/s), 300 us backward (6.72 TB/s); a copy reaches 6.69 TB/s.
+// Measured at B = 1, H = 32 + 8, S = 65536, D = 128, bf16: 203 us forward
+// (6.61 TB/s), 301 us backward (6.69 TB/s); a copy reaches 6.69 TB/s.  fp32 at
+// D = 64, the same bytes: 200 and 305 us.
 #include <math.h>
 
 #include "common.cuh"
@@ -164,7 +167,7 @@ __device__ __forceinline__ void rope_angles(const uint64_t *freq, uint64_t pos, 
     for (int j = 0; j < VN; ++j) {
         const int32_t top = (int32_t)((pos * freq[j]) >> 32);
         const float half_turns = (float)top * 4.656612873077393e-10f;  // top / 2^31
-        // bf16 results are rounded at 2^-9 of their size: the fast
+        // bf16 results are rounded by up to 2^-8 of their size: the fast
         // instructions' 2^-21 of the pair's size on [-pi, pi] is far below
         if (sizeof(T) == 2) __sincosf(half_turns * 3.14159265f, &sn[j], &cs[j]);
         else sincospif(half_turns, &sn[j], &cs[j]);
@@ -432,8 +435,9 @@ __global__ void __launch_bounds__(256)
 // than fit at once, which would cost a whole further round (H = 32 + 8, S =
 // 65536: 285 us with 1220 blocks, 222 with 605 of 608); long sequences take
 // four rounds of shorter blocks, whose ends overlap (201 us; at S = 8192 they
-// cost 5 us in set-up).  The block count depends on the sizes only, so the
-// backward's shares, and with them dw, do not depend on the device.
+// cost 5 us in set-up).  "At once" is counted for 152 multiprocessors, not
+// asked of the device: the backward's shares, and with them the last bits of
+// dw, so depend on the sizes only.
 //
 // Rows are streamed through shared memory by bulk copies when a sequence fills
 // at least one block's rows; shorter ones (decoding: one row a request) are
