@@ -378,7 +378,8 @@ int striped_attn_window_bwd(const void *q, const void *k, const void *v, const v
  * first `sinks` positions (window = 0: all).  A token before position 0
  * (len + P < T) keeps none: o = 0, lse = -infinity.
  * bf16 with D == 64 or 128, at most 128 stripes in the striped placement,
- * zig-zag as for striped_attn_fwd, P + C + T <= 2^31 - 256; with g = H/Hkv * T
+ * zig-zag as for striped_attn_fwd, P + C + T <= 2^31 - 256, B * H * T <= 2^30
+ * and at most 2^30 key tiles over all heads; with g = H/Hkv * T
  * rows a request, Bp * ceil(B/Bp * g / 128) (P > 0) + B * ceil(g / 128)
  * <= 2048: else STRIPED_ERR_UNSUPPORTED (split the batch).
  * Segments are joined in a fixed order: results are the same from run to run

@@ -28,7 +28,7 @@
 // and serve every head of the block's chunk.  Rows are brought in by bulk
 // copies well ahead of the arithmetic (see the streamed form below).
 // Measured at B = 1, H = 32 + 8, S = 65536, D = 128, bf16: 203 us forward
-// (6.61 TB/s), 301 us backward (6.69 TB/s); a copy reaches 6.69 TB/s.  fp32 at
+// (6.61 TB/s), 299 us backward (6.73 TB/s); a copy reaches 6.69 TB/s.  fp32 at
 // D = 64, the same bytes: 200 and 305 us.
 #include <math.h>
 
