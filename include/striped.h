@@ -402,6 +402,103 @@ size_t striped_attn_decode_workspace_size(int64_t B, int64_t Bp, int64_t H, int6
                                           int64_t sinks);
 
 /*
+ * Rows of a key/value cache in 4 bits (not on the pages; a prompt that stays
+ * for decoding).  Every 32 consecutive channels of a row are a group with one
+ * scale:
+ *     s = max|x| / 7 rounded to 5 significant bits (nearest, ties to even),
+ *         0 where max|x| < 2^-100,
+ *     code = x / s rounded to the nearest whole number (ties to even),
+ * -7 .. 7, 0 where s = 0.  The value of a code is code * s, which is a bf16
+ * number.  Four bytes hold 8 consecutive channels as a little-endian 32-bit
+ * word: code + 8 of channel c of the eight at bit 16 (c mod 2) + 4 (c / 2).
+ *  k, v:              [B,Hkv,S,D] bf16 (any row order: rows keep their places);
+ *                     |x| <= 3e38, finite.
+ *  k_codes, v_codes:  [B,Hkv,S,D/2] bytes.
+ *  k_scales, v_scales:[B,Hkv,S,D/32] bf16.
+ * D a multiple of 32 up to 256 (STRIPED_ERR_UNSUPPORTED otherwise), 16-byte
+ * aligned pointers, no result overlaps another tensor of the call.
+ * striped_kv4_store writes codes and scales, striped_kv4_load their values.
+ */
+int striped_kv4_store(const void *k, const void *v, void *k_codes, void *k_scales, void *v_codes, void *v_scales,
+                      int64_t B, int64_t Hkv, int64_t S, int64_t D, int dtype, void *stream);
+int striped_kv4_load(const void *k_codes, const void *k_scales, const void *v_codes, const void *v_scales, void *k,
+                     void *v, int64_t B, int64_t Hkv, int64_t S, int64_t D, int dtype, void *stream);
+
+/*
+ * striped_attn_decode against a prompt in 4 bits, as striped_kv4_store left
+ * the rows of the prefill: k_codes, v_codes [Bp,Hkv,P,D/2] and k_scales,
+ * v_scales [Bp,Hkv,P,D/32], rows in `layout` order, P >= 1; tails as for
+ * striped_attn_decode (bf16).  The result is that of striped_attn_decode on
+ * the stored values.  Every query keeps all positions at or before it: there
+ * is no window.  Limits, lengths, order of sums, workspace and overlaps as for
+ * striped_attn_decode; with
+ * g = H/Hkv * T rows a request, ceil(B/Bp * g / 128) row tiles a prompt.
+ */
+int striped_attn_decode_kv4(const void *q, const void *k_codes, const void *k_scales, const void *v_codes,
+                            const void *v_scales, const void *k_tail, const void *v_tail, const int32_t *tail_lens,
+                            void *o, float *lse, void *workspace, size_t ws_bytes, int64_t B, int64_t Bp, int64_t H,
+                            int64_t Hkv, int64_t T, int64_t P, int64_t C, int64_t D, int N, int layout, int dtype,
+                            float scale, void *stream);
+
+/* Bytes of device workspace striped_attn_decode_kv4 needs on the current
+ * device, or 0 for arguments that it rejects. */
+size_t striped_attn_decode_kv4_workspace_size(int64_t B, int64_t Bp, int64_t H, int64_t Hkv, int64_t T, int64_t P,
+                                              int64_t C, int64_t D, int N, int layout, int dtype);
+
+/*
+ * The attention weight that every key of a prompt got (not on the pages; what
+ * striped_kv_evict goes by): over the queries at positions >= first, causal,
+ * and the query heads that share a key/value head,
+ *     weight[b,hkv,row] (+)= sum of exp(scale * q.k - lse).
+ *  q: [B,H,S,D], k: [B,Hkv,S,D], lse: [B,H,S] fp32 in `layout` order, as
+ *     striped_attn_fwd had and left them; only the queries from `first`
+ *     (0 .. S-1) on count, the others' lse is not read.
+ *  weight: [B,Hkv,S] fp32 in `layout` order: overwritten, or with
+ *     accumulate != 0 added to.
+ * A query whose lse is +infinity or -infinity (padding) counts nothing.  Queries
+ * must be finite, padding too; what a key's row holds matters to its own
+ * weight alone.
+ * bf16 with D == 64 or 128; at most 128 stripes in the striped placement,
+ * S <= 2^31 - 256, zig-zag as for striped_attn_fwd, and at most 2^30 pairs of
+ * 128-position tiles a multiprocessor: else STRIPED_ERR_UNSUPPORTED.  scale as
+ * for striped_attn_window_fwd.  Sums in a fixed order: the same from run to run
+ * (on the same kind of GPU).  workspace: 256-byte aligned, >=
+ * striped_attn_key_weight_workspace_size() bytes, contents ignored; calls that
+ * may overlap each need their own.  weight and the workspace overlap nothing.
+ */
+int striped_attn_key_weight(const void *q, const void *k, const float *lse, float *weight, void *workspace,
+                            size_t ws_bytes, int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t D, int N, int layout,
+                            int dtype, int64_t first, int accumulate, float scale, void *stream);
+
+/* Bytes of device workspace striped_attn_key_weight needs on the current
+ * device, or 0 for arguments that it rejects. */
+size_t striped_attn_key_weight_workspace_size(int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t D, int N,
+                                              int layout, int dtype, int64_t first);
+
+/*
+ * The rows of a prompt that stay in its cache (not on the pages): for every
+ * (b, hkv) the first `sinks` and the last `recent` positions, and of the
+ * others those with the largest weight, the lower position of equal ones,
+ * `keep` rows in all (NaN is below every number, -0 is 0).  They are moved
+ * together in the order of their positions: a contiguous prompt of `keep` rows
+ * for striped_attn_decode or striped_attn_decode_kv4 (N = 1, no window), whose
+ * tails go on unchanged.
+ *  x, y:      HOST arrays of n <= 4 device pointers: tensors [B,Hkv,S,row] in
+ *             `layout` order and their kept rows [B,Hkv,keep,row]; a row of
+ *             tensor i has row_bytes[i] bytes, a multiple of 4 up to 1024 (keys
+ *             and values, or their codes and scales).
+ *  weight:    [B,Hkv,S] fp32 in `layout` order.
+ *  index:     int32 [B,Hkv,keep], the kept positions in ascending order.
+ *  weight_out: [B,Hkv,keep] fp32, or NULL.
+ * 0 <= sinks, 0 <= recent, 1 <= keep, sinks + recent <= keep <= S, else
+ * STRIPED_ERR_INVALID_ARG; S <= 2^31 - 256.  Any N that divides S (zig-zag:
+ * 2 N).  No result overlaps another tensor.
+ */
+int striped_kv_evict(const void *const *x, void *const *y, const int64_t *row_bytes, int n, const float *weight,
+                     int32_t *index, float *weight_out, int64_t B, int64_t Hkv, int64_t S, int64_t keep, int64_t sinks,
+                     int64_t recent, int N, int layout, void *stream);
+
+/*
  * RMS norm of every query and key head and the rotary position rotation, in
  * one pass (not on the pages; the step between a layer's projections and its
  * attention, where every row needs the position that the placement gives

@@ -103,6 +103,16 @@ def load(build_if_missing: bool = True):
                                             I, I, I64, I64, F, P]
         lib.striped_attn_decode_workspace_size.argtypes = [I64, I64, I64, I64, I64, I64, I64, I64, I, I, I, I64, I64]
         lib.striped_attn_decode_workspace_size.restype = SZ
+        lib.striped_kv4_store.argtypes = [P, P, P, P, P, P, I64, I64, I64, I64, I, P]
+        lib.striped_kv4_load.argtypes = [P, P, P, P, P, P, I64, I64, I64, I64, I, P]
+        lib.striped_attn_decode_kv4.argtypes = [P, P, P, P, P, P, P, P, P, P, P, SZ, I64, I64, I64, I64, I64, I64, I64,
+                                                I64, I, I, I, F, P]
+        lib.striped_attn_decode_kv4_workspace_size.argtypes = [I64, I64, I64, I64, I64, I64, I64, I64, I, I, I]
+        lib.striped_attn_decode_kv4_workspace_size.restype = SZ
+        lib.striped_attn_key_weight.argtypes = [P, P, P, P, P, SZ, I64, I64, I64, I64, I64, I, I, I, I64, I, F, P]
+        lib.striped_attn_key_weight_workspace_size.argtypes = [I64, I64, I64, I64, I64, I, I, I, I64]
+        lib.striped_attn_key_weight_workspace_size.restype = SZ
+        lib.striped_kv_evict.argtypes = [P, P, P, I, P, P, P, I64, I64, I64, I64, I64, I64, I, I, P]
         lib.striped_qk_norm_rope.argtypes = [P, P, P, P, P, P, P, P, I64, I64, I64, I64, I64, I, I, I, I, I, F, I, P]
         lib.striped_qk_norm_rope_workspace_size.argtypes = [I64, I64, I64, I64, I64, I]
         lib.striped_qk_norm_rope_workspace_size.restype = SZ
@@ -646,6 +656,205 @@ def striped_attn_decode(q, k_prompt, v_prompt, k_tail, v_tail, tail_lens, N: int
         layout, code, window, sinks, 1.0 / D ** 0.5 if scale is None else scale, _raw_stream(dev)),
         "striped_attn_decode")
     return o, lse
+
+
+# ------------------------------------------------------------------ a kept prompt
+KV4_GROUP = 32  # channels that share a scale
+
+
+def striped_kv4_store(k, v, k_codes=None, k_scales=None, v_codes=None, v_scales=None, stream=None):
+    """Keys and values [B,Hkv,S,D] bf16 in 4 bits, rows in their places:
+    returns (k_codes uint8 [B,Hkv,S,D/2], k_scales bf16 [B,Hkv,S,D/32],
+    v_codes, v_scales)."""
+    _rank(k, "k", 4)
+    dev = k.get_device()
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream):
+            return striped_kv4_store(k, v, k_codes, k_scales, v_codes, v_scales)
+    B, Hkv, S, D = k.shape
+    code = _dtype_code(k)
+    cs, ss, u8, bf = (B, Hkv, S, D // 2), (B, Hkv, S, D // KV4_GROUP), torch.uint8, torch.bfloat16
+
+    def new(t, shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=k.device) if t is None else t
+
+    kc, ks, vc, vs = new(k_codes, cs, u8), new(k_scales, ss, bf), new(v_codes, cs, u8), new(v_scales, ss, bf)
+    _check(load().striped_kv4_store(
+        _need(k, "k", k.shape, k.dtype, dev), _need(v, "v", k.shape, k.dtype, dev), _need(kc, "k_codes", cs, u8, dev),
+        _need(ks, "k_scales", ss, bf, dev), _need(vc, "v_codes", cs, u8, dev), _need(vs, "v_scales", ss, bf, dev), B,
+        Hkv, S, D, code, _raw_stream(dev)), "striped_kv4_store")
+    return kc, ks, vc, vs
+
+
+def striped_kv4_load(k_codes, k_scales, v_codes, v_scales, k=None, v=None, stream=None):
+    """The values that striped_kv4_store's codes and scales stand for (bf16
+    numbers, without a further rounding): returns (k, v) [B,Hkv,S,D]."""
+    _rank(k_codes, "k_codes", 4)
+    dev = k_codes.get_device()
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream):
+            return striped_kv4_load(k_codes, k_scales, v_codes, v_scales, k, v)
+    cs = B, Hkv, S, half = k_codes.shape
+    D, u8, bf = 2 * half, torch.uint8, torch.bfloat16
+    xs, ss = (B, Hkv, S, D), (B, Hkv, S, D // KV4_GROUP)
+    k = torch.empty(xs, dtype=bf, device=k_codes.device) if k is None else k
+    v = torch.empty(xs, dtype=bf, device=k_codes.device) if v is None else v
+    _check(load().striped_kv4_load(
+        _need(k_codes, "k_codes", cs, u8, dev), _need(k_scales, "k_scales", ss, bf, dev),
+        _need(v_codes, "v_codes", cs, u8, dev), _need(v_scales, "v_scales", ss, bf, dev), _need(k, "k", xs, bf, dev),
+        _need(v, "v", xs, bf, dev), B, Hkv, S, D, BF16, _raw_stream(dev)), "striped_kv4_load")
+    return k, v
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_kv4_workspace_size(dev: int, *args) -> int:
+    return int(load().striped_attn_decode_kv4_workspace_size(*args))
+
+
+def new_decode_kv4_workspace(q, k_codes, k_tail, N: int = 1, layout: int = STRIPED) -> torch.Tensor:
+    """Workspace of striped_attn_decode_kv4 for these tensors and arguments;
+    calls that may overlap (two captured steps among them) each need their
+    own."""
+    n = _decode_sizes(q, k_codes, k_tail)
+    dev = q.get_device()
+    if not _here(dev, None):
+        with _elsewhere(dev, None):
+            return new_decode_kv4_workspace(q, k_codes, k_tail, N, layout)
+    return _work(None, _decode_kv4_workspace_size, dev, *n, N, layout, _dtype_code(q))[2]
+
+
+def striped_attn_decode_kv4(q, k_codes, k_scales, v_codes, v_scales, k_tail, v_tail, tail_lens, N: int = 1,
+                            layout: int = STRIPED, scale: float | None = None, workspace: torch.Tensor | None = None,
+                            out=None, lse_out=None, stream=None):
+    """striped_attn_decode (without a window) against a prompt in 4 bits:
+    k_codes, v_codes uint8 [Bp,Hkv,P,D/2] and k_scales, v_scales bf16
+    [Bp,Hkv,P,D/32] of striped_kv4_store in `layout` rows; q [B,H,T,D], tails
+    [B,Hkv,C,D] bf16, tail_lens int32 [B].  Returns (o [B,H,T,D], lse
+    [B,H,T])."""
+    _rank(k_codes, "k_codes", 4)
+    n = B, Bp, H, Hkv, T, P, C, D = _decode_sizes(q, k_codes, k_tail)
+    dev = q.get_device()
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream):
+            return striped_attn_decode_kv4(q, k_codes, k_scales, v_codes, v_scales, k_tail, v_tail, tail_lens, N,
+                                           layout, scale, workspace, out, lse_out)
+    dt, code, u8, bf, f32 = q.dtype, _dtype_code(q), torch.uint8, torch.bfloat16, torch.float32
+    cs, ss, tail = (Bp, Hkv, P, D // 2), (Bp, Hkv, P, D // KV4_GROUP), (B, Hkv, C, D)
+    o = torch.empty_like(q) if out is None else out
+    lse = torch.empty((B, H, T), dtype=f32, device=q.device) if lse_out is None else lse_out
+    wp, wn, workspace = _work(workspace, _decode_kv4_workspace_size, dev, *n, N, layout, code)
+    _check(load().striped_attn_decode_kv4(
+        _need(q, "q", q.shape, dt, dev), _need(k_codes, "k_codes", cs, u8, dev),
+        _need(k_scales, "k_scales", ss, bf, dev), _need(v_codes, "v_codes", cs, u8, dev),
+        _need(v_scales, "v_scales", ss, bf, dev), _need(k_tail, "k_tail", tail, dt, dev),
+        _need(v_tail, "v_tail", tail, dt, dev), _need(tail_lens, "tail_lens", (B,), torch.int32, dev),
+        _need(o, "out", q.shape, dt, dev), _need(lse, "lse_out", (B, H, T), f32, dev), wp, wn, *n, N, layout, code,
+        1.0 / D ** 0.5 if scale is None else scale, _raw_stream(dev)), "striped_attn_decode_kv4")
+    return o, lse
+
+
+@functools.lru_cache(maxsize=256)
+def _key_weight_workspace_size(dev: int, *args) -> int:
+    return int(load().striped_attn_key_weight_workspace_size(*args))
+
+
+def new_key_weight_workspace(q, k, N: int, layout: int = STRIPED, first: int = 0) -> torch.Tensor:
+    """Workspace of striped_attn_key_weight for these tensors and arguments;
+    calls that may overlap each need their own."""
+    _rank(q, "q", 4)
+    _rank(k, "k", 4)
+    dev = q.get_device()
+    if not _here(dev, None):
+        with _elsewhere(dev, None):
+            return new_key_weight_workspace(q, k, N, layout, first)
+    B, H, S, D = q.shape
+    return _work(None, _key_weight_workspace_size, dev, B, H, k.shape[1], S, D, N, layout, _dtype_code(q), first)[2]
+
+
+def striped_attn_key_weight(q, k, lse, N: int, layout: int = STRIPED, first: int = 0, scale: float | None = None,
+                            accumulate: bool = False, workspace: torch.Tensor | None = None, weight=None, stream=None):
+    """The attention weight that every key got from the queries at positions
+    >= first, over the query heads that share it: q [B,H,S,D], k [B,Hkv,S,D]
+    bf16 and the forward's lse [B,H,S] in `layout` order.  Returns weight fp32
+    [B,Hkv,S]; accumulate adds to the given one."""
+    _rank(q, "q", 4)
+    _rank(k, "k", 4)
+    if accumulate and weight is None:
+        raise ValueError("accumulate needs the weight to add to")
+    dev = q.get_device()
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream):
+            return striped_attn_key_weight(q, k, lse, N, layout, first, scale, accumulate, workspace, weight)
+    qs = B, H, S, D = q.shape
+    Hkv, dt, code, f32 = k.shape[1], q.dtype, _dtype_code(q), torch.float32
+    w = torch.empty((B, Hkv, S), dtype=f32, device=q.device) if weight is None else weight
+    wp, wn, workspace = _work(workspace, _key_weight_workspace_size, dev, B, H, Hkv, S, D, N, layout, code, first)
+    _check(load().striped_attn_key_weight(
+        _need(q, "q", qs, dt, dev), _need(k, "k", (B, Hkv, S, D), dt, dev), _need(lse, "lse", (B, H, S), f32, dev),
+        _need(w, "weight", (B, Hkv, S), f32, dev), wp, wn, B, H, Hkv, S, D, N, layout, code, first,
+        1 if accumulate else 0, 1.0 / D ** 0.5 if scale is None else scale, _raw_stream(dev)),
+        "striped_attn_key_weight")
+    return w
+
+
+def _evict(tensors, names, weight, keep, sinks, recent, N, layout, outs, index, weight_out):
+    """striped_kv_evict of tensors [B,Hkv,S,row] whose rows begin on 4 bytes."""
+    dev = weight.get_device()
+    B, Hkv, S = weight.shape
+    f32, i32, n = torch.float32, torch.int32, len(tensors)
+    outs = [torch.empty((B, Hkv, keep, t.shape[-1]), dtype=t.dtype, device=t.device) if o is None else o
+            for t, o in zip(tensors, outs)]
+    index = torch.empty((B, Hkv, keep), dtype=i32, device=weight.device) if index is None else index
+    weight_out = torch.empty((B, Hkv, keep), dtype=f32, device=weight.device) if weight_out is None else weight_out
+    xs = [_need(t, m, (B, Hkv, S, t.shape[-1]), t.dtype, dev) for t, m in zip(tensors, names)]
+    ys = [_need(o, m + "_out", (B, Hkv, keep, t.shape[-1]), t.dtype, dev) for t, o, m in zip(tensors, outs, names)]
+    rows = [t.shape[-1] * t.element_size() for t in tensors]
+    _check(load().striped_kv_evict(
+        (ctypes.c_void_p * n)(*xs), (ctypes.c_void_p * n)(*ys), (ctypes.c_int64 * n)(*rows), n,
+        _need(weight, "weight", (B, Hkv, S), f32, dev), _need(index, "index", (B, Hkv, keep), i32, dev),
+        _need(weight_out, "weight_out", (B, Hkv, keep), f32, dev), B, Hkv, S, keep, sinks, recent, N, layout,
+        _raw_stream(dev)), "striped_kv_evict")
+    return (*outs, index, weight_out)
+
+
+def _kept(keep, weight):
+    _rank(weight, "weight", 3)
+    if keep < 1:
+        raise StripedError(-1, "striped_kv_evict")
+    return weight.get_device()
+
+
+def striped_kv_evict(k, v, weight, keep: int, sinks: int = 0, recent: int = 0, N: int = 1, layout: int = STRIPED,
+                     k_out=None, v_out=None, index=None, weight_out=None, stream=None):
+    """The rows of k and v [B,Hkv,S,D] in `layout` order that stay: the first
+    `sinks`, the last `recent` and the heaviest others by weight fp32
+    [B,Hkv,S], `keep` in all, in the order of their positions (a contiguous
+    prompt: N = 1).  Returns (k_out, v_out [B,Hkv,keep,D], index int32
+    [B,Hkv,keep], the kept positions, weight_out fp32 [B,Hkv,keep])."""
+    _rank(k, "k", 4)
+    _rank(v, "v", 4)
+    dev = _kept(keep, weight)
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream):
+            return striped_kv_evict(k, v, weight, keep, sinks, recent, N, layout, k_out, v_out, index, weight_out)
+    return _evict((k, v), ("k", "v"), weight, keep, sinks, recent, N, layout, (k_out, v_out), index, weight_out)
+
+
+def striped_kv4_evict(k_codes, k_scales, v_codes, v_scales, weight, keep: int, sinks: int = 0, recent: int = 0,
+                      N: int = 1, layout: int = STRIPED, k_codes_out=None, k_scales_out=None, v_codes_out=None,
+                      v_scales_out=None, index=None, weight_out=None, stream=None):
+    """striped_kv_evict of rows in 4 bits, as they are.  Returns (k_codes,
+    k_scales, v_codes, v_scales, index, weight) of the kept rows."""
+    rows = (k_codes, k_scales, v_codes, v_scales)
+    names = ("k_codes", "k_scales", "v_codes", "v_scales")
+    for t, m in zip(rows, names):
+        _rank(t, m, 4)
+    dev = _kept(keep, weight)
+    outs = (k_codes_out, k_scales_out, v_codes_out, v_scales_out)
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream):
+            return striped_kv4_evict(*rows, weight, keep, sinks, recent, N, layout, *outs, index, weight_out)
+    return _evict(rows, names, weight, keep, sinks, recent, N, layout, outs, index, weight_out)
 
 
 # ------------------------------------------------------------------ norm and rotation

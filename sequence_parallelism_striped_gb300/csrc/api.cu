@@ -715,6 +715,148 @@ int striped_attn_decode(const void *q, const void *k_prompt, const void *v_promp
                             (cudaStream_t)stream);
 }
 
+size_t striped_attn_decode_kv4_workspace_size(int64_t B, int64_t Bp, int64_t H, int64_t Hkv, int64_t T, int64_t P,
+                                              int64_t C, int64_t D, int N, int layout, int dtype) {
+    const DecodeArgs a{B, Bp, H, Hkv, T, P, C, D, N, layout, 0, 0, 1.f, true};
+    return P < 1 || check_decode(a, dtype) ? 0 : decode_workspace(a);
+}
+
+int striped_attn_decode_kv4(const void *q, const void *k_codes, const void *k_scales, const void *v_codes,
+                            const void *v_scales, const void *k_tail, const void *v_tail, const int32_t *tail_lens,
+                            void *o, float *lse, void *workspace, size_t ws_bytes, int64_t B, int64_t Bp, int64_t H,
+                            int64_t Hkv, int64_t T, int64_t P, int64_t C, int64_t D, int N, int layout, int dtype,
+                            float scale, void *stream) {
+    if (!q || !k_codes || !k_scales || !v_codes || !v_scales || !k_tail || !v_tail || !tail_lens || !o || !lse || P < 1)
+        return STRIPED_ERR_INVALID_ARG;
+    const DecodeArgs a{B, Bp, H, Hkv, T, P, C, D, N, layout, 0, 0, scale, true};
+    const int st = check_decode(a, dtype);
+    if (st) return st;
+    const size_t need = decode_workspace(a);
+    if (!workspace || ws_bytes < need) return STRIPED_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return STRIPED_ERR_ALIGN;
+    const void *ptrs[9] = {q, k_codes, k_scales, v_codes, v_scales, k_tail, v_tail, o, lse};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return STRIPED_ERR_ALIGN;
+    if ((reinterpret_cast<uintptr_t>(tail_lens) & 3u) != 0) return STRIPED_ERR_ALIGN;
+    const int64_t nq = B * H * T * D * 2, rows = Bp * Hkv * P, nt = B * Hkv * C * D * 2;
+    const Range out[3] = {{o, nq}, {lse, B * H * T * 4}, {workspace, (int64_t)need}};
+    const Range in[8] = {{q, nq},           {k_codes, rows * D / 2}, {k_scales, rows * D / 16}, {v_codes, rows * D / 2},
+                         {v_scales, rows * D / 16}, {k_tail, nt},    {v_tail, nt},              {tail_lens, B * 4}};
+    if (results_overlap(out, 3, in, 8)) return STRIPED_ERR_INVALID_ARG;
+    const Kv4Prompt prompt{k_codes, k_scales, v_codes, v_scales};
+    return launch_decode_kv4(q, prompt, k_tail, v_tail, tail_lens, o, lse, workspace, a, (cudaStream_t)stream);
+}
+
+// ---------------------------------------------------------------- a kept prompt
+static int check_kv4(const void *const *in, void *const *out, int n_in, int n_out, int64_t B, int64_t Hkv, int64_t S,
+                     int64_t D, int dtype) {
+    const int st = check_sizes(B, Hkv, S, D, 1);
+    if (st) return st;
+    if (dtype != STRIPED_BF16) return dtype == STRIPED_FP32 ? STRIPED_ERR_UNSUPPORTED : STRIPED_ERR_INVALID_ARG;
+    if (D % 32 != 0 || D > 256 || B * Hkv * S > kMaxRows) return STRIPED_ERR_UNSUPPORTED;
+    for (int i = 0; i < n_in; ++i)
+        if (!aligned16(in[i])) return STRIPED_ERR_ALIGN;
+    for (int i = 0; i < n_out; ++i)
+        if (!aligned16(out[i])) return STRIPED_ERR_ALIGN;
+    return STRIPED_OK;
+}
+
+int striped_kv4_store(const void *k, const void *v, void *k_codes, void *k_scales, void *v_codes, void *v_scales,
+                      int64_t B, int64_t Hkv, int64_t S, int64_t D, int dtype, void *stream) {
+    const void *in[2] = {k, v};
+    void *out[4] = {k_codes, k_scales, v_codes, v_scales};
+    if (!k || !v || !k_codes || !k_scales || !v_codes || !v_scales) return STRIPED_ERR_INVALID_ARG;
+    const int st = check_kv4(in, out, 2, 4, B, Hkv, S, D, dtype);
+    if (st) return st;
+    const int64_t rows = B * Hkv * S, nx = rows * D * 2, nc = rows * D / 2, ns = rows * D / 16;
+    const Range results[4] = {{k_codes, nc}, {k_scales, ns}, {v_codes, nc}, {v_scales, ns}}, given[2] = {{k, nx}, {v, nx}};
+    if (results_overlap(results, 4, given, 2)) return STRIPED_ERR_INVALID_ARG;
+    return launch_kv4(const_cast<void *>(k), k_codes, k_scales, const_cast<void *>(v), v_codes, v_scales, rows, D, true,
+                      (cudaStream_t)stream);
+}
+
+int striped_kv4_load(const void *k_codes, const void *k_scales, const void *v_codes, const void *v_scales, void *k,
+                     void *v, int64_t B, int64_t Hkv, int64_t S, int64_t D, int dtype, void *stream) {
+    const void *in[4] = {k_codes, k_scales, v_codes, v_scales};
+    void *out[2] = {k, v};
+    if (!k || !v || !k_codes || !k_scales || !v_codes || !v_scales) return STRIPED_ERR_INVALID_ARG;
+    const int st = check_kv4(in, out, 4, 2, B, Hkv, S, D, dtype);
+    if (st) return st;
+    const int64_t rows = B * Hkv * S, nx = rows * D * 2, nc = rows * D / 2, ns = rows * D / 16;
+    const Range results[2] = {{k, nx}, {v, nx}}, given[4] = {{k_codes, nc}, {k_scales, ns}, {v_codes, nc}, {v_scales, ns}};
+    if (results_overlap(results, 2, given, 4)) return STRIPED_ERR_INVALID_ARG;
+    return launch_kv4(k, const_cast<void *>(k_codes), const_cast<void *>(k_scales), v, const_cast<void *>(v_codes),
+                      const_cast<void *>(v_scales), rows, D, false, (cudaStream_t)stream);
+}
+
+static int check_key_weight(const KeyWeightArgs &a, int dtype) {
+    if (a.Hkv < 1 || a.H < 1 || a.H % a.Hkv != 0 || a.first < 0 || a.first >= a.S || !valid_scale(a.scale))
+        return STRIPED_ERR_INVALID_ARG;
+    const int st = check_attn(a.B, a.H, a.S, a.D, a.N, a.layout, dtype);
+    if (st) return st;
+    if (a.B * a.H * a.S > kMaxRows || dtype != STRIPED_BF16 || a.S > kMaxPositions) return STRIPED_ERR_UNSUPPORTED;
+    if (a.layout == STRIPED_LAYOUT_STRIPED && a.N > 128) return STRIPED_ERR_UNSUPPORTED;
+    return key_weight_workspace(a) == 0 ? STRIPED_ERR_UNSUPPORTED : STRIPED_OK;
+}
+
+size_t striped_attn_key_weight_workspace_size(int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t D, int N,
+                                              int layout, int dtype, int64_t first) {
+    const KeyWeightArgs a{B, H, Hkv, S, D, N, layout, first, 1.f, 0};
+    return check_key_weight(a, dtype) ? 0 : align256(key_weight_workspace(a));
+}
+
+int striped_attn_key_weight(const void *q, const void *k, const float *lse, float *weight, void *workspace,
+                            size_t ws_bytes, int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t D, int N, int layout,
+                            int dtype, int64_t first, int accumulate, float scale, void *stream) {
+    if (!q || !k || !lse || !weight) return STRIPED_ERR_INVALID_ARG;
+    const KeyWeightArgs a{B, H, Hkv, S, D, N, layout, first, scale, accumulate ? 1 : 0};
+    const int st = check_key_weight(a, dtype);
+    if (st) return st;
+    const size_t need = key_weight_workspace(a);
+    if (!workspace || ws_bytes < need) return STRIPED_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return STRIPED_ERR_ALIGN;
+    const void *ptrs[4] = {q, k, lse, weight};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return STRIPED_ERR_ALIGN;
+    const Range out[2] = {{weight, B * Hkv * S * 4}, {workspace, (int64_t)need}};
+    const Range in[3] = {{q, B * H * S * D * 2}, {k, B * Hkv * S * D * 2}, {lse, B * H * S * 4}};
+    if (results_overlap(out, 2, in, 3)) return STRIPED_ERR_INVALID_ARG;
+    return launch_tc_key_weight(q, k, lse, weight, workspace, a, (cudaStream_t)stream);
+}
+
+int striped_kv_evict(const void *const *x, void *const *y, const int64_t *row_bytes, int n, const float *weight,
+                     int32_t *index, float *weight_out, int64_t B, int64_t Hkv, int64_t S, int64_t keep, int64_t sinks,
+                     int64_t recent, int N, int layout, void *stream) {
+    if (n < 0 || (n > 0 && (!x || !y || !row_bytes)) || !weight || !index) return STRIPED_ERR_INVALID_ARG;
+    const int st = check_sizes(B, Hkv, S, 1, N);
+    if (st) return st;
+    if (!valid_layout(layout) || (layout == STRIPED_LAYOUT_ZIGZAG && S % (2 * (int64_t)N) != 0))
+        return STRIPED_ERR_INVALID_ARG;
+    if (keep < 1 || keep > S || sinks < 0 || recent < 0 || sinks > keep || recent > keep - sinks)
+        return STRIPED_ERR_INVALID_ARG;
+    if (n > kEvictTensors || S > kMaxPositions || B * Hkv * S > kMaxRows) return STRIPED_ERR_UNSUPPORTED;
+    EvictArgs e{};
+    e.n = n;
+    const int64_t lines = B * Hkv;
+    Range out[kEvictTensors + 2] = {{index, lines * keep * 4}, {weight_out, lines * keep * 4}};
+    Range in[kEvictTensors + 1] = {{weight, lines * S * 4}};
+    if (((reinterpret_cast<uintptr_t>(weight) | reinterpret_cast<uintptr_t>(index) |
+          reinterpret_cast<uintptr_t>(weight_out)) & 3u) != 0)
+        return STRIPED_ERR_ALIGN;
+    for (int i = 0; i < n; ++i) {
+        if (!x[i] || !y[i] || row_bytes[i] < 1) return STRIPED_ERR_INVALID_ARG;
+        if (row_bytes[i] > 1024 || row_bytes[i] % 4 != 0) return STRIPED_ERR_UNSUPPORTED;
+        if (!aligned16(x[i]) || !aligned16(y[i])) return STRIPED_ERR_ALIGN;
+        e.x[i] = x[i], e.y[i] = y[i], e.row_bytes[i] = row_bytes[i];
+        in[i + 1] = {x[i], lines * S * row_bytes[i]};
+        out[i + 2] = {y[i], lines * keep * row_bytes[i]};
+    }
+    if (results_overlap(out, n + 2, in, n + 1)) return STRIPED_ERR_INVALID_ARG;
+    e.weight = weight, e.weight_out = weight_out, e.index = index;
+    e.lines = lines, e.S = S, e.keep = keep, e.sinks = sinks, e.recent = recent, e.N = N, e.layout = layout;
+    return launch_kv_evict(e, (cudaStream_t)stream);
+}
+
 // ---------------------------------------------------------------- norm and rotation
 constexpr int64_t kMaxRopeHeads = 1 << 16;  // a block row of the grid per eight of them, for both tensors
 

@@ -46,19 +46,22 @@
 // softmax, product and join.
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
+#include "decode.cuh"
 #include "internal.h"
+#include "kv4.cuh"
 #include "window.cuh"
 
 namespace striped {
 
 namespace {
 
-constexpr int DT = 128;                 // rows and keys of a tile
 constexpr uint32_t kDBox = 128 * 128;   // 128 rows x 64 bf16
 constexpr int kDThreads = 192;
+constexpr int kDThreads4 = kDThreads + 128;
 constexpr float kDRescale = 8.0f;       // lazy rescale threshold, log2 units
-constexpr int kMaxEntries = 2048;       // row tiles of prompts and tails, over one key/value head
 
 template <int HD>
 struct DecCfg {
@@ -80,100 +83,11 @@ struct DecBars {
     int scan[kDThreads / 32];
 };
 
-struct DecParams {
-    PosGeom g;            // the prompt (S = 0 positions if there is none)
-    int P;                // prompt positions
-    int B, R, H, Hkv, G, T, C;
-    int W, sinks;         // W = 0: no window
-    int rows_p, rows_t;   // query rows over a prompt / a tail
-    int nrt_p, nrt_t;     // their row tiles
-    int ep, entries;      // prompt entries, all entries
-    float scale;
-    const __nv_bfloat16 *q;
-    const int32_t *lens;
-    __nv_bfloat16 *o;
-    float *lse;
-    int over;             // what beginning an item costs, in key tiles
-    int32_t *cum;         // [entries + 1] cost of the entries before each one (over one key/value head)
-    float *part_o[2], *part_ml[2];  // prompt and tail slots: [slot][rows][D], [slot][rows][m, l]
-    int slot_rows[2];
-    WaitCtl wc;
-};
-
-// The key tiles that an entry's rows need: ns sink tiles, then lo, lo + 1, ..
-struct Span {
-    int ns, lo, n;
-};
-
-__device__ __forceinline__ int len_of(const DecParams &p, int b) {
-    return min(max(p.lens[b], 0), p.C);
-}
-
-__device__ __forceinline__ Span span_of(int first, int last, int tile, int sinks, int rows) {
-    // first .. last: the keys between the lowest window edge and the highest
-    // query; sinks of `rows` keys stay visible below it
-    first = max(first, 0);
-    last = min(last, rows - 1);
-    const int nst = (min(max(sinks, 0), rows) + tile - 1) / tile;
-    if (last < first) return Span{nst, 0, nst};
-    const int lo = first / tile, ns = min(nst, lo);
-    return Span{ns, lo, ns + last / tile - lo + 1};
-}
-
-__device__ Span entry_span(const DecParams &p, int e) {
-    if (e < p.ep) {
-        if (p.W == 0) return Span{0, 0, p.g.nt};
-        const int bp = e / p.nrt_p, rt = e - bp * p.nrt_p;
-        const int per = p.G * p.T;
-        const int j0 = rt * DT / per, j1 = min((rt * DT + DT - 1) / per, p.R - 1);
-        int shortest = 0x7fffffff, longest = 0;
-        for (int j = j0; j <= j1; ++j) {
-            const int n = len_of(p, bp * p.R + j);
-            shortest = min(shortest, n);
-            longest = max(longest, n);
-        }
-        return span_of(p.P + shortest - p.T - p.W + 1, p.P + longest - 1, p.g.P, p.sinks, p.P);
-    }
-    const int n = len_of(p, (e - p.ep) / p.nrt_t);
-    const int first = p.W == 0 ? 0 : n - p.T - p.W + 1;
-    return span_of(first, n - 1, DT, p.sinks - p.P, n);
-}
-
-// Share of CTA c of `parts`: tiles [share(c), share(c + 1)).
-__device__ __forceinline__ int share(int64_t total, int c, int parts) { return (int)(total * c / parts); }
-
-// One stretch of an item inside a CTA's share [x, x1) of the costs; every item
-// costs `over` and then one per key tile.
-struct Segment {
-    int e, hkv, t0, t1, nt;  // entry, key/value head, tiles t0 .. t1-1 of the entry's nt (none if t1 <= t0)
-    int next;                // where the next segment begins
-    Span s;
-};
-
-__device__ __forceinline__ Segment segment_at(const int *cum, const int *lo, const int *ns, int entries, int hkv_n,
-                                              int over, int x, int x1) {
-    int a = 0, b = entries - 1;  // last entry that begins at or below x (entries without tiles are passed over)
-    while (a < b) {
-        const int m = (a + b + 1) >> 1;
-        if (cum[m] * hkv_n <= x) a = m;
-        else b = m - 1;
-    }
-    Segment s;
-    s.e = a;
-    const int cost = cum[a + 1] - cum[a];
-    const int in = x - cum[a] * hkv_n;
-    s.hkv = in / cost;
-    s.nt = cost - over;
-    const int off = in - s.hkv * cost;
-    s.t0 = max(0, off - over);
-    s.t1 = min(s.nt, off + (x1 - x) - over);
-    s.next = min(x1, x + cost - off);
-    s.s = Span{ns[a], lo[a], s.nt};
-    return s;
-}
-
-template <int HD>
-__global__ void __launch_bounds__(kDThreads, 1)
+// KV4: the prompt is in 4 bits.  Four more warps make its tiles: thread t takes
+// the codes and scales of key row t from memory, a tile ahead, and writes the
+// values, which are bf16 numbers, where TMA puts the rows of a bf16 prompt.
+template <int HD, bool KV4>
+__global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
     tc_decode_kernel(const __grid_constant__ CUtensorMap tmKp, const __grid_constant__ CUtensorMap tmVp,
                      const __grid_constant__ CUtensorMap tmKt, const __grid_constant__ CUtensorMap tmVt,
                      const DecParams p) {
@@ -194,7 +108,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&bars->q_full), 4);
         for (int s = 0; s < NS; ++s) {
-            mbar_init(smem_u32(&bars->kv_full[s]), 1);
+            mbar_init(smem_u32(&bars->kv_full[s]), KV4 ? 5 : 1);
             mbar_init(smem_u32(&bars->kv_empty[s]), 1);
         }
         mbar_init(smem_u32(&bars->s_full[0]), 1);
@@ -208,7 +122,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
         tmem_alloc(smem_u32(&bars->tmem_slot), 512);
         tmem_relinquish();
     }
-    if (p.ep > 0 && g.P < DT) {
+    if (!KV4 && p.ep > 0 && g.P < DT) {
         // rows past a prompt tile's positions are never loaded: V has to be
         // finite there, because P = 0 times it is added to O
         for (uint32_t i = threadIdx.x * 16; i < NS * kStage; i += kDThreads * 16)
@@ -217,7 +131,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
     }
     // every entry's span, and the running count of key tiles before it
     {
-        const int per = (p.entries + kDThreads - 1) / kDThreads;
+        const int per = (p.entries + kDThreads - 1) / kDThreads;  // the first kDThreads threads have some
         const int e0 = min((int)threadIdx.x * per, p.entries), e1 = min(e0 + per, p.entries);
         int sum = 0;
         for (int e = e0; e < e1; ++e) {
@@ -232,10 +146,10 @@ __global__ void __launch_bounds__(kDThreads, 1)
             const int v = __shfl_up_sync(0xffffffffu, run, o);
             if (lane >= o) run += v;
         }
-        if (lane == 31) bars->scan[warp] = run;
+        if (lane == 31 && warp < kDThreads / 32) bars->scan[warp] = run;
         __syncthreads();
         int before = run - sum;
-        for (int w = 0; w < warp; ++w) before += bars->scan[w];
+        for (int w = 0; w < min(warp, kDThreads / 32); ++w) before += bars->scan[w];
         for (int e = e0; e < e1; ++e) {
             cum[e + 1] += before;
             if (blockIdx.x == 0) p.cum[e + 1] = cum[e + 1];
@@ -291,6 +205,10 @@ __global__ void __launch_bounds__(kDThreads, 1)
                 const TileAt at = tail ? TileAt{kt * DT, 0} : tile_at(g, kt);
                 const uint32_t fb = smem_u32(&bars->kv_full[s]);
                 const uint32_t kdst = sbase + s * kStage, vdst = kdst + kTile;
+                if (KV4 && !tail) {
+                    mbar_arrive(fb);  // the dequantising warps write this tile
+                    continue;
+                }
                 mbar_arrive_expect_tx(fb, bytes);
 #pragma unroll
                 for (int c = 0; c < kBoxes; ++c) {
@@ -358,6 +276,85 @@ __global__ void __launch_bounds__(kDThreads, 1)
         // every MMA issued above completes before TMEM is freed (error paths)
         if (leader) mma_commit(smem_u32(&bars->drain));
         mbar_wait_warp(smem_u32(&bars->drain), 0, p.wc);
+    } else if (KV4 && warp >= kDThreads / 32 && nx > 0) {
+        // ---------------- 4 bits -> bf16
+        const int r = threadIdx.x - kDThreads;  // key row of the tile
+        constexpr int V = HD / 32;              // groups of a row: 16 bytes of codes, one scale
+        using Scales = typename std::conditional<HD == 128, uint2, uint32_t>::type;
+        // the stored row of this thread in the tile that is read next
+        int64_t at = -1;
+        uint4 kc[V], vc[V];
+        Scales ks{}, vs{};
+        auto fetch = [&]() {
+            if (at < 0) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) kc[i] = vc[i] = make_uint4(0u, 0u, 0u, 0u);
+                ks = vs = Scales{};
+                return;
+            }
+            const uint4 *k = reinterpret_cast<const uint4 *>(p.k_codes) + at * V;
+            const uint4 *v = reinterpret_cast<const uint4 *>(p.v_codes) + at * V;
+#pragma unroll
+            for (int i = 0; i < V; ++i) kc[i] = __ldg(k + i), vc[i] = __ldg(v + i);
+            ks = __ldg(reinterpret_cast<const Scales *>(p.k_scales) + at);
+            vs = __ldg(reinterpret_cast<const Scales *>(p.v_scales) + at);
+        };
+        auto put = [&](uint8_t *tile, const uint4 (&c)[V], const Scales &sc) {
+            const uint32_t *sw = reinterpret_cast<const uint32_t *>(&sc);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const uint32_t s2 = __byte_perm(sw[i / 2], 0, i % 2 ? 0x3232 : 0x1010);
+                const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int chunk = 4 * i + k;  // 8 channels
+                    *reinterpret_cast<uint4 *>(tile + chunk / 8 * kDBox + r * 128 + (((chunk & 7) ^ (r & 7)) * 16)) =
+                        make_uint4(bf16x2_mul(kv4_codes(w[k], 0), s2), bf16x2_mul(kv4_codes(w[k], 1), s2),
+                                   bf16x2_mul(kv4_codes(w[k], 2), s2), bf16x2_mul(kv4_codes(w[k], 3), s2));
+                }
+            }
+        };
+        // walks over the prompt tiles of this CTA, one ahead of the writing
+        int fx = x0, ft = 0;
+        Segment fs{};
+        fs.t1 = 0;
+        auto advance = [&]() {
+            at = -1;
+            ++ft;
+            while (ft >= fs.t1) {
+                if (fx >= x1) return false;
+                fs = segment(fx);
+                fx = fs.next;
+                ft = fs.e < p.ep ? fs.t0 : fs.t1;  // tails are not ours
+            }
+            const int row = ft * DT + r;
+            if (row < p.P) at = ((int64_t)(fs.e / p.nrt_p) * p.Hkv + fs.hkv) * p.P + row;
+            return true;
+        };
+        if (advance()) fetch();
+        int j = 0;
+        bool ok = true;
+        for (int x = x0; x < x1 && ok;) {
+            const Segment sg = segment(x);
+            x = sg.next;
+            const bool tail = sg.e >= p.ep;
+            for (int t = sg.t0; t < sg.t1; ++t, ++j) {
+                const int s = j % NS;
+                if (j >= NS && !mbar_wait_warp(smem_u32(&bars->kv_empty[s]), ((j / NS) + 1) & 1, p.wc)) {
+                    ok = false;
+                    break;
+                }
+                if (!tail) {
+                    uint8_t *tile = smem + s * kStage;
+                    put(tile, kc, ks);
+                    put(tile + kTile, vc, vs);
+                    if (advance()) fetch();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(smem_u32(&bars->kv_full[s]));
+            }
+        }
     } else if (warp >= 2 && nx > 0) {
         // ---------------- softmax + partial results
         const int quarter = warp & 3;
@@ -469,7 +466,21 @@ __global__ void __launch_bounds__(kDThreads, 1)
                         }
                     }
                     const bool full = tile_w == DT && kbase + DT - 1 <= hi && (kbase >= lo || kbase + DT <= sk);
-                    if (!__all_sync(0xffffffffu, full)) {
+                    if (KV4 && !tail && __any_sync(0xffffffffu, qpos < p.P - 1)) {
+                        // a query inside a 4-bit prompt: row by row, by position
+#pragma unroll
+                        for (int w = 0; w < DT / 32; ++w) {
+                            uint32_t k = 0;
+#pragma unroll 1
+                            for (int c = 0; c < 32; ++c) {
+                                const int row = kbase + 32 * w + c;
+                                if (row < p.P && row_position(p, row) <= qpos) k |= 1u << c;
+                            }
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (!(k & (1u << c))) sv[32 * w + c] = -INFINITY;
+                        }
+                    } else if (!__all_sync(0xffffffffu, full)) {
                         // columns past the tile's positions are never kept
                         const int h2 = min(hi - kbase, tile_w - 1), l2 = lo - kbase, s2 = sk - kbase;
 #pragma unroll
@@ -568,195 +579,26 @@ __global__ void __launch_bounds__(kDThreads, 1)
     }
 }
 
-// o and lse of every row from its segments: those of its prompt's row tile,
-// then those of its tail's.  One block per row; warp w takes every fourth
-// segment from the w-th on, eight loads in flight, and the four are added in
-// order.
-template <int HD>
-__global__ void __launch_bounds__(128) decode_join_kernel(const DecParams p, int grid) {
-    wait_for_previous();
-    constexpr int E = HD / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row = blockIdx.x;  // (b, h, t)
-    const int t = (int)(row % p.T);
-    const int64_t bh = row / p.T;
-    const int b = (int)(bh / p.H), h = (int)(bh % p.H), hkv = h / p.G;
-    const int64_t total = (int64_t)p.cum[p.entries] * p.Hkv, parts = min((int64_t)grid, total);
-    // first slot and count of the row's segments: prompt, tail
-    int64_t at[2];
-    int n[2];
-#pragma unroll
-    for (int tail = 0; tail < 2; ++tail) {
-        const int in = (h % p.G) * p.T + t;
-        const int r = tail ? in : (b % p.R) * p.G * p.T + in;
-        const int e = (tail ? p.ep + b * p.nrt_t : b / p.R * p.nrt_p) + r / DT;
-        n[tail] = 0;
-        at[tail] = 0;
-        if (!tail && p.ep == 0) continue;
-        const int cost = p.cum[e + 1] - p.cum[e];
-        if (cost == 0) continue;
-        const int64_t first = (int64_t)p.cum[e] * p.Hkv + (int64_t)hkv * cost + p.over;  // its tile 0
-        const int64_t last = first + cost - p.over - 1;
-        const int c0 = (int)(((first + 1) * parts - 1) / total), c1 = (int)(((last + 1) * parts - 1) / total);
-        n[tail] = c1 - c0 + 1;
-        at[tail] = (int64_t)((tail ? e - p.ep : e) * p.Hkv + hkv + c0) * p.slot_rows[tail] + r % DT;
-    }
-    float m = -INFINITY, l = 0.f, acc[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] = 0.f;
-    const int all = n[0] + n[1];
-    constexpr int U = 8;
-    for (int s0 = warp; s0 < all; s0 += 4 * U) {
-        float2 ml[U];
-        float v[U][E];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int s = s0 + 4 * u, tail = s >= n[0];
-            ml[u] = make_float2(-INFINITY, 0.f);
-            if (s < all) {
-                const int64_t slot = at[tail] + (int64_t)(s - (tail ? n[0] : 0)) * p.slot_rows[tail];
-                ml[u] = *reinterpret_cast<const float2 *>(p.part_ml[tail] + 2 * slot);
-                const float *src = p.part_o[tail] + slot * HD + lane * E;
-                if constexpr (E == 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(src);
-                    v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][3] = x.w;
-                } else {
-                    const float2 x = *reinterpret_cast<const float2 *>(src);
-                    v[u][0] = x.x, v[u][1] = x.y;
-                }
-            }
-        }
-        float m_new = m;
-#pragma unroll
-        for (int u = 0; u < U; ++u) m_new = fmaxf(m_new, ml[u].x);
-        if (m_new == -INFINITY) continue;
-        const float old = ex2(m - m_new);
-        l *= old;
-#pragma unroll
-        for (int i = 0; i < E; ++i) acc[i] *= old;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (ml[u].x == -INFINITY) continue;  // no key kept, or no segment
-            const float w = ex2(ml[u].x - m_new);
-            l = fmaf(ml[u].y, w, l);
-#pragma unroll
-            for (int i = 0; i < E; ++i) acc[i] = fmaf(v[u][i], w, acc[i]);
-        }
-        m = m_new;
-    }
-    __shared__ float sm[4], sl[4], sa[4][HD];
-    if (lane == 0) sm[warp] = m, sl[warp] = l;
-#pragma unroll
-    for (int i = 0; i < E; ++i) sa[warp][lane * E + i] = acc[i];
-    __syncthreads();
-    m = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-    float w[4];
-    l = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        w[i] = sm[i] == -INFINITY ? 0.f : ex2(sm[i] - m);
-        l = fmaf(sl[i], w[i], l);
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    if (threadIdx.x == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-    if (threadIdx.x < HD / 2) {
-        float o2[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int d = 2 * threadIdx.x + k;
-            o2[k] = ((sa[0][d] * w[0] + sa[1][d] * w[1]) + (sa[2][d] * w[2] + sa[3][d] * w[3])) * inv;
-        }
-        reinterpret_cast<uint32_t *>(p.o + row * HD)[threadIdx.x] = pack_bf16x2(o2[0], o2[1]);
-    }
-}
-
-struct DecPlan {
-    DecParams p;
-    int parts;
-    size_t cum_bytes, ml_bytes[2], o_bytes[2];
-};
-
-bool decode_plan(DecPlan *plan, const DecodeArgs &a) {
-    DecParams &p = plan->p;
-    p = DecParams{};
-    if (a.P > 0 && !pos_geom(&p.g, a.P, a.N, a.layout)) return false;
-    p.P = (int)a.P;
-    p.B = (int)a.B;
-    p.R = (int)(a.B / a.Bp);
-    p.H = (int)a.H;
-    p.Hkv = (int)a.Hkv;
-    p.G = (int)(a.H / a.Hkv);
-    p.T = (int)a.T;
-    p.C = (int)a.C;
-    // a window that no query can leave is none
-    p.W = a.window >= a.P + a.C ? 0 : (int)a.window;
-    p.sinks = p.W == 0 ? 0 : (int)(a.sinks < a.P + a.C ? a.sinks : a.P + a.C);
-    const int64_t per = (int64_t)p.G * p.T, rows_p = per * p.R;
-    const int64_t nrt_p = (rows_p + DT - 1) / DT, nrt_t = (per + DT - 1) / DT;
-    const int64_t ep = a.P > 0 ? a.Bp * nrt_p : 0, entries = ep + a.B * nrt_t;
-    if (entries > kMaxEntries) return false;
-    // a segment of one tile takes about 2.8 us more than a further tile of a
-    // long one, which takes 1.35 us at D = 128 and half of that at D = 64:
-    // counted as so many tiles.  16 requests on prompts of their own of 32768,
-    // D = 128: 386 us at a cost of 1, 308 at 2, 307 at 3, 309 at 4; 24
-    // requests, window 4096, D = 64: 40.3 us at 1, 37.5 at 2, 34.8 at 4, 36.2
-    // at 6, 37.5 at 8
-    p.over = a.D == 128 ? 2 : 4;
-    const int64_t tiles =
-        (ep * (a.P > 0 ? p.g.nt + p.over : 0) + a.B * nrt_t * ((a.C + DT - 1) / DT + p.over)) * a.Hkv;
-    if (tiles > (1ll << 30)) return false;
-    p.rows_p = (int)rows_p;
-    p.rows_t = (int)per;
-    p.nrt_p = (int)nrt_p;
-    p.nrt_t = (int)nrt_t;
-    p.ep = (int)ep;
-    p.entries = (int)entries;
-    p.scale = a.scale;
-    const int sms = device_sm_count();
-    plan->parts = (int)(tiles < sms ? tiles : sms);
-    p.slot_rows[0] = (int)(rows_p < DT ? rows_p : DT);
-    p.slot_rows[1] = (int)(per < DT ? per : DT);
-    plan->cum_bytes = ((size_t)(entries + 1) * 4 + 255) & ~size_t(255);
-    for (int t = 0; t < 2; ++t) {
-        const size_t slots = (size_t)((t ? a.B * nrt_t : ep) * a.Hkv + plan->parts);
-        plan->ml_bytes[t] = (slots * p.slot_rows[t] * 8 + 255) & ~size_t(255);
-        plan->o_bytes[t] = (slots * p.slot_rows[t] * a.D * 4 + 255) & ~size_t(255);
-    }
-    return true;
-}
-
-template <int HD>
-int launch_decode_hd(const void *q, const void *kp, const void *vp, const void *kt, const void *vt,
-                     const int32_t *lens, void *o, float *lse, void *workspace, const DecodeArgs &a,
+template <int HD, bool KV4>
+int launch_decode_hd(const void *q, const void *kp, const void *vp, const Kv4Prompt &prompt, const void *kt,
+                     const void *vt, const int32_t *lens, void *o, float *lse, void *workspace, const DecodeArgs &a,
                      cudaStream_t stream) {
     static PerDeviceOnce once;
     const int attr = once.get([] {
-        return cuda_status(cudaFuncSetAttribute(tc_decode_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                (int)DecCfg<HD>::kSmemBytes));
+        return cuda_status(cudaFuncSetAttribute(
+            tc_decode_kernel<HD, KV4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)DecCfg<HD>::kSmemBytes));
     });
     if (attr != STRIPED_OK) return attr;
     DecPlan plan;
     if (!decode_plan(&plan, a)) return STRIPED_ERR_UNSUPPORTED;
     DecParams &p = plan.p;
-    p.q = static_cast<const __nv_bfloat16 *>(q);
-    p.lens = lens;
-    p.o = static_cast<__nv_bfloat16 *>(o);
-    p.lse = lse;
-    char *ws = static_cast<char *>(workspace);
-    p.cum = reinterpret_cast<int32_t *>(ws);
-    ws += plan.cum_bytes;
-    for (int t = 0; t < 2; ++t) {
-        p.part_ml[t] = reinterpret_cast<float *>(ws);
-        p.part_o[t] = reinterpret_cast<float *>(ws + plan.ml_bytes[t]);
-        ws += plan.ml_bytes[t] + plan.o_bytes[t];
-    }
-    p.wc = device_wait_ctl();
+    decode_buffers(&plan, q, prompt, lens, o, lse, workspace);
     CUtensorMap mkp, mvp, mkt, mvt;
     int st;
     if ((st = make_bf16_map(&mkt, kt, a.D, a.C, 1, a.B * a.Hkv, a.C * a.D, a.C * a.D, DT)) ||
         (st = make_bf16_map(&mvt, vt, a.D, a.C, 1, a.B * a.Hkv, a.C * a.D, a.C * a.D, DT)))
         return st;
-    if (p.ep > 0) {
+    if (p.ep > 0 && !KV4) {
         if ((st = make_pos_map(&mkp, kp, a.D, p.g, a.Bp * a.Hkv)) ||
             (st = make_pos_map(&mvp, vp, a.D, p.g, a.Bp * a.Hkv)))
             return st;
@@ -764,7 +606,8 @@ int launch_decode_hd(const void *q, const void *kp, const void *vp, const void *
         mkp = mkt;  // never read
         mvp = mvt;
     }
-    tc_decode_kernel<HD><<<plan.parts, kDThreads, DecCfg<HD>::kSmemBytes, stream>>>(mkp, mvp, mkt, mvt, p);
+    tc_decode_kernel<HD, KV4><<<plan.parts, KV4 ? kDThreads4 : kDThreads, DecCfg<HD>::kSmemBytes, stream>>>(
+        mkp, mvp, mkt, mvt, p);
     if ((st = cuda_status(cudaGetLastError()))) return st;
     return launch_after(decode_join_kernel<HD>, dim3((unsigned)(a.B * a.H * a.T)), 128, 0, stream, p, plan.parts);
 }
@@ -780,8 +623,17 @@ size_t decode_workspace(const DecodeArgs &a) {
 int launch_tc_decode(const void *q, const void *kp, const void *vp, const void *kt, const void *vt,
                      const int32_t *lens, void *o, float *lse, void *workspace, const DecodeArgs &a,
                      cudaStream_t stream) {
-    return a.D == 128 ? launch_decode_hd<128>(q, kp, vp, kt, vt, lens, o, lse, workspace, a, stream)
-                      : launch_decode_hd<64>(q, kp, vp, kt, vt, lens, o, lse, workspace, a, stream);
+    const Kv4Prompt none{};
+    return a.D == 128
+               ? launch_decode_hd<128, false>(q, kp, vp, none, kt, vt, lens, o, lse, workspace, a, stream)
+               : launch_decode_hd<64, false>(q, kp, vp, none, kt, vt, lens, o, lse, workspace, a, stream);
+}
+
+int launch_decode_kv4(const void *q, const Kv4Prompt &prompt, const void *kt, const void *vt, const int32_t *lens,
+                      void *o, float *lse, void *workspace, const DecodeArgs &a, cudaStream_t stream) {
+    return a.D == 128
+               ? launch_decode_hd<128, true>(q, nullptr, nullptr, prompt, kt, vt, lens, o, lse, workspace, a, stream)
+               : launch_decode_hd<64, true>(q, nullptr, nullptr, prompt, kt, vt, lens, o, lse, workspace, a, stream);
 }
 
 }  // namespace striped

@@ -169,11 +169,49 @@ struct DecodeArgs {
     int N, layout;
     int64_t window, sinks;  // window 0: none
     float scale;
+    bool kv4;               // the prompt is in 4 bits (window 0)
+};
+// A prompt in 4 bits: codes and scales of its rows.
+struct Kv4Prompt {
+    const void *k_codes, *k_scales, *v_codes, *v_scales;
 };
 size_t decode_workspace(const DecodeArgs &a);  // 0: no kernel for these sizes
+int launch_decode_kv4(const void *q, const Kv4Prompt &prompt, const void *kt, const void *vt, const int32_t *lens,
+                      void *o, float *lse, void *workspace, const DecodeArgs &a, cudaStream_t stream);
 int launch_tc_decode(const void *q, const void *kp, const void *vp, const void *kt, const void *vt,
                      const int32_t *lens, void *o, float *lse, void *workspace, const DecodeArgs &a,
                      cudaStream_t stream);
+
+// ---- kv4.cu: rows of two bf16 tensors to codes and scales (kv4.cuh), or back
+int launch_kv4(void *k, void *k_codes, void *k_scales, void *v, void *v_codes, void *v_scales, int64_t rows, int64_t D,
+               bool store, cudaStream_t stream);
+
+// ---- kv_evict.cu
+constexpr int kEvictTensors = 4;
+struct EvictArgs {
+    const void *x[kEvictTensors];  // [lines][S][row_bytes]
+    void *y[kEvictTensors];        // [lines][keep][row_bytes]
+    int64_t row_bytes[kEvictTensors];
+    int n;
+    const float *weight;           // [lines][S]
+    float *weight_out;             // [lines][keep] or NULL
+    int32_t *index;                // [lines][keep]
+    int64_t lines, S, keep, sinks, recent;
+    int N, layout;
+};
+int launch_kv_evict(const EvictArgs &e, cudaStream_t stream);
+
+// ---- key_weight.cu (bf16, tiles of consecutive positions, window.cuh)
+struct KeyWeightArgs {
+    int64_t B, H, Hkv, S, D;
+    int N, layout;
+    int64_t first;
+    float scale;
+    int accumulate;
+};
+size_t key_weight_workspace(const KeyWeightArgs &a);  // 0: no kernel for these sizes
+int launch_tc_key_weight(const void *q, const void *k, const float *lse, float *weight, void *workspace,
+                         const KeyWeightArgs &a, cudaStream_t stream);
 
 // ---- norm_rope.cu
 // Norm and rotation of q [B][H][S][D] and k [B][Hkv][S][D] (forward: dq_out

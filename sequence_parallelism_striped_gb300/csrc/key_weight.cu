@@ -1,0 +1,442 @@
+// key_weight.cu -- the attention weight that every key of a prompt got, summed
+// over its queries and over the query heads that share the key, bf16 on tcgen05:
+//     w[t] = sum over heads h of the group, positions p >= max(t, first) of
+//            exp(scale q_{h,p} . k_t - lse_{h,p}).
+//
+// The product is formed transposed, S^T = K Q^T: a lane of tensor memory is a
+// key, so a thread sums its key's weights over a tile's 128 queries in its own
+// registers, and nothing is exchanged until the key tile is done.  Only the
+// log-sum-exp runs along the columns; a warp of its own gathers it from the
+// placed rows into shared memory.
+//
+// Bound by the exponentials (128 x 128 of a tile: 16 a clock and quarter) beside
+// the tensor core (512 clocks a tile at D = 128); the bytes are few.  So one CTA
+// per multiprocessor, and all (key tile, head, query tile) triples of the call
+// are cut into shares of equal length, one per CTA.  A key tile whose triples
+// lie in several shares leaves partial sums, which a second kernel adds in
+// order: no atomics, the same result in every run.
+//
+//   warp 0       TMA producer: K tile of an item, Q tiles
+//   warp 1       TMEM allocator + tcgen05.mma issuer (one elected lane)
+//   warp 2       log-sum-exp of the query tiles
+//   warps 4..11  two groups that take every other tile; thread t of a group owns
+//                key t
+// Tensor memory: four S^T of 128 columns.
+#include <math.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "window.cuh"
+
+namespace striped {
+
+namespace {
+
+constexpr int KT = 128;
+constexpr uint32_t kWBox = 128 * 128;  // 128 rows x 64 bf16
+constexpr int kWtThreads = 384;
+constexpr int kSBufs = 4;
+
+template <int HD>
+struct WeightCfg {
+    static constexpr int NS = HD == 128 ? 4 : 8;  // Q stages
+    static constexpr uint32_t kTile = (HD / 64) * kWBox;
+    static constexpr uint32_t kKOff = NS * kTile;  // two K tiles
+    static constexpr uint32_t kLseOff = kKOff + 2 * kTile;
+    static constexpr uint32_t kCombOff = kLseOff + kSBufs * KT * 4;
+    static constexpr uint32_t kBarOff = kCombOff + KT * 4;
+    static constexpr size_t kSmemBytes = 1024 + kBarOff + 512;
+    static_assert(kSmemBytes <= 232448, "shared memory over the per-block limit");
+};
+
+template <int NS>
+struct WeightBars {
+    uint64_t k_full[2], k_empty[2];
+    uint64_t q_full[NS], q_empty[NS];
+    uint64_t s_full[kSBufs], s_empty[kSBufs], lse_full[kSBufs];
+    uint64_t comb_full, comb_empty, drain;
+    uint32_t tmem_slot;
+};
+
+struct WeightParams {
+    PosGeom g;
+    int64_t total;        // triples of the call
+    int parts;            // CTAs
+    int H, Hkv, G;
+    int first, f0;        // first query that counts, its tile
+    float scale;
+    int accumulate;
+    const float *lse;
+    float *weight;
+    float *part;          // [parts][2][KT]: of a CTA's first and last item
+    WaitCtl wc;
+};
+
+// Triples of a key/value head before its key tile kt, over the group's heads.
+__host__ __device__ __forceinline__ int64_t weight_before(const PosGeom &g, int f0, int G, int64_t kt) {
+    const int64_t nt = g.nt, f = f0;
+    if (kt <= f) return G * kt * (nt - f);
+    return G * (f * (nt - f) + (kt - f) * nt - (kt * (kt - 1) - f * (f - 1)) / 2);
+}
+
+__host__ __device__ __forceinline__ int64_t weight_share(const WeightParams &p, int c) {
+    return p.total / p.parts * c + p.total % p.parts * c / p.parts;
+}
+
+// The stretch [n0, n1) of the triples of one key tile that begins at x; next()
+// goes on to the one behind it.
+struct WeightItem {
+    int64_t x;
+    int line, kt;       // key/value head of the batch, key tile
+    int qlo, cnt, all;  // first query tile, query tiles, triples
+    int n0, n1;
+    __device__ __forceinline__ WeightItem(const WeightParams &p, int64_t from, int64_t x1) {
+        x = from;
+        const int64_t per = weight_before(p.g, p.f0, p.G, p.g.nt);
+        line = (int)(x / per);
+        const int64_t in = x - line * per;
+        int a = 0, b = p.g.nt - 1;
+        while (a < b) {
+            const int m = (int)(((int64_t)a + b + 1) >> 1);
+            if (weight_before(p.g, p.f0, p.G, m) <= in) a = m;
+            else b = m - 1;
+        }
+        kt = a;
+        n0 = (int)(in - weight_before(p.g, p.f0, p.G, kt));
+        sizes(p, x1);
+    }
+    __device__ __forceinline__ void next(const WeightParams &p, int64_t x1) {
+        x += n1 - n0;
+        n0 = 0;
+        if (++kt == p.g.nt) kt = 0, ++line;
+        sizes(p, x1);
+    }
+
+  private:
+    __device__ __forceinline__ void sizes(const WeightParams &p, int64_t x1) {
+        qlo = max(kt, p.f0);
+        cnt = p.g.nt - qlo;
+        all = p.G * cnt;
+        n1 = (int)min((int64_t)all, n0 + (x1 - x));
+    }
+};
+
+__device__ __forceinline__ void write_weight(const WeightParams &p, const WeightItem &it, int r, float sum) {
+    if (!tile_has(p.g, it.kt, r)) return;
+    float *dst = p.weight + (int64_t)it.line * p.g.S + tile_row(p.g, it.kt, r);
+    *dst = p.accumulate ? *dst + sum : sum;
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kWtThreads, 1)
+    tc_key_weight_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                         const WeightParams p) {
+    using Cfg = WeightCfg<HD>;
+    constexpr int NS = Cfg::NS, kBoxes = HD / 64;
+    constexpr uint32_t kTile = Cfg::kTile;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem =
+        reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    WeightBars<NS> *bars = reinterpret_cast<WeightBars<NS> *>(smem + Cfg::kBarOff);
+    float *lse_s = reinterpret_cast<float *>(smem + Cfg::kLseOff);
+    float *comb = reinterpret_cast<float *>(smem + Cfg::kCombOff);
+    const uint32_t sbase = smem_u32(smem);
+    const PosGeom &g = p.g;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&bars->k_full[i]), 1);
+            mbar_init(smem_u32(&bars->k_empty[i]), 1);
+        }
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(smem_u32(&bars->q_full[s]), 1);
+            mbar_init(smem_u32(&bars->q_empty[s]), 1);
+        }
+        for (int i = 0; i < kSBufs; ++i) {
+            mbar_init(smem_u32(&bars->s_full[i]), 1);
+            mbar_init(smem_u32(&bars->s_empty[i]), 4);
+            mbar_init(smem_u32(&bars->lse_full[i]), 1);
+        }
+        mbar_init(smem_u32(&bars->comb_full), 4);
+        mbar_init(smem_u32(&bars->comb_empty), 4);
+        mbar_init(smem_u32(&bars->drain), 1);
+        fence_barrier_init();
+    }
+    if (g.P < KT) {
+        // rows past a tile's positions are never loaded: a query there counts
+        // nothing only if its scores are finite
+        for (uint32_t i = threadIdx.x * 16; i < Cfg::kLseOff; i += kWtThreads * 16)
+            *reinterpret_cast<uint4 *>(smem + i) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&bars->tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    let_next_begin();
+    const uint32_t tmem = bars->tmem_slot;
+    const int64_t x0 = weight_share(p, blockIdx.x), x1 = weight_share(p, blockIdx.x + 1);
+    const int nx = (int)(x1 - x0);
+
+    if (warp == 0 && lane == 0) {
+        // ---------------- TMA producer
+        const bool skip_first = p.wc.inject == kInjectFwdSkipKV;  // test hook: the first K tile is never loaded
+        const uint32_t bytes = (uint32_t)g.P * 128 * kBoxes;
+        int j = 0, seg = 0;
+        bool ok = true;
+        for (WeightItem it(p, x0, x1); it.x < x1 && ok; it.next(p, x1), ++seg) {
+            const int ks = seg & 1, b = it.line / p.Hkv, hkv = it.line - b * p.Hkv;
+            if (seg >= 2 && !mbar_wait(smem_u32(&bars->k_empty[ks]), ((seg >> 1) + 1) & 1, p.wc)) {
+                ok = false;
+                break;
+            }
+            if (!(skip_first && seg == 0)) {
+                const TileAt at = tile_at(g, it.kt);
+                const uint32_t fb = smem_u32(&bars->k_full[ks]), dst = sbase + Cfg::kKOff + ks * kTile;
+                mbar_arrive_expect_tx(fb, bytes);
+#pragma unroll
+                for (int c = 0; c < kBoxes; ++c) tma_load_4d(dst + c * kWBox, &tmK, fb, 64 * c, at.c1, at.c2, it.line);
+            }
+            int head = b * p.H + hkv * p.G + it.n0 / it.cnt, qt = it.qlo + it.n0 % it.cnt;
+            for (int n = it.n0; n < it.n1; ++n, ++j) {
+                const int s = j % NS;
+                if (j >= NS && !mbar_wait(smem_u32(&bars->q_empty[s]), ((j / NS) + 1) & 1, p.wc)) {
+                    ok = false;
+                    break;
+                }
+                const TileAt at = tile_at(g, qt);
+                const uint32_t fb = smem_u32(&bars->q_full[s]), dst = sbase + s * kTile;
+                mbar_arrive_expect_tx(fb, bytes);
+#pragma unroll
+                for (int c = 0; c < kBoxes; ++c) tma_load_4d(dst + c * kWBox, &tmQ, fb, 64 * c, at.c1, at.c2, head);
+                if (++qt == g.nt) qt = it.qlo, ++head;
+            }
+        }
+        // the last load of each stage has landed before the CTA exits
+        for (int t = j > NS ? j - NS : 0; t < j; ++t) mbar_wait(smem_u32(&bars->q_full[t % NS]), (t / NS) & 1, p.wc);
+        for (int t = seg > 2 ? seg - 2 : 0; t < seg; ++t)
+            if (!(skip_first && t == 0)) mbar_wait(smem_u32(&bars->k_full[t & 1]), (t >> 1) & 1, p.wc);
+    } else if (warp == 1) {
+        // ---------------- MMA issuer (the whole warp, one lane issues)
+        constexpr uint32_t idesc = idesc_bf16_f32(KT, KT, false, false);
+        const bool leader = elect_one();
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t dq = sdesc_sw128(sbase, 16, 1024), dk = sdesc_sw128(sbase + Cfg::kKOff, 16, 1024);
+        int j = 0, seg = 0;
+        bool ok = true;
+        for (WeightItem it(p, x0, x1); it.x < x1 && ok; it.next(p, x1), ++seg) {
+            ok = mbar_wait_warp(smem_u32(&bars->k_full[seg & 1]), (seg >> 1) & 1, p.wc);
+            const uint64_t da = dk + (seg & 1) * (kTile >> 4);
+            for (int n = it.n0; n < it.n1 && ok; ++n, ++j) {
+                const int s = j % NS, u = j % kSBufs;
+                ok = mbar_wait_warp(smem_u32(&bars->q_full[s]), (j / NS) & 1, p.wc);
+                if (ok && j >= kSBufs) ok = mbar_wait_warp(smem_u32(&bars->s_empty[u]), ((j / kSBufs) + 1) & 1, p.wc);
+                if (!ok) break;
+                tc_fence_after();
+                if (leader) {
+#pragma unroll
+                    for (int kk = 0; kk < HD / 16; ++kk) {
+                        const uint64_t off = ((kk >> 2) * kWBox + (kk & 3) * 32) >> 4;
+                        mma_ss(tm + 128 * u, da + off, dq + s * (kTile >> 4) + off, idesc, kk > 0 ? 1u : 0u);
+                    }
+                    // only what will be refilled is released
+                    if (j + NS < nx) mma_commit(smem_u32(&bars->q_empty[s]));
+                    mma_commit(smem_u32(&bars->s_full[u]));
+                    if (n + 1 == it.n1 && it.x + (it.n1 - it.n0) < x1) mma_commit(smem_u32(&bars->k_empty[seg & 1]));
+                }
+            }
+        }
+        // every MMA issued above completes before TMEM is freed
+        if (leader) mma_commit(smem_u32(&bars->drain));
+        mbar_wait_warp(smem_u32(&bars->drain), 0, p.wc);
+    } else if (warp == 2) {
+        // ---------------- log-sum-exp of the query tiles: negative, in units of
+        // log2, -infinity for queries that do not count
+        int j = 0;
+        bool ok = true;
+        for (WeightItem it(p, x0, x1); it.x < x1 && ok; it.next(p, x1)) {
+            const int b = it.line / p.Hkv, hkv = it.line - b * p.Hkv;
+            int head = b * p.H + hkv * p.G + it.n0 / it.cnt, qt = it.qlo + it.n0 % it.cnt;
+            for (int n = it.n0; n < it.n1; ++n, ++j) {
+                float v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = lane + 32 * i;
+                    v[i] = -INFINITY;
+                    if (tile_has(g, qt, r) && qt * g.P + r >= p.first) {
+                        const float l = __ldg(p.lse + (int64_t)head * g.S + tile_row(g, qt, r));
+                        v[i] = l == -INFINITY ? l : -1.4426950408889634f * l;
+                    }
+                }
+                const int u = j % kSBufs;
+                if (j >= kSBufs && !mbar_wait_warp(smem_u32(&bars->s_empty[u]), ((j / kSBufs) + 1) & 1, p.wc)) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) lse_s[u * KT + lane + 32 * i] = v[i];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->lse_full[u]));
+                if (++qt == g.nt) qt = it.qlo, ++head;
+            }
+        }
+    } else if (warp >= 4) {
+        // ---------------- weights of the keys
+        const int group = (warp - 4) >> 2, quarter = warp & 3;
+        const int r = quarter * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        const float cl2 = p.scale * 1.4426950408889634f;
+        const uint64_t cl2x2 = f2(cl2, cl2);
+        int j = 0, seg = 0;
+        bool ok = true;
+        for (WeightItem it(p, x0, x1); it.x < x1 && ok; it.next(p, x1), ++seg) {
+            float sum = 0.f;
+            int qt = it.qlo + it.n0 % it.cnt;
+            for (int n = it.n0; n < it.n1; ++n, ++j) {
+                const int at = qt;
+                if (++qt == g.nt) qt = it.qlo;
+                if ((j & 1) != group) continue;
+                const int u = j % kSBufs;
+                if (!mbar_wait_warp(smem_u32(&bars->lse_full[u]), (j / kSBufs) & 1, p.wc) ||
+                    !mbar_wait_warp(smem_u32(&bars->s_full[u]), (j / kSBufs) & 1, p.wc)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                // columns that count for some key of this warp: queries from
+                // `first` and, in the keys' own tile, from the warp's first key
+                const bool diag = at == it.kt;
+                const int c0 = max(max(0, p.first - at * g.P) / 32, diag ? quarter : 0);
+                const int c1 = (min(g.P, g.S - at * g.P) + 31) / 32;
+                const float4 *l4 = reinterpret_cast<const float4 *>(lse_s + u * KT);
+                uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+                for (int c = c0; c < c1; ++c) {
+                    uint32_t s[32];
+                    tmem_ld32(tmem + 128 * u + lane_off + 32 * c, s);
+                    tmem_ld_wait(s);
+                    const bool cut = diag && c == quarter;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 l = l4[8 * c + i];
+                        const float2 a = f2_split(
+                            fma2(f2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), cl2x2, f2(l.x, l.y)));
+                        const float2 b = f2_split(fma2(
+                            f2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), cl2x2, f2(l.z, l.w)));
+                        float e[4] = {ex2(a.x), ex2(a.y), ex2(b.x), ex2(b.y)};
+                        if (cut)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (4 * i + k < lane) e[k] = 0.f;
+                        acc[(2 * i) & 3] = add2(acc[(2 * i) & 3], f2(e[0], e[1]));
+                        acc[(2 * i + 1) & 3] = add2(acc[(2 * i + 1) & 3], f2(e[2], e[3]));
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->s_empty[u]));
+                const float2 t = f2_split(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])));
+                sum += t.x + t.y;
+            }
+            if (!ok) break;
+            // the second group's sums go to the first one
+            if (group == 1) {
+                if (seg > 0 && !mbar_wait_warp(smem_u32(&bars->comb_empty), (seg + 1) & 1, p.wc)) break;
+                comb[r] = sum;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->comb_full));
+            } else {
+                if (!mbar_wait_warp(smem_u32(&bars->comb_full), seg & 1, p.wc)) break;
+                sum += comb[r];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->comb_empty));
+                if (it.n0 == 0 && it.n1 == it.all) write_weight(p, it, r, sum);
+                else p.part[((int64_t)blockIdx.x * 2 + (it.n0 == 0)) * KT + r] = sum;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// A key tile that lies in several shares: block c - 1 adds its sums, if the
+// boundary between the shares of CTAs c - 1 and c is the first one inside it.
+__global__ void __launch_bounds__(KT) key_weight_join_kernel(const WeightParams p) {
+    wait_for_previous();
+    const int c = blockIdx.x + 1;
+    const int64_t x = weight_share(p, c);
+    const WeightItem it(p, x, x + 1);
+    const int64_t begin = x - it.n0, end = begin + it.all;
+    if (it.n0 == 0 || weight_share(p, c - 1) > begin) return;
+    const int r = threadIdx.x;
+    float sum = p.part[((int64_t)(c - 1) * 2 + 1) * KT + r];
+    for (int d = c; d < p.parts && weight_share(p, d) < end; ++d) sum += p.part[(int64_t)d * 2 * KT + r];
+    write_weight(p, it, r, sum);
+}
+
+bool weight_plan(WeightParams *p, const KeyWeightArgs &a) {
+    *p = WeightParams{};
+    if (!pos_geom(&p->g, a.S, a.N, a.layout)) return false;
+    p->H = (int)a.H;
+    p->Hkv = (int)a.Hkv;
+    p->G = (int)(a.H / a.Hkv);
+    p->first = (int)a.first;
+    p->f0 = (int)(a.first / p->g.P);
+    p->scale = a.scale;
+    p->accumulate = a.accumulate;
+    const int64_t lines = a.B * a.Hkv;
+    const int n = device_sm_count(), sms = n > 0 ? n : 152;  // no device: sizes are still told
+    // a head's triples and a CTA's share are counted in 32 bits
+    const double all = (double)lines * p->G * p->g.nt * (p->g.nt - p->f0);
+    if (all > (double)(1ll << 30) * sms || (double)p->G * p->g.nt > (double)(1ll << 30)) return false;
+    p->total = lines * weight_before(p->g, p->f0, p->G, p->g.nt);
+    p->parts = (int)(p->total < sms ? p->total : sms);
+    return true;
+}
+
+template <int HD>
+int launch_hd(const void *q, const void *k, const float *lse, float *weight, void *workspace, const KeyWeightArgs &a,
+              cudaStream_t stream) {
+    static PerDeviceOnce once;
+    const int attr = once.get([] {
+        return cuda_status(cudaFuncSetAttribute(tc_key_weight_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                (int)WeightCfg<HD>::kSmemBytes));
+    });
+    if (attr != STRIPED_OK) return attr;
+    WeightParams p;
+    if (!weight_plan(&p, a)) return STRIPED_ERR_UNSUPPORTED;
+    p.lse = lse;
+    p.weight = weight;
+    p.part = static_cast<float *>(workspace);
+    p.wc = device_wait_ctl();
+    CUtensorMap mq, mk;
+    int st;
+    if ((st = make_pos_map(&mq, q, a.D, p.g, a.B * a.H)) || (st = make_pos_map(&mk, k, a.D, p.g, a.B * a.Hkv))) return st;
+    tc_key_weight_kernel<HD><<<p.parts, kWtThreads, WeightCfg<HD>::kSmemBytes, stream>>>(mq, mk, p);
+    if ((st = cuda_status(cudaGetLastError()))) return st;
+    if (p.parts < 2) return STRIPED_OK;
+    return launch_after(key_weight_join_kernel, dim3((unsigned)(p.parts - 1)), KT, 0, stream, p);
+}
+
+}  // namespace
+
+size_t key_weight_workspace(const KeyWeightArgs &a) {
+    WeightParams p;
+    return weight_plan(&p, a) ? (size_t)p.parts * 2 * KT * 4 : 0;
+}
+
+int launch_tc_key_weight(const void *q, const void *k, const float *lse, float *weight, void *workspace,
+                         const KeyWeightArgs &a, cudaStream_t stream) {
+    return a.D == 128 ? launch_hd<128>(q, k, lse, weight, workspace, a, stream)
+                      : launch_hd<64>(q, k, lse, weight, workspace, a, stream);
+}
+
+}  // namespace striped
