@@ -629,7 +629,7 @@ int launch_tc_decode(const void *q, const void *kp, const void *vp, const void *
                : launch_decode_hd<64, false>(q, kp, vp, none, kt, vt, lens, o, lse, workspace, a, stream);
 }
 
-int launch_decode_kv4(const void *q, const Kv4Prompt &prompt, const void *kt, const void *vt, const int32_t *lens,
+int launch_tc_decode_kv4(const void *q, const Kv4Prompt &prompt, const void *kt, const void *vt, const int32_t *lens,
                       void *o, float *lse, void *workspace, const DecodeArgs &a, cudaStream_t stream) {
     return a.D == 128
                ? launch_decode_hd<128, true>(q, nullptr, nullptr, prompt, kt, vt, lens, o, lse, workspace, a, stream)

@@ -15,6 +15,8 @@ namespace {
 
 constexpr int DT = 128;              // rows and keys of a tile
 constexpr int kMaxEntries = 2048;    // row tiles of prompts and tails, over one key/value head
+constexpr int kTailTile = 32;        // keys of a tail's tile beside a 4-bit prompt and few rows: about
+                                     // the bytes of 128 stored keys
 
 struct DecParams {
     PosGeom g;            // the prompt (S = 0 positions if there is none)
@@ -89,6 +91,13 @@ __device__ Span entry_span(const DecParams &p, int e) {
     return span_of(first, n - 1, DT, p.sinks - p.P, n);
 }
 
+// Key tiles of an entry without a window, tails in tiles of TT keys.
+template <int TT>
+__device__ __forceinline__ int entry_tiles(const DecParams &p, int e) {
+    if (e < p.ep) return p.g.nt;
+    return (len_of(p, (e - p.ep) / p.nrt_t) + TT - 1) / TT;
+}
+
 // Share of CTA c of `parts`: tiles [share(c), share(c + 1)).
 __device__ __forceinline__ int share(int64_t total, int c, int parts) { return (int)(total * c / parts); }
 
@@ -100,8 +109,7 @@ struct Segment {
     Span s;
 };
 
-__device__ __forceinline__ Segment segment_at(const int *cum, const int *lo, const int *ns, int entries, int hkv_n,
-                                              int over, int x, int x1) {
+__device__ __forceinline__ Segment segment_of(const int *cum, int entries, int hkv_n, int over, int x, int x1) {
     int a = 0, b = entries - 1;  // last entry that begins at or below x (entries without tiles are passed over)
     while (a < b) {
         const int m = (a + b + 1) >> 1;
@@ -118,7 +126,14 @@ __device__ __forceinline__ Segment segment_at(const int *cum, const int *lo, con
     s.t0 = max(0, off - over);
     s.t1 = min(s.nt, off + (x1 - x) - over);
     s.next = min(x1, x + cost - off);
-    s.s = Span{ns[a], lo[a], s.nt};
+    s.s = Span{0, 0, s.nt};
+    return s;
+}
+__device__ __forceinline__ Segment segment_at(const int *cum, const int *lo, const int *ns, int entries, int hkv_n,
+                                              int over, int x, int x1) {
+    Segment s = segment_of(cum, entries, hkv_n, over, x, x1);
+    s.s.ns = ns[s.e];
+    s.s.lo = lo[s.e];
     return s;
 }
 
@@ -227,6 +242,7 @@ __global__ void __launch_bounds__(128) decode_join_kernel(const DecParams p, int
 struct DecPlan {
     DecParams p;
     int parts;
+    bool small;  // a 4-bit prompt under few rows (attn_decode_kv4.cu)
     size_t cum_bytes, ml_bytes[2], o_bytes[2];
 };
 
@@ -261,8 +277,10 @@ bool decode_plan(DecPlan *plan, const DecodeArgs &a) {
     // requests, window 4096, D = 64: 40.3 us at 1, 37.5 at 2, 34.8 at 4, 36.2
     // at 6, 37.5 at 8
     p.over = a.D == 128 ? 2 : 4;
+    plan->small = a.kv4 && rows_p <= 16;
+    const int tail_tile = plan->small ? kTailTile : DT;
     const int64_t tiles =
-        (ep * (a.P > 0 ? p.g.nt + p.over : 0) + a.B * nrt_t * ((a.C + DT - 1) / DT + p.over)) * a.Hkv;
+        (ep * (a.P > 0 ? p.g.nt + p.over : 0) + a.B * nrt_t * ((a.C + tail_tile - 1) / tail_tile + p.over)) * a.Hkv;
     if (tiles > (1ll << 30)) return false;
     p.rows_p = (int)rows_p;
     p.rows_t = (int)per;
@@ -271,8 +289,8 @@ bool decode_plan(DecPlan *plan, const DecodeArgs &a) {
     p.ep = (int)ep;
     p.entries = (int)entries;
     p.scale = a.scale;
-    const int sms = device_sm_count();
-    plan->parts = (int)(tiles < sms ? tiles : sms);
+    const int ctas = device_sm_count() * (plan->small && rows_p <= 8 ? 2 : 1);
+    plan->parts = (int)(tiles < ctas ? tiles : ctas);
     p.slot_rows[0] = (int)(rows_p < DT ? rows_p : DT);
     p.slot_rows[1] = (int)(per < DT ? per : DT);
     plan->cum_bytes = ((size_t)(entries + 1) * 4 + 255) & ~size_t(255);
