@@ -315,8 +315,8 @@ __global__ void __launch_bounds__(kQThreads, NT == 1 ? 2 : 1)
                         const uint32_t *row = reinterpret_cast<const uint32_t *>(at + (16 * i + g) * Cfg::kRow) + v * 4 + t;
                         const uint32_t a = row[0], b = row[8 * Cfg::kRow / 4];
                         uint32_t ca[4], cb[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) ca[j] = kv4_codes(a, j), cb[j] = kv4_codes(b, j);
+                        kv4_pairs(a, ca);
+                        kv4_pairs(b, cb);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             const uint4 q = q_at(n, v);
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kQThreads, NT == 1 ? 2 : 1)
                 }
                 if (inside || key0 + kStep - 1 > hi_min) masked(s, key0);
                 uint32_t pt[2][NT][2];
-                st.template softmax<2>(s, pt, cl2);
+                st.template softmax<2>(s, pt, cl2 * kKv4Unit);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     // this thread's keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of the 16
@@ -355,14 +355,17 @@ __global__ void __launch_bounds__(kQThreads, NT == 1 ? 2 : 1)
                     for (int u = 0; u < HD / 64; ++u) {
                         const uint32_t e0 = __byte_perm(w[0][u], w[1][u], 0x5410), o0 = __byte_perm(w[0][u], w[1][u], 0x7632);
                         const uint32_t e1 = __byte_perm(w[2][u], w[3][u], 0x5410), o1 = __byte_perm(w[2][u], w[3][u], 0x7632);
+                        uint32_t ce0[4], co0[4], ce1[4], co1[4];
+                        kv4_pairs(e0, ce0);
+                        kv4_pairs(o0, co0);
+                        kv4_pairs(e1, ce1);
+                        kv4_pairs(o1, co1);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t a0 = bf16x2_mul(kv4_codes(e0, j), s0), a1 = bf16x2_mul(kv4_codes(o0, j), s0);
-                            const uint32_t a2 = bf16x2_mul(kv4_codes(e1, j), s1), a3 = bf16x2_mul(kv4_codes(o1, j), s1);
+                        for (int j = 0; j < 4; ++j)
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
-                                mma16816(st.o[4 * u + j][n], a0, a1, a2, a3, pt[i][n][0], pt[i][n][1]);
-                        }
+                                mma16816(st.o[4 * u + j][n], bf16x2_mul(ce0[j], s0), bf16x2_mul(co0[j], s0),
+                                         bf16x2_mul(ce1[j], s1), bf16x2_mul(co1[j], s1), pt[i][n][0], pt[i][n][1]);
                     }
                 }
                 __syncwarp();  // the stage is free
@@ -450,7 +453,7 @@ __global__ void __launch_bounds__(kQThreads, NT == 1 ? 2 : 1)
                 float top = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < kQWarps; ++w) top = fmaxf(top, sm[w * 8 * NT + r]);
-                const float a = st.m[n][k] == -INFINITY ? 0.f : ex2(st.m[n][k] - top);
+                const float a = st.m[n][k] == -INFINITY ? 0.f : ex2(st.m[n][k] - top) * (tail ? 1.f : kKv4Unit);
                 float *dst = po + (warp * 8 * NT + r) * Cfg::kORow + g * (HD / 8);
 #pragma unroll
                 for (int c = 0; c < HD / 16; c += 2)

@@ -39,4 +39,25 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
 // The codes of pair j as whole bf16 numbers (exact: 128 + 15 has 8 bits).
 __device__ __forceinline__ uint32_t kv4_codes(uint32_t w, int j) { return bf16x2_sub(kv4_biased(w, j), 0x43084308u); }
 
+// The codes of all four pairs, times 2^-6, at 5 operations of the integer pipe
+// instead of 7 (it has half the rate of the others and bounds what reads 4-bit
+// rows).  A bf16 number whose bits are the whole number n < 256 is n * 2^-133:
+// the first normal binade goes on where the subnormals end.  So codes + 8 in
+// the low or in the high nibble of a byte are numbers as they stand, and one
+// fused multiply-add makes (code + 8 - 8) * 2^-6 of them, exactly.
+constexpr float kKv4Unit = 64.f;  // undoes the 2^-6
+__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+__device__ __forceinline__ void kv4_pairs(uint32_t w, uint32_t (&c)[4]) {
+    constexpr uint32_t k2e127 = 0x7f007f00u, k2e123 = 0x7d007d00u, kMinus8th = 0xbe00be00u;
+    const uint32_t h = w >> 8;
+    c[0] = bf16x2_fma(w & 0x000f000fu, k2e127, kMinus8th);
+    c[1] = bf16x2_fma(w & 0x00f000f0u, k2e123, kMinus8th);
+    c[2] = bf16x2_fma(h & 0x000f000fu, k2e127, kMinus8th);
+    c[3] = bf16x2_fma(h & 0x00f000f0u, k2e123, kMinus8th);
+}
+
 }  // namespace striped
