@@ -21,8 +21,14 @@
 //   warps 2, 3   log-sum-exp of the query tiles
 //   warps 4..11  two groups that take every other tile; thread t of a group owns
 //                key t
-// Tensor memory: four S^T of 128 columns.
+//   warps 12..15 K tile from shared to tensor memory: as the left operand it is
+//                read there, and a product takes half the bytes from shared
+//                memory (both operands from there: 512 clocks a tile of its
+//                bandwidth, beside TMA's and the log-sum-exp's)
+// Tensor memory: three S^T of 128 columns, two K tiles.
 #include <math.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -34,8 +40,12 @@ namespace {
 
 constexpr int KT = 128;
 constexpr uint32_t kWBox = 128 * 128;  // 128 rows x 64 bf16
-constexpr int kWtThreads = 384;
-constexpr int kSBufs = 4;
+constexpr int kWtThreads = 512;
+constexpr int kSBufs = 3;
+// Log-sum-exp buffers: an even number, so that a buffer's tiles are all of one
+// writing warp and one reading group.  (A wait tells a phase from the next one
+// only; whoever could be two phases ahead or behind must not wait there.)
+constexpr int kLBufs = 4;
 
 template <int HD>
 struct WeightCfg {
@@ -43,7 +53,7 @@ struct WeightCfg {
     static constexpr uint32_t kTile = (HD / 64) * kWBox;
     static constexpr uint32_t kKOff = NS * kTile;  // two K tiles
     static constexpr uint32_t kLseOff = kKOff + 2 * kTile;
-    static constexpr uint32_t kCombOff = kLseOff + kSBufs * KT * 4;
+    static constexpr uint32_t kCombOff = kLseOff + kLBufs * KT * 4;
     static constexpr uint32_t kBarOff = kCombOff + KT * 4;
     static constexpr size_t kSmemBytes = 1024 + kBarOff + 512;
     static_assert(kSmemBytes <= 232448, "shared memory over the per-block limit");
@@ -51,9 +61,11 @@ struct WeightCfg {
 
 template <int NS>
 struct WeightBars {
-    uint64_t k_full[2], k_empty[2];
+    uint64_t k_full[2], k_empty[2];    // in shared memory
+    uint64_t kt_full[2], kt_empty[2];  // in tensor memory
     uint64_t q_full[NS], q_empty[NS];
-    uint64_t s_full[kSBufs], s_empty[kSBufs], lse_full[kSBufs];
+    uint64_t s_full[kSBufs], s_empty[kSBufs];
+    uint64_t lse_full[kLBufs], lse_empty[kLBufs];
     uint64_t comb_full, comb_empty, drain;
     uint32_t tmem_slot;
 };
@@ -133,7 +145,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                          const WeightParams p) {
     using Cfg = WeightCfg<HD>;
     constexpr int NS = Cfg::NS, kBoxes = HD / 64;
-    constexpr uint32_t kTile = Cfg::kTile;
+    constexpr uint32_t kTile = Cfg::kTile, kKCol = kSBufs * KT;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem =
         reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -147,7 +159,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&bars->k_full[i]), 1);
-            mbar_init(smem_u32(&bars->k_empty[i]), 1);
+            mbar_init(smem_u32(&bars->k_empty[i]), 4);
+            mbar_init(smem_u32(&bars->kt_full[i]), 4);
+            mbar_init(smem_u32(&bars->kt_empty[i]), 1);
         }
         for (int s = 0; s < NS; ++s) {
             mbar_init(smem_u32(&bars->q_full[s]), 1);
@@ -156,7 +170,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         for (int i = 0; i < kSBufs; ++i) {
             mbar_init(smem_u32(&bars->s_full[i]), 1);
             mbar_init(smem_u32(&bars->s_empty[i]), 4);
+        }
+        for (int i = 0; i < kLBufs; ++i) {
             mbar_init(smem_u32(&bars->lse_full[i]), 1);
+            mbar_init(smem_u32(&bars->lse_empty[i]), 4);
         }
         mbar_init(smem_u32(&bars->comb_full), 4);
         mbar_init(smem_u32(&bars->comb_empty), 4);
@@ -222,31 +239,35 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             if (!(skip_first && t == 0)) mbar_wait(smem_u32(&bars->k_full[t & 1]), (t >> 1) & 1, p.wc);
     } else if (warp == 1) {
         // ---------------- MMA issuer (the whole warp, one lane issues)
-        constexpr uint32_t idesc = idesc_bf16_f32(KT, KT, false, false);
         const bool leader = elect_one();
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        const uint64_t dq = sdesc_sw128(sbase, 16, 1024), dk = sdesc_sw128(sbase + Cfg::kKOff, 16, 1024);
+        const uint64_t dq = sdesc_sw128(sbase, 16, 1024);
         int j = 0, seg = 0;
         bool ok = true;
         for (WeightItem it(p, x0, x1); it.x < x1 && ok; it.next(p, x1), ++seg) {
-            ok = mbar_wait_warp(smem_u32(&bars->k_full[seg & 1]), (seg >> 1) & 1, p.wc);
-            const uint64_t da = dk + (seg & 1) * (kTile >> 4);
+            ok = mbar_wait_warp(smem_u32(&bars->kt_full[seg & 1]), (seg >> 1) & 1, p.wc);
+            const uint32_t ta = tm + kKCol + (seg & 1) * (HD / 2);
+            int qt = it.qlo + it.n0 % it.cnt;
             for (int n = it.n0; n < it.n1 && ok; ++n, ++j) {
                 const int s = j % NS, u = j % kSBufs;
                 ok = mbar_wait_warp(smem_u32(&bars->q_full[s]), (j / NS) & 1, p.wc);
                 if (ok && j >= kSBufs) ok = mbar_wait_warp(smem_u32(&bars->s_empty[u]), ((j / kSBufs) + 1) & 1, p.wc);
                 if (!ok) break;
                 tc_fence_after();
+                // queries before `first` in its tile are left out, 32 at a time
+                const int skip = max(0, p.first - qt * g.P) / 32;
+                if (++qt == g.nt) qt = it.qlo;
+                const uint32_t idesc = idesc_bf16_f32(KT, KT, false, false) - ((uint32_t)(skip * 32 / 8) << 17);
                 if (leader) {
+                    const uint64_t db = dq + s * (kTile >> 4) + (skip * 32 * 128 >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < HD / 16; ++kk) {
-                        const uint64_t off = ((kk >> 2) * kWBox + (kk & 3) * 32) >> 4;
-                        mma_ss(tm + 128 * u, da + off, dq + s * (kTile >> 4) + off, idesc, kk > 0 ? 1u : 0u);
-                    }
+                    for (int kk = 0; kk < HD / 16; ++kk)
+                        mma_ts(tm + 128 * u + 32 * skip, ta + kk * 8, db + (((kk >> 2) * kWBox + (kk & 3) * 32) >> 4),
+                               idesc, kk > 0 ? 1u : 0u);
                     // only what will be refilled is released
                     if (j + NS < nx) mma_commit(smem_u32(&bars->q_empty[s]));
                     mma_commit(smem_u32(&bars->s_full[u]));
-                    if (n + 1 == it.n1 && it.x + (it.n1 - it.n0) < x1) mma_commit(smem_u32(&bars->k_empty[seg & 1]));
+                    if (n + 1 == it.n1 && it.x + (it.n1 - it.n0) < x1) mma_commit(smem_u32(&bars->kt_empty[seg & 1]));
                 }
             }
         }
@@ -291,8 +312,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             if (at < nx) step();
         };
         auto put = [&](int j, const float (&v)[4]) -> bool {
-            const int u = j % kSBufs;
-            if (j >= kSBufs && !mbar_wait_warp(smem_u32(&bars->s_empty[u]), ((j / kSBufs) + 1) & 1, p.wc)) return false;
+            const int u = j % kLBufs;
+            if (j >= kLBufs && !mbar_wait_warp(smem_u32(&bars->lse_empty[u]), ((j / kLBufs) + 1) & 1, p.wc)) return false;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 lse_s[u * KT + lane + 32 * i] = v[i] == -INFINITY ? v[i] : -1.4426950408889634f * v[i];
@@ -310,6 +331,34 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             if (j + 2 >= nx || !put(j + 2, v1)) break;
             read(v1);
         }
+    } else if (warp >= 12) {
+        // ---------------- K tiles: shared -> tensor memory
+        const int r = (warp & 3) * 32 + lane;
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        int seg = 0;
+        for (WeightItem it(p, x0, x1); it.x < x1; it.next(p, x1), ++seg) {
+            const int ks = seg & 1;
+            if (!mbar_wait_warp(smem_u32(&bars->k_full[ks]), (seg >> 1) & 1, p.wc)) break;
+            const uint8_t *src = smem + Cfg::kKOff + ks * kTile + r * 128;
+            uint32_t k[HD / 64][32];
+#pragma unroll
+            for (int c = 0; c < kBoxes; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(src + c * kWBox + ((i ^ (r & 7)) * 16));
+                    k[c][4 * i] = w.x, k[c][4 * i + 1] = w.y, k[c][4 * i + 2] = w.z, k[c][4 * i + 3] = w.w;
+                }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->k_empty[ks]));
+            if (seg >= 2 && !mbar_wait_warp(smem_u32(&bars->kt_empty[ks]), ((seg >> 1) + 1) & 1, p.wc)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < kBoxes; ++c) tmem_st32(tmem + kKCol + ks * (HD / 2) + 32 * c + lane_off, k[c]);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->kt_full[ks]));
+        }
     } else if (warp >= 4) {
         // ---------------- weights of the keys
         const int group = (warp - 4) >> 2, quarter = warp & 3;
@@ -326,8 +375,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 const int at = qt;
                 if (++qt == g.nt) qt = it.qlo;
                 if ((j & 1) != group) continue;
-                const int u = j % kSBufs;
-                if (!mbar_wait_warp(smem_u32(&bars->lse_full[u]), (j / kSBufs) & 1, p.wc) ||
+                const int u = j % kSBufs, lb = j % kLBufs;
+                if (!mbar_wait_warp(smem_u32(&bars->lse_full[lb]), (j / kLBufs) & 1, p.wc) ||
                     !mbar_wait_warp(smem_u32(&bars->s_full[u]), (j / kSBufs) & 1, p.wc)) {
                     ok = false;
                     break;
@@ -338,13 +387,14 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 const bool diag = at == it.kt;
                 const int c0 = max(max(0, p.first - at * g.P) / 32, diag ? quarter : 0);
                 const int c1 = (min(g.P, g.S - at * g.P) + 31) / 32;
-                const float4 *l4 = reinterpret_cast<const float4 *>(lse_s + u * KT);
+                const float4 *l4 = reinterpret_cast<const float4 *>(lse_s + lb * KT);
                 uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-                for (int c = c0; c < c1; ++c) {
+                // 32 columns; in the keys' own tile the first ones that a warp
+                // looks at are cut along the diagonal
+                auto add = [&](int c, auto cut) {
                     uint32_t s[32];
                     tmem_ld32(tmem + 128 * u + lane_off + 32 * c, s);
                     tmem_ld_wait(s);
-                    const bool cut = diag && c == quarter;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float4 l = l4[8 * c + i];
@@ -353,17 +403,23 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                         const float2 b = f2_split(fma2(
                             f2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), cl2x2, f2(l.z, l.w)));
                         float e[4] = {ex2(a.x), ex2(a.y), ex2(b.x), ex2(b.y)};
-                        if (cut)
+                        if constexpr (decltype(cut)::value)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 if (4 * i + k < lane) e[k] = 0.f;
                         acc[(2 * i) & 3] = add2(acc[(2 * i) & 3], f2(e[0], e[1]));
                         acc[(2 * i + 1) & 3] = add2(acc[(2 * i + 1) & 3], f2(e[2], e[3]));
                     }
-                }
+                };
+                int c = c0;
+                if (diag && c == quarter && c < c1) add(c++, std::true_type{});
+                for (; c < c1; ++c) add(c, std::false_type{});
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars->s_empty[u]));
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&bars->s_empty[u]));
+                    mbar_arrive(smem_u32(&bars->lse_empty[lb]));
+                }
                 const float2 t = f2_split(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])));
                 sum += t.x + t.y;
             }
