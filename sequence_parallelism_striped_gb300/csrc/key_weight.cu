@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 // queries before `first` in its tile are left out, 32 at a time
-                const int skip = max(0, p.first - qt * g.P) / 32;
+                const int skip = qt == p.f0 ? (p.first - qt * g.P) / 32 : 0;
                 if (++qt == g.nt) qt = it.qlo;
                 const uint32_t idesc = idesc_bf16_f32(KT, KT, false, false) - ((uint32_t)(skip * 32 / 8) << 17);
                 if (leader) {
@@ -366,38 +366,43 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
         const float cl2 = p.scale * 1.4426950408889634f;
         const uint64_t cl2x2 = f2(cl2, cl2);
-        int j = 0, seg = 0;
+        int seg = 0;
         bool ok = true;
-        for (WeightItem it(p, x0, x1); it.x < x1 && ok; it.next(p, x1), ++seg) {
+        // the group's tiles are j = group, group + 2, ..: their buffer and its phase
+        int j = group, u = group, phase = 0;
+        int j0 = 0;  // first tile of the item
+        for (WeightItem it(p, x0, x1); it.x < x1 && ok; j0 += it.n1 - it.n0, it.next(p, x1), ++seg) {
             float sum = 0.f;
-            int qt = it.qlo + it.n0 % it.cnt;
-            for (int n = it.n0; n < it.n1; ++n, ++j) {
+            const int j1 = j0 + it.n1 - it.n0;
+            int qt = it.qlo + (it.n0 + j - j0) % it.cnt;
+            for (; j < j1; j += 2) {
                 const int at = qt;
-                if (++qt == g.nt) qt = it.qlo;
-                if ((j & 1) != group) continue;
-                const int u = j % kSBufs, lb = j % kLBufs;
-                if (!mbar_wait_warp(smem_u32(&bars->lse_full[lb]), (j / kLBufs) & 1, p.wc) ||
-                    !mbar_wait_warp(smem_u32(&bars->s_full[u]), (j / kSBufs) & 1, p.wc)) {
+                qt += 2;
+                while (qt >= g.nt) qt -= it.cnt;
+                const int lb = j % kLBufs;
+                const uint32_t lse_bar = smem_u32(&bars->lse_full[lb]), s_bar = smem_u32(&bars->s_full[u]);
+                const bool l_ok = mbar_try_wait(lse_bar, (j / kLBufs) & 1), s_ok = mbar_try_wait(s_bar, phase);
+                if (!__all_sync(0xffffffffu, l_ok && s_ok) &&
+                    (!mbar_wait_warp(lse_bar, (j / kLBufs) & 1, p.wc) || !mbar_wait_warp(s_bar, phase, p.wc))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                // columns that count for some key of this warp: queries from
-                // `first` and, in the keys' own tile, from the warp's first key
-                const bool diag = at == it.kt;
-                const int c0 = max(max(0, p.first - at * g.P) / 32, diag ? quarter : 0);
-                const int c1 = (min(g.P, g.S - at * g.P) + 31) / 32;
-                const float4 *l4 = reinterpret_cast<const float4 *>(lse_s + lb * KT);
+                const float4 *lse4 = reinterpret_cast<const float4 *>(lse_s + lb * KT);
+                const uint32_t src = tmem + 128 * u + lane_off;
                 uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
                 // 32 columns; in the keys' own tile the first ones that a warp
                 // looks at are cut along the diagonal
                 auto add = [&](int c, auto cut) {
                     uint32_t s[32];
-                    tmem_ld32(tmem + 128 * u + lane_off + 32 * c, s);
+                    tmem_ld32(src + 32 * c, s);
+                    float4 l4[8];  // all on their way before the first is used
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) l4[i] = lse4[8 * c + i];
                     tmem_ld_wait(s);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float4 l = l4[8 * c + i];
+                        const float4 l = l4[i];
                         const float2 a = f2_split(
                             fma2(f2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), cl2x2, f2(l.x, l.y)));
                         const float2 b = f2_split(fma2(
@@ -411,15 +416,27 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                         acc[(2 * i + 1) & 3] = add2(acc[(2 * i + 1) & 3], f2(e[2], e[3]));
                     }
                 };
-                int c = c0;
-                if (diag && c == quarter && c < c1) add(c++, std::true_type{});
-                for (; c < c1; ++c) add(c, std::false_type{});
+                if (at != it.kt && at != p.f0 && at + 1 != g.nt) {
+#pragma unroll
+                    for (int c = 0; c < KT / 32; ++c) add(c, std::false_type{});
+                } else {
+                    // columns that count for some key of this warp: queries from
+                    // `first` and, in the keys' own tile, from the warp's first key
+                    const bool diag = at == it.kt;
+                    int c = max(max(0, p.first - at * g.P) / 32, diag ? quarter : 0);
+                    const int c1 = (min(g.P, g.S - at * g.P) + 31) / 32;
+                    if (diag && c == quarter && c < c1) add(c++, std::true_type{});
+#pragma unroll 1
+                    for (; c < c1; ++c) add(c, std::false_type{});
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(smem_u32(&bars->s_empty[u]));
                     mbar_arrive(smem_u32(&bars->lse_empty[lb]));
                 }
+                u += 2;
+                if (u >= kSBufs) u -= kSBufs, phase ^= 1;
                 const float2 t = f2_split(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])));
                 sum += t.x + t.y;
             }
