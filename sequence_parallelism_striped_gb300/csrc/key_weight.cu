@@ -393,13 +393,22 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
                 // 32 columns; in the keys' own tile the first ones that a warp
                 // looks at are cut along the diagonal
-                auto add = [&](int c, auto cut) {
+                auto add = [&](int c, auto cut, bool last) {
                     uint32_t s[32];
                     tmem_ld32(src + 32 * c, s);
                     float4 l4[8];  // all on their way before the first is used
 #pragma unroll
                     for (int i = 0; i < 8; ++i) l4[i] = lse4[8 * c + i];
                     tmem_ld_wait(s);
+                    if (last) {
+                        // the buffers are read: products and log-sum-exps may go on
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(smem_u32(&bars->s_empty[u]));
+                            mbar_arrive(smem_u32(&bars->lse_empty[lb]));
+                        }
+                    }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float4 l = l4[i];
@@ -418,22 +427,22 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 };
                 if (at != it.kt && at != p.f0 && at + 1 != g.nt) {
 #pragma unroll
-                    for (int c = 0; c < KT / 32; ++c) add(c, std::false_type{});
+                    for (int c = 0; c < KT / 32; ++c) add(c, std::false_type{}, c == KT / 32 - 1);
                 } else {
                     // columns that count for some key of this warp: queries from
                     // `first` and, in the keys' own tile, from the warp's first key
                     const bool diag = at == it.kt;
                     int c = max(max(0, p.first - at * g.P) / 32, diag ? quarter : 0);
                     const int c1 = (min(g.P, g.S - at * g.P) + 31) / 32;
-                    if (diag && c == quarter && c < c1) add(c++, std::true_type{});
+                    if (diag && c == quarter && c < c1) add(c++, std::true_type{}, false);
 #pragma unroll 1
-                    for (; c < c1; ++c) add(c, std::false_type{});
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&bars->s_empty[u]));
-                    mbar_arrive(smem_u32(&bars->lse_empty[lb]));
+                    for (; c < c1; ++c) add(c, std::false_type{}, false);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_u32(&bars->s_empty[u]));
+                        mbar_arrive(smem_u32(&bars->lse_empty[lb]));
+                    }
                 }
                 u += 2;
                 if (u >= kSBufs) u -= kSBufs, phase ^= 1;
