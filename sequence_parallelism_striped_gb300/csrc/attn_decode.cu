@@ -60,7 +60,7 @@ namespace {
 
 constexpr uint32_t kDBox = 128 * 128;   // 128 rows x 64 bf16
 constexpr int kDThreads = 192;
-constexpr int kDThreads4 = kDThreads + 128;
+constexpr int kDThreads4 = kDThreads + 256;
 constexpr float kDRescale = 8.0f;       // lazy rescale threshold, log2 units
 
 template <int HD>
@@ -83,9 +83,13 @@ struct DecBars {
     int scan[kDThreads / 32];
 };
 
-// KV4: the prompt is in 4 bits.  Four more warps make its tiles: thread t takes
-// the codes and scales of key row t from memory, a tile ahead, and writes the
-// values, which are bf16 numbers, where TMA puts the rows of a bf16 prompt.
+// KV4: the prompt is in 4 bits.  Eight more warps make its tiles, four those of K
+// and four those of V: thread t takes the codes and scales of row t from memory,
+// a tile ahead, and writes the values, which are bf16 numbers (times 2^-6:
+// kv4.cuh), where TMA puts the rows of a bf16 prompt.  With them there are 128
+// registers a thread, so the softmax reads a row's scores twice, 32 at a time
+// (32 requests on 131072: 157 us with four such warps and the scores in
+// registers, which bounds them by the latency of a warp alone).
 template <int HD, bool KV4>
 __global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
     tc_decode_kernel(const __grid_constant__ CUtensorMap tmKp, const __grid_constant__ CUtensorMap tmVp,
@@ -108,7 +112,7 @@ __global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&bars->q_full), 4);
         for (int s = 0; s < NS; ++s) {
-            mbar_init(smem_u32(&bars->kv_full[s]), KV4 ? 5 : 1);
+            mbar_init(smem_u32(&bars->kv_full[s]), KV4 ? 9 : 1);
             mbar_init(smem_u32(&bars->kv_empty[s]), 1);
         }
         mbar_init(smem_u32(&bars->s_full[0]), 1);
@@ -278,60 +282,39 @@ __global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
         mbar_wait_warp(smem_u32(&bars->drain), 0, p.wc);
     } else if (KV4 && warp >= kDThreads / 32 && nx > 0) {
         // ---------------- 4 bits -> bf16
-        const int r = threadIdx.x - kDThreads;  // key row of the tile
-        constexpr int V = HD / 32;              // groups of a row: 16 bytes of codes, one scale
+        const bool is_v = warp >= kDThreads / 32 + 4;
+        const int r = (threadIdx.x - kDThreads) & 127;  // row of the tile
+        constexpr int V = HD / 32;                      // groups of a row: 16 bytes of codes, one scale
         using Scales = typename std::conditional<HD == 128, uint2, uint32_t>::type;
-        // the stored row of this thread in the tile that is read next
-        int64_t at = -1;
-        uint4 kc[V], vc[V];
-        Scales ks{}, vs{};
-        auto fetch = [&]() {
-            if (at < 0) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) kc[i] = vc[i] = make_uint4(0u, 0u, 0u, 0u);
-                ks = vs = Scales{};
-                return;
-            }
-            const uint4 *k = reinterpret_cast<const uint4 *>(p.k_codes) + at * V;
-            const uint4 *v = reinterpret_cast<const uint4 *>(p.v_codes) + at * V;
-#pragma unroll
-            for (int i = 0; i < V; ++i) kc[i] = __ldg(k + i), vc[i] = __ldg(v + i);
-            ks = __ldg(reinterpret_cast<const Scales *>(p.k_scales) + at);
-            vs = __ldg(reinterpret_cast<const Scales *>(p.v_scales) + at);
-        };
-        auto put = [&](uint8_t *tile, const uint4 (&c)[V], const Scales &sc) {
-            const uint32_t *sw = reinterpret_cast<const uint32_t *>(&sc);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const uint32_t s2 = __byte_perm(sw[i / 2], 0, i % 2 ? 0x3232 : 0x1010);
-                const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int chunk = 4 * i + k;  // 8 channels
-                    *reinterpret_cast<uint4 *>(tile + chunk / 8 * kDBox + r * 128 + (((chunk & 7) ^ (r & 7)) * 16)) =
-                        make_uint4(bf16x2_mul(kv4_codes(w[k], 0), s2), bf16x2_mul(kv4_codes(w[k], 1), s2),
-                                   bf16x2_mul(kv4_codes(w[k], 2), s2), bf16x2_mul(kv4_codes(w[k], 3), s2));
-                }
-            }
-        };
+        const uint4 *codes = reinterpret_cast<const uint4 *>(is_v ? p.v_codes : p.k_codes);
+        const Scales *scales = reinterpret_cast<const Scales *>(is_v ? p.v_scales : p.k_scales);
+        // this thread's row of the tile that is written next
+        uint4 code[V];
+        Scales scale{};
         // walks over the prompt tiles of this CTA, one ahead of the writing
         int fx = x0, ft = 0;
         Segment fs{};
         fs.t1 = 0;
-        auto advance = [&]() {
-            at = -1;
+        auto fetch = [&]() {
             ++ft;
             while (ft >= fs.t1) {
-                if (fx >= x1) return false;
+                if (fx >= x1) return;
                 fs = segment(fx);
                 fx = fs.next;
                 ft = fs.e < p.ep ? fs.t0 : fs.t1;  // tails are not ours
             }
             const int row = ft * DT + r;
-            if (row < p.P) at = ((int64_t)(fs.e / p.nrt_p) * p.Hkv + fs.hkv) * p.P + row;
-            return true;
+#pragma unroll
+            for (int i = 0; i < V; ++i) code[i] = make_uint4(0u, 0u, 0u, 0u);
+            scale = Scales{};
+            if (row < p.P) {
+                const int64_t at = ((int64_t)(fs.e / p.nrt_p) * p.Hkv + fs.hkv) * p.P + row;
+#pragma unroll
+                for (int i = 0; i < V; ++i) code[i] = __ldg(codes + at * V + i);
+                scale = __ldg(scales + at);
+            }
         };
-        if (advance()) fetch();
+        fetch();
         int j = 0;
         bool ok = true;
         for (int x = x0; x < x1 && ok;) {
@@ -345,10 +328,23 @@ __global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
                     break;
                 }
                 if (!tail) {
-                    uint8_t *tile = smem + s * kStage;
-                    put(tile, kc, ks);
-                    put(tile + kTile, vc, vs);
-                    if (advance()) fetch();
+                    uint8_t *tile = smem + s * kStage + (is_v ? kTile : 0) + r * 128;
+                    const uint32_t *sw = reinterpret_cast<const uint32_t *>(&scale);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const uint32_t s2 = __byte_perm(sw[i / 2], 0, i % 2 ? 0x3232 : 0x1010);
+                        const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int chunk = 4 * i + k;  // 8 channels
+                            uint32_t c[4];
+                            kv4_pairs(w[k], c);
+                            *reinterpret_cast<uint4 *>(tile + chunk / 8 * kDBox + (((chunk & 7) ^ (r & 7)) * 16)) =
+                                make_uint4(bf16x2_mul(c[0], s2), bf16x2_mul(c[1], s2), bf16x2_mul(c[2], s2),
+                                           bf16x2_mul(c[3], s2));
+                        }
+                    }
+                    fetch();
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
@@ -360,7 +356,6 @@ __global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
         const int quarter = warp & 3;
         const int ri = quarter * 32 + lane;  // row of the tile
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-        const float cl2 = p.scale * 1.4426950408889634f;
         const int per = p.G * p.T;
         int j = 0;
         bool ok = true;
@@ -369,6 +364,8 @@ __global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
             x = sg.next;
             if (sg.t1 <= sg.t0) continue;
             const bool tail = sg.e >= p.ep;
+            const float unit = KV4 && !tail ? kKv4Unit : 1.f;  // of the values in the tiles
+            const float cl2 = p.scale * 1.4426950408889634f * unit;
             // this thread's query row: request b, head h, token t
             int grp, rt, rows;
             if (tail) {
@@ -446,6 +443,67 @@ __global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
                         break;
                     }
                     tc_fence_after();
+                    if constexpr (KV4) {
+                        // columns that are kept, 32 bits at a time
+                        const bool inside = !tail && __any_sync(0xffffffffu, qpos < p.P - 1);
+                        const bool full = !inside && __all_sync(0xffffffffu, kbase + DT - 1 <= hi);
+                        uint32_t keep[DT / 32];
+                        if (!full)
+#pragma unroll
+                            for (int w = 0; w < DT / 32; ++w) {
+                                keep[w] = kept_bits(32 * w, hi - kbase, lo - kbase, 0);
+                                if (inside) {  // a query inside the prompt keeps rows by their position
+                                    keep[w] = 0;
+#pragma unroll 1
+                                    for (int c = 0; c < 32; ++c) {
+                                        const int row = kbase + 32 * w + c;
+                                        if (row < p.P && row_position(p, row) <= qpos) keep[w] |= 1u << c;
+                                    }
+                                }
+                            }
+                        auto scores = [&](int w, uint32_t (&x)[32]) {
+                            tmem_ld32(tS + 32 * w, x);
+                            tmem_ld_wait(x);
+                            if (!full)
+#pragma unroll
+                                for (int c = 0; c < 32; ++c)
+                                    if (!(keep[w] & (1u << c))) x[c] = 0xff800000u;  // -infinity
+                        };
+                        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int w = 0; w < DT / 32; ++w) {
+                            uint32_t x[32];
+                            scores(w, x);
+#pragma unroll
+                            for (int c = 0; c < 32; c += 2)
+                                top[(c >> 1) & 3] = fmax3(top[(c >> 1) & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+                        }
+                        const float m_tile = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * cl2;
+                        const bool move = n == 0 || m_tile > m_ref + kDRescale;
+                        const float m_new = move ? fmaxf(m_ref, m_tile) : m_ref;
+                        alpha = (n == 0 || !move) ? 1.f : ex2(m_ref - m_new);
+                        const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
+                        const uint64_t cl2x2 = f2(cl2, cl2), nm2 = f2(-m_use, -m_use);
+                        uint64_t acc[2] = {0ull, 0ull};
+#pragma unroll
+                        for (int w = 0; w < DT / 32; ++w) {
+                            uint32_t x[32], pk[16];
+                            scores(w, x);
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) {
+                                const float2 e = f2_split(
+                                    fma2(f2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), cl2x2, nm2));
+                                const float p0 = ex2(e.x), p1 = ex2(e.y);
+                                acc[c & 1] = add2(acc[c & 1], f2(p0, p1));
+                                pk[c] = pack_bf16x2(p0, p1);
+                            }
+                            tmem_st16(tS + 16 * w, pk);  // over scores that were read
+                        }
+                        tmem_st_wait();
+                        const float2 sum = f2_split(add2(acc[0], acc[1]));
+                        l = l * alpha + (sum.x + sum.y);
+                        m_ref = m_new;
+                    } else {
                     float sv[DT];
                     {
                         uint32_t r0[32], r1[32], r2[32], r3[32];
@@ -466,21 +524,7 @@ __global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
                         }
                     }
                     const bool full = tile_w == DT && kbase + DT - 1 <= hi && (kbase >= lo || kbase + DT <= sk);
-                    if (KV4 && !tail && __any_sync(0xffffffffu, qpos < p.P - 1)) {
-                        // a query inside a 4-bit prompt: row by row, by position
-#pragma unroll
-                        for (int w = 0; w < DT / 32; ++w) {
-                            uint32_t k = 0;
-#pragma unroll 1
-                            for (int c = 0; c < 32; ++c) {
-                                const int row = kbase + 32 * w + c;
-                                if (row < p.P && row_position(p, row) <= qpos) k |= 1u << c;
-                            }
-#pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                if (!(k & (1u << c))) sv[32 * w + c] = -INFINITY;
-                        }
-                    } else if (!__all_sync(0xffffffffu, full)) {
+                    if (!__all_sync(0xffffffffu, full)) {
                         // columns past the tile's positions are never kept
                         const int h2 = min(hi - kbase, tile_w - 1), l2 = lo - kbase, s2 = sk - kbase;
 #pragma unroll
@@ -517,6 +561,7 @@ __global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
                     tmem_st_wait();
                     l = l * alpha + ((s01.x + s01.y) + (s23.x + s23.y));
                     m_ref = m_new;
+                    }
                 }
                 if (n > 0) {
                     // the previous product must be complete before O is
@@ -563,8 +608,9 @@ __global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
                     if (row_on)
 #pragma unroll
                         for (int v = 0; v < 8; ++v)
-                            dst[8 * c + v] = make_float4(__uint_as_float(rr[4 * v]), __uint_as_float(rr[4 * v + 1]),
-                                                         __uint_as_float(rr[4 * v + 2]), __uint_as_float(rr[4 * v + 3]));
+                            dst[8 * c + v] =
+                                make_float4(__uint_as_float(rr[4 * v]) * unit, __uint_as_float(rr[4 * v + 1]) * unit,
+                                            __uint_as_float(rr[4 * v + 2]) * unit, __uint_as_float(rr[4 * v + 3]) * unit);
                 }
                 tc_fence_before();
             }
