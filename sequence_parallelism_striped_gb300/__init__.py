@@ -492,6 +492,22 @@ def _need(t, name: str, shape, dtype, dev: int) -> int:
     raise ValueError(f"{name} must be contiguous")
 
 
+def _result(t, name: str, shape, dtype, dev: int, device):
+    """A result and its address: the caller's, checked, or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return t, _need(t, name, shape, dtype, dev)
+
+
+def _result_like(t, name: str, like, shape, dev: int):
+    """_result of the type and device of a contiguous tensor of that shape."""
+    if t is None:
+        t = torch.empty_like(like)
+        return t, t.data_ptr()
+    return t, _need(t, name, shape, like.dtype, dev)
+
+
 def _buffer(t, name: str, dev: int):
     """Address and bytes of a workspace."""
     _rank(t, name, 1)
@@ -671,18 +687,16 @@ def striped_kv4_store(k, v, k_codes=None, k_scales=None, v_codes=None, v_scales=
     if not _here(dev, stream):
         with _elsewhere(dev, stream):
             return striped_kv4_store(k, v, k_codes, k_scales, v_codes, v_scales)
-    B, Hkv, S, D = k.shape
-    code = _dtype_code(k)
-    cs, ss, u8, bf = (B, Hkv, S, D // 2), (B, Hkv, S, D // KV4_GROUP), torch.uint8, torch.bfloat16
-
-    def new(t, shape, dtype):
-        return torch.empty(shape, dtype=dtype, device=k.device) if t is None else t
-
-    kc, ks, vc, vs = new(k_codes, cs, u8), new(k_scales, ss, bf), new(v_codes, cs, u8), new(v_scales, ss, bf)
-    _check(load().striped_kv4_store(
-        _need(k, "k", k.shape, k.dtype, dev), _need(v, "v", k.shape, k.dtype, dev), _need(kc, "k_codes", cs, u8, dev),
-        _need(ks, "k_scales", ss, bf, dev), _need(vc, "v_codes", cs, u8, dev), _need(vs, "v_scales", ss, bf, dev), B,
-        Hkv, S, D, code, _raw_stream(dev)), "striped_kv4_store")
+    xs = B, Hkv, S, D = k.shape
+    cs, ss, u8, bf, dt = (B, Hkv, S, D // 2), (B, Hkv, S, D // KV4_GROUP), torch.uint8, torch.bfloat16, k.dtype
+    kp, vp = _need(k, "k", xs, dt, dev), _need(v, "v", xs, dt, dev)
+    code, device = _dtype_code(k), k.device
+    kc, kcp = _result(k_codes, "k_codes", cs, u8, dev, device)
+    ks, ksp = _result(k_scales, "k_scales", ss, bf, dev, device)
+    vc, vcp = _result_like(v_codes, "v_codes", kc, cs, dev)
+    vs, vsp = _result_like(v_scales, "v_scales", ks, ss, dev)
+    _check(load().striped_kv4_store(kp, vp, kcp, ksp, vcp, vsp, B, Hkv, S, D, code, _raw_stream(dev)),
+           "striped_kv4_store")
     return kc, ks, vc, vs
 
 
@@ -697,12 +711,12 @@ def striped_kv4_load(k_codes, k_scales, v_codes, v_scales, k=None, v=None, strea
     cs = B, Hkv, S, half = k_codes.shape
     D, u8, bf = 2 * half, torch.uint8, torch.bfloat16
     xs, ss = (B, Hkv, S, D), (B, Hkv, S, D // KV4_GROUP)
-    k = torch.empty(xs, dtype=bf, device=k_codes.device) if k is None else k
-    v = torch.empty(xs, dtype=bf, device=k_codes.device) if v is None else v
-    _check(load().striped_kv4_load(
-        _need(k_codes, "k_codes", cs, u8, dev), _need(k_scales, "k_scales", ss, bf, dev),
-        _need(v_codes, "v_codes", cs, u8, dev), _need(v_scales, "v_scales", ss, bf, dev), _need(k, "k", xs, bf, dev),
-        _need(v, "v", xs, bf, dev), B, Hkv, S, D, BF16, _raw_stream(dev)), "striped_kv4_load")
+    kcp, ksp = _need(k_codes, "k_codes", cs, u8, dev), _need(k_scales, "k_scales", ss, bf, dev)
+    vcp, vsp = _need(v_codes, "v_codes", cs, u8, dev), _need(v_scales, "v_scales", ss, bf, dev)
+    k, kp = _result(k, "k", xs, bf, dev, k_codes.device)
+    v, vp = _result_like(v, "v", k, xs, dev)
+    _check(load().striped_kv4_load(kcp, ksp, vcp, vsp, kp, vp, B, Hkv, S, D, BF16, _raw_stream(dev)),
+           "striped_kv4_load")
     return k, v
 
 
@@ -739,17 +753,17 @@ def striped_attn_decode_kv4(q, k_codes, k_scales, v_codes, v_scales, k_tail, v_t
             return striped_attn_decode_kv4(q, k_codes, k_scales, v_codes, v_scales, k_tail, v_tail, tail_lens, N,
                                            layout, scale, workspace, out, lse_out)
     dt, code, u8, bf, f32 = q.dtype, _dtype_code(q), torch.uint8, torch.bfloat16, torch.float32
-    cs, ss, tail = (Bp, Hkv, P, D // 2), (Bp, Hkv, P, D // KV4_GROUP), (B, Hkv, C, D)
-    o = torch.empty_like(q) if out is None else out
-    lse = torch.empty((B, H, T), dtype=f32, device=q.device) if lse_out is None else lse_out
+    cs, ss, tail, qs = (Bp, Hkv, P, D // 2), (Bp, Hkv, P, D // KV4_GROUP), (B, Hkv, C, D), (B, H, T, D)
+    qp, kcp = _need(q, "q", qs, dt, dev), _need(k_codes, "k_codes", cs, u8, dev)
+    ksp, vcp = _need(k_scales, "k_scales", ss, bf, dev), _need(v_codes, "v_codes", cs, u8, dev)
+    vsp, ktp = _need(v_scales, "v_scales", ss, bf, dev), _need(k_tail, "k_tail", tail, dt, dev)
+    vtp, lp = _need(v_tail, "v_tail", tail, dt, dev), _need(tail_lens, "tail_lens", (B,), torch.int32, dev)
+    o, op = _result_like(out, "out", q, qs, dev)
+    lse, lsep = _result(lse_out, "lse_out", (B, H, T), f32, dev, q.device)
     wp, wn, workspace = _work(workspace, _decode_kv4_workspace_size, dev, *n, N, layout, code)
-    _check(load().striped_attn_decode_kv4(
-        _need(q, "q", q.shape, dt, dev), _need(k_codes, "k_codes", cs, u8, dev),
-        _need(k_scales, "k_scales", ss, bf, dev), _need(v_codes, "v_codes", cs, u8, dev),
-        _need(v_scales, "v_scales", ss, bf, dev), _need(k_tail, "k_tail", tail, dt, dev),
-        _need(v_tail, "v_tail", tail, dt, dev), _need(tail_lens, "tail_lens", (B,), torch.int32, dev),
-        _need(o, "out", q.shape, dt, dev), _need(lse, "lse_out", (B, H, T), f32, dev), wp, wn, *n, N, layout, code,
-        1.0 / D ** 0.5 if scale is None else scale, _raw_stream(dev)), "striped_attn_decode_kv4")
+    _check(load().striped_attn_decode_kv4(qp, kcp, ksp, vcp, vsp, ktp, vtp, lp, op, lsep, wp, wn, *n, N, layout, code,
+                                          1.0 / D ** 0.5 if scale is None else scale, _raw_stream(dev)),
+           "striped_attn_decode_kv4")
     return o, lse
 
 
@@ -787,34 +801,40 @@ def striped_attn_key_weight(q, k, lse, N: int, layout: int = STRIPED, first: int
             return striped_attn_key_weight(q, k, lse, N, layout, first, scale, accumulate, workspace, weight)
     qs = B, H, S, D = q.shape
     Hkv, dt, code, f32 = k.shape[1], q.dtype, _dtype_code(q), torch.float32
-    w = torch.empty((B, Hkv, S), dtype=f32, device=q.device) if weight is None else weight
+    qp, kp = _need(q, "q", qs, dt, dev), _need(k, "k", (B, Hkv, S, D), dt, dev)
+    lp = _need(lse, "lse", (B, H, S), f32, dev)
+    w, p = _result(weight, "weight", (B, Hkv, S), f32, dev, q.device)
     wp, wn, workspace = _work(workspace, _key_weight_workspace_size, dev, B, H, Hkv, S, D, N, layout, code, first)
-    _check(load().striped_attn_key_weight(
-        _need(q, "q", qs, dt, dev), _need(k, "k", (B, Hkv, S, D), dt, dev), _need(lse, "lse", (B, H, S), f32, dev),
-        _need(w, "weight", (B, Hkv, S), f32, dev), wp, wn, B, H, Hkv, S, D, N, layout, code, first,
-        1 if accumulate else 0, 1.0 / D ** 0.5 if scale is None else scale, _raw_stream(dev)),
-        "striped_attn_key_weight")
+    _check(load().striped_attn_key_weight(qp, kp, lp, p, wp, wn, B, H, Hkv, S, D, N, layout, code, first,
+                                          1 if accumulate else 0, 1.0 / D ** 0.5 if scale is None else scale,
+                                          _raw_stream(dev)), "striped_attn_key_weight")
     return w
 
 
+_TWO, _TWO_SIZES = ctypes.c_void_p * 2, ctypes.c_int64 * 2
+_FOUR, _FOUR_SIZES = ctypes.c_void_p * 4, ctypes.c_int64 * 4
+
+
 def _evict(tensors, names, weight, keep, sinks, recent, N, layout, outs, index, weight_out):
-    """striped_kv_evict of tensors [B,Hkv,S,row] whose rows begin on 4 bytes."""
-    dev = weight.get_device()
-    B, Hkv, S = weight.shape
-    f32, i32, n = torch.float32, torch.int32, len(tensors)
-    outs = [torch.empty((B, Hkv, keep, t.shape[-1]), dtype=t.dtype, device=t.device) if o is None else o
-            for t, o in zip(tensors, outs)]
-    index = torch.empty((B, Hkv, keep), dtype=i32, device=weight.device) if index is None else index
-    weight_out = torch.empty((B, Hkv, keep), dtype=f32, device=weight.device) if weight_out is None else weight_out
-    xs = [_need(t, m, (B, Hkv, S, t.shape[-1]), t.dtype, dev) for t, m in zip(tensors, names)]
-    ys = [_need(o, m + "_out", (B, Hkv, keep, t.shape[-1]), t.dtype, dev) for t, o, m in zip(tensors, outs, names)]
-    rows = [t.shape[-1] * t.element_size() for t in tensors]
-    _check(load().striped_kv_evict(
-        (ctypes.c_void_p * n)(*xs), (ctypes.c_void_p * n)(*ys), (ctypes.c_int64 * n)(*rows), n,
-        _need(weight, "weight", (B, Hkv, S), f32, dev), _need(index, "index", (B, Hkv, keep), i32, dev),
-        _need(weight_out, "weight_out", (B, Hkv, keep), f32, dev), B, Hkv, S, keep, sinks, recent, N, layout,
-        _raw_stream(dev)), "striped_kv_evict")
-    return (*outs, index, weight_out)
+    """striped_kv_evict of two or four tensors [B,Hkv,S,row] whose rows begin on 4 bytes."""
+    dev, device = weight.get_device(), weight.device
+    ws = B, Hkv, S = weight.shape
+    kept, n, f32 = (B, Hkv, keep), len(tensors), torch.float32
+    xs, ys, rows, res = [], [], [], []
+    for t, o, m in zip(tensors, outs, names):
+        row, dt = t.shape[-1], t.dtype
+        xs.append(_need(t, m, (B, Hkv, S, row), dt, dev))
+        o, p = _result(o, m + "_out", (B, Hkv, keep, row), dt, dev, device)
+        res.append(o)
+        ys.append(p)
+        rows.append(row * dt.itemsize)
+    wp = _need(weight, "weight", ws, f32, dev)
+    index, ip = _result(index, "index", kept, torch.int32, dev, device)
+    weight_out, wop = _result(weight_out, "weight_out", kept, f32, dev, device)
+    ptrs, sizes = (_TWO, _TWO_SIZES) if n == 2 else (_FOUR, _FOUR_SIZES)
+    _check(load().striped_kv_evict(ptrs(*xs), ptrs(*ys), sizes(*rows), n, wp, ip, wop, B, Hkv, S, keep, sinks, recent, N,
+                                   layout, _raw_stream(dev)), "striped_kv_evict")
+    return (*res, index, weight_out)
 
 
 def _kept(keep, weight):

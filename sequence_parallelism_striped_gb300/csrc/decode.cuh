@@ -289,7 +289,8 @@ bool decode_plan(DecPlan *plan, const DecodeArgs &a) {
     p.ep = (int)ep;
     p.entries = (int)entries;
     p.scale = a.scale;
-    const int ctas = device_sm_count() * (plan->small && rows_p <= 8 ? 2 : 1);
+    const int sms = device_sm_count();  // no device: sizes are still told
+    const int ctas = (sms > 0 ? sms : 152) * (plan->small && rows_p <= 8 ? 2 : 1);
     plan->parts = (int)(tiles < ctas ? tiles : ctas);
     p.slot_rows[0] = (int)(rows_p < DT ? rows_p : DT);
     p.slot_rows[1] = (int)(per < DT ? per : DT);
