@@ -26,7 +26,13 @@ namespace {
 
 constexpr int kEThreads = 1024;
 constexpr int kEWarps = kEThreads / 32;
-constexpr int kDigit = 256;
+// 11, 11 and 10 bits: with 8 at a time, most weights of a prompt share a few first
+// digits (an exponent less its last bit), and their counts are added one after
+// another
+constexpr int kDigitBits = 11;
+constexpr int kDigit = 1 << kDigitBits;
+constexpr int kBatch = 8;      // loads of a thread in flight
+constexpr int kMaxBlocks = 8;  // of a cluster
 // positions whose numbers a block holds in shared memory; a longer part is read
 // from the weights (from L2) in every pass
 constexpr int kEHeld = 49152;
@@ -63,7 +69,6 @@ struct SelectShared {
     uint32_t hist[2][kDigit];  // of this block, by the parity of the digit
     uint32_t above[kEWarps], at[kEWarps];
     uint32_t sum_above, sum_at;
-    uint32_t total[kDigit];
     uint32_t digit, left;
 };
 
@@ -87,67 +92,83 @@ __global__ void __launch_bounds__(kEThreads, 1) kv_select_kernel(const SelectArg
         if (a.g.layout == STRIPED_LAYOUT_STRIPED && a.g.N > 1 && a.g.N <= 1024) {
             // stripe by stripe, so that neighbouring lanes read neighbouring rows
             const uint32_t N = a.g.N, per = n / N + 2, i0 = p0 / N;
-            for (uint32_t f = threadIdx.x; f < per * N; f += kEThreads) {
-                const uint32_t d = f / per, p = (i0 + (f - d * per)) * N + d;
-                if (p >= p0 && p < p1) held[p - p0] = number(p);
+            for (uint32_t f0 = threadIdx.x; f0 < per * N; f0 += kBatch * kEThreads) {
+                uint32_t p[kBatch];
+                float w[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const uint32_t f = f0 + k * kEThreads, d = f / per, i = i0 + (f - d * per);
+                    p[k] = f < per * N ? i * N + d : 0xffffffffu;
+                    w[k] = p[k] >= p0 && p[k] < p1 ? __ldg(weight + d * a.g.L + i) : 0.f;
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k)
+                    if (p[k] >= p0 && p[k] < p1)
+                        held[p[k] - p0] = p[k] < a.sinks || p[k] >= tail ? ~0u : order_of(w[k]);
             }
         } else {
-            for (int i = threadIdx.x; i < n; i += kEThreads) held[i] = number(p0 + i);
+            for (int i0 = threadIdx.x; i0 < n; i0 += kBatch * kEThreads) {
+                uint32_t v[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) v[k] = i0 + k * kEThreads < n ? number(p0 + i0 + k * kEThreads) : 0u;
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k)
+                    if (i0 + k * kEThreads < n) held[i0 + k * kEThreads] = v[k];
+            }
         }
     }
     for (int i = threadIdx.x; i < 2 * kDigit; i += kEThreads) sh.hist[i / kDigit][i % kDigit] = 0;
+    static_assert(kDigit == 2 * kEThreads && kEWarps == 32, "a thread has two digits, a lane a warp's sum");
     __syncthreads();
     // digits from the highest on; `left` of the numbers that begin with
     // `prefix` are among the largest `keep`
     uint32_t prefix = 0, left = a.keep;
-#pragma unroll 1
-    for (int pass = 0; pass < 4; ++pass) {
-        const int shift = 24 - 8 * pass;
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const int above_shift = pass == 1 ? 21 : 10;  // where the digits before this one end
+        const uint32_t mask = pass == 2 ? 1023u : kDigit - 1u;
         uint32_t *hist = sh.hist[pass & 1];
+#pragma unroll 4
         for (int i = threadIdx.x; i < n; i += kEThreads) {
             const uint32_t v = hold ? held[i] : number(p0 + i);
-            if (pass == 0 || (v >> (shift + 8)) == prefix) atomicAdd(&hist[(v >> shift) & (kDigit - 1)], 1u);
+            if (pass == 0 || (v >> above_shift) == prefix) atomicAdd(&hist[(v >> shift) & mask], 1u);
         }
         cluster.sync();
-        if (threadIdx.x < kDigit) {
-            uint32_t sum = 0;
-            for (int b = 0; b < blocks; ++b) sum += cluster.map_shared_rank(hist, b)[threadIdx.x];
-            sh.total[threadIdx.x] = sum;
-            // the counts of the other parity were read before this barrier
-            sh.hist[(pass + 1) & 1][threadIdx.x] = 0;
+        // thread t has the digits 2 t and 2 t + 1, over all blocks
+        uint2 c = make_uint2(0u, 0u), part[kMaxBlocks];
+#pragma unroll
+        for (int b = 0; b < kMaxBlocks; ++b)
+            part[b] = b < blocks ? reinterpret_cast<const uint2 *>(cluster.map_shared_rank(hist, b))[threadIdx.x]
+                                 : make_uint2(0u, 0u);
+#pragma unroll
+        for (int b = 0; b < kMaxBlocks; ++b) c.x += part[b].x, c.y += part[b].y;
+        // the counts of the other parity were read before this barrier
+        reinterpret_cast<uint2 *>(sh.hist[(pass + 1) & 1])[threadIdx.x] = make_uint2(0u, 0u);
+        // numbers of the higher digits: first those of this warp, then of others
+        uint32_t run = c.x + c.y;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_down_sync(0xffffffffu, run, o);
+            if (lane + o < 32) run += x;
         }
+        if (lane == 0) sh.above[warp] = run;
         __syncthreads();
-        if (warp == 0) {
-            // lane l has digits 8 l .. 8 l + 7; `over`: numbers of higher digits
-            uint32_t c[kDigit / 32], sum = 0;
-#pragma unroll
-            for (int j = 0; j < kDigit / 32; ++j) sum += c[j] = sh.total[lane * (kDigit / 32) + j];
-            uint32_t run = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t x = __shfl_down_sync(0xffffffffu, run, o);
-                if (lane + o < 32) run += x;
-            }
-            uint32_t over = run - sum;
-            if (over < left && left <= run) {
-#pragma unroll
-                for (int j = kDigit / 32 - 1; j >= 0; --j) {
-                    if (over < left && left <= over + c[j]) {
-                        sh.digit = lane * (kDigit / 32) + j;
-                        sh.left = left - over;
-                    }
-                    over += c[j];
-                }
-            }
-        }
+        uint32_t higher = sh.above[lane];  // lane w: what warp w has
+        higher = __reduce_add_sync(0xffffffffu, lane > warp ? higher : 0u);
+        uint32_t over = higher + run - (c.x + c.y);
+        if (over < left && left <= over + c.y) sh.digit = 2 * threadIdx.x + 1, sh.left = left - over;
+        over += c.y;
+        if (over < left && left <= over + c.x) sh.digit = 2 * threadIdx.x, sh.left = left - over;
         __syncthreads();
-        prefix = (prefix << 8) | sh.digit;
+        prefix = (prefix << (pass == 2 ? 10 : kDigitBits)) | sh.digit;
         left = sh.left;
     }
     // every warp counts a stretch of the block's positions, then writes it
     const int per = (int)(a.part / kEWarps);
     const int i0 = min(warp * per, n), i1 = min(i0 + per, n);
     uint32_t above = 0, at = 0;
+#pragma unroll 4
     for (int i = i0 + lane; i < i1; i += 32) {
         const uint32_t v = hold ? held[i] : number(p0 + i);
         above += v > prefix;
@@ -163,13 +184,15 @@ __global__ void __launch_bounds__(kEThreads, 1) kv_select_kernel(const SelectArg
         if (lane == 0) sh.sum_above = sa, sh.sum_at = st;
     }
     cluster.sync();
-    uint32_t before_above = 0, before_at = 0;
-    for (int b = 0; b < rank; ++b) {
-        before_above += *cluster.map_shared_rank(&sh.sum_above, b);
-        before_at += *cluster.map_shared_rank(&sh.sum_at, b);
+    uint32_t before_above = lane < warp ? sh.above[lane] : 0u, before_at = lane < warp ? sh.at[lane] : 0u;
+    if (lane < rank) {
+        before_above += *cluster.map_shared_rank(&sh.sum_above, lane);
+        before_at += *cluster.map_shared_rank(&sh.sum_at, lane);
     }
-    for (int w = 0; w < warp; ++w) before_above += sh.above[w], before_at += sh.at[w];
+    before_above = __reduce_add_sync(0xffffffffu, before_above);
+    before_at = __reduce_add_sync(0xffffffffu, before_at);
     int32_t *index = a.index + line * a.keep;
+#pragma unroll 4
     for (int i = i0; i < i1; i += 32) {
         const bool in = i + lane < i1;
         const uint32_t v = in ? (hold ? held[i + lane] : number(p0 + i + lane)) : 0u;
@@ -198,13 +221,14 @@ struct GatherArgs {
 };
 
 // V a lane, 2^log lanes a row (more than a row has: some idle; fewer: they go on
-// behind one another), four rows in flight.
+// behind one another), two rows in flight: more take registers and with them
+// lanes (16384 of 131072 rows, 8 heads: 42 us at 8 rows, 31 at 4, 22 so).
 template <typename V>
 __device__ __forceinline__ void gather_rows(const GatherArgs &a, int t) {
     const int log = a.lanes_log[t], per = a.row_bytes[t] / (int)sizeof(V);
     const uint32_t first = (blockIdx.x * kGThreads + threadIdx.x) >> log, step = (gridDim.x * kGThreads) >> log;
     const int c0 = threadIdx.x & ((1 << log) - 1);
-    constexpr int U = 4;
+    constexpr int U = 2;
     for (int64_t line = blockIdx.z; line < a.lines; line += gridDim.z) {
         const V *x = reinterpret_cast<const V *>(a.x[t]) + line * a.g.S * per;
         V *y = reinterpret_cast<V *>(a.y[t]) + line * a.keep * per;
@@ -218,16 +242,16 @@ __device__ __forceinline__ void gather_rows(const GatherArgs &a, int t) {
                 V v[U];
 #pragma unroll
                 for (int k = 0; k < U; ++k)
-                    if (r + k * step < a.keep) v[k] = x[(int64_t)from[k] * per + c];
+                    if (r + k * step < a.keep) v[k] = __ldcs(x + (int64_t)from[k] * per + c);
 #pragma unroll
                 for (int k = 0; k < U; ++k)
-                    if (r + k * step < a.keep) y[(int64_t)(r + k * step) * per + c] = v[k];
+                    if (r + k * step < a.keep) __stcs(y + (int64_t)(r + k * step) * per + c, v[k]);
             }
         }
     }
 }
 
-__global__ void __launch_bounds__(kGThreads) kv_gather_kernel(const GatherArgs a) {
+__global__ void __launch_bounds__(kGThreads, 8) kv_gather_kernel(const GatherArgs a) {
     wait_for_previous();
     const int t = blockIdx.y;
     if (a.row_bytes[t] % 16 == 0) gather_rows<uint4>(a, t);
@@ -257,7 +281,7 @@ int launch_kv_evict(const EvictArgs &e, cudaStream_t stream) {
     s.sinks = (uint32_t)e.sinks;
     s.recent = (uint32_t)e.recent;
     int blocks = 1;
-    while (blocks < 8 && blocks * (int64_t)kEPart < e.S) blocks *= 2;
+    while (blocks < kMaxBlocks && blocks * (int64_t)kEPart < e.S) blocks *= 2;
     s.part = (uint32_t)(((e.S + blocks - 1) / blocks + kEThreads - 1) / kEThreads * kEThreads);
     if (e.lines * blocks > 0x7fffffff) return STRIPED_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg{};
@@ -294,9 +318,9 @@ int launch_kv_evict(const EvictArgs &e, cudaStream_t stream) {
     ga.keep = s.keep;
     ga.lines = e.lines;
     if (n == 0) return STRIPED_OK;
-    // four rows a lane, but no more blocks than fill the GPU a few times over
+    // two rows a lane, but no more blocks than fill the GPU a few times over
     const uint64_t z = e.lines < 65535 ? e.lines : 65535;
-    uint64_t x = (lanes + 4 * kGThreads - 1) / (4 * kGThreads);
+    uint64_t x = (lanes + 2 * kGThreads - 1) / (2 * kGThreads);
     const uint64_t most = (16 * (uint64_t)device_sm_count() + z - 1) / z;
     x = x > most ? most : x;
     return launch_after(kv_gather_kernel, dim3((unsigned)x, (unsigned)n, (unsigned)z), kGThreads, 0, stream, ga);
