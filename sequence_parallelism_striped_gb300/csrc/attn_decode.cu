@@ -46,12 +46,9 @@
 // softmax, product and join.
 #include <math.h>
 
-#include <type_traits>
-
 #include "common.cuh"
 #include "decode.cuh"
 #include "internal.h"
-#include "kv4.cuh"
 #include "window.cuh"
 
 namespace striped {
@@ -60,7 +57,6 @@ namespace {
 
 constexpr uint32_t kDBox = 128 * 128;   // 128 rows x 64 bf16
 constexpr int kDThreads = 192;
-constexpr int kDThreads4 = kDThreads + 256;
 constexpr float kDRescale = 8.0f;       // lazy rescale threshold, log2 units
 
 template <int HD>
@@ -83,15 +79,8 @@ struct DecBars {
     int scan[kDThreads / 32];
 };
 
-// KV4: the prompt is in 4 bits.  Eight more warps make its tiles, four those of K
-// and four those of V: thread t takes the codes and scales of row t from memory,
-// a tile ahead, and writes the values, which are bf16 numbers (times 2^-6:
-// kv4.cuh), where TMA puts the rows of a bf16 prompt.  With them there are 128
-// registers a thread, so the softmax reads a row's scores twice, 32 at a time
-// (32 requests on 131072: 157 us with four such warps and the scores in
-// registers, which bounds them by the latency of a warp alone).
-template <int HD, bool KV4>
-__global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
+template <int HD>
+__global__ void __launch_bounds__(kDThreads, 1)
     tc_decode_kernel(const __grid_constant__ CUtensorMap tmKp, const __grid_constant__ CUtensorMap tmVp,
                      const __grid_constant__ CUtensorMap tmKt, const __grid_constant__ CUtensorMap tmVt,
                      const DecParams p) {
@@ -112,7 +101,7 @@ __global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&bars->q_full), 4);
         for (int s = 0; s < NS; ++s) {
-            mbar_init(smem_u32(&bars->kv_full[s]), KV4 ? 9 : 1);
+            mbar_init(smem_u32(&bars->kv_full[s]), 1);
             mbar_init(smem_u32(&bars->kv_empty[s]), 1);
         }
         mbar_init(smem_u32(&bars->s_full[0]), 1);
@@ -126,7 +115,7 @@ __global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
         tmem_alloc(smem_u32(&bars->tmem_slot), 512);
         tmem_relinquish();
     }
-    if (!KV4 && p.ep > 0 && g.P < DT) {
+    if (p.ep > 0 && g.P < DT) {
         // rows past a prompt tile's positions are never loaded: V has to be
         // finite there, because P = 0 times it is added to O
         for (uint32_t i = threadIdx.x * 16; i < NS * kStage; i += kDThreads * 16)
@@ -135,7 +124,7 @@ __global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
     }
     // every entry's span, and the running count of key tiles before it
     {
-        const int per = (p.entries + kDThreads - 1) / kDThreads;  // the first kDThreads threads have some
+        const int per = (p.entries + kDThreads - 1) / kDThreads;
         const int e0 = min((int)threadIdx.x * per, p.entries), e1 = min(e0 + per, p.entries);
         int sum = 0;
         for (int e = e0; e < e1; ++e) {
@@ -150,10 +139,10 @@ __global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
             const int v = __shfl_up_sync(0xffffffffu, run, o);
             if (lane >= o) run += v;
         }
-        if (lane == 31 && warp < kDThreads / 32) bars->scan[warp] = run;
+        if (lane == 31) bars->scan[warp] = run;
         __syncthreads();
         int before = run - sum;
-        for (int w = 0; w < min(warp, kDThreads / 32); ++w) before += bars->scan[w];
+        for (int w = 0; w < warp; ++w) before += bars->scan[w];
         for (int e = e0; e < e1; ++e) {
             cum[e + 1] += before;
             if (blockIdx.x == 0) p.cum[e + 1] = cum[e + 1];
@@ -209,10 +198,6 @@ __global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
                 const TileAt at = tail ? TileAt{kt * DT, 0} : tile_at(g, kt);
                 const uint32_t fb = smem_u32(&bars->kv_full[s]);
                 const uint32_t kdst = sbase + s * kStage, vdst = kdst + kTile;
-                if (KV4 && !tail) {
-                    mbar_arrive(fb);  // the dequantising warps write this tile
-                    continue;
-                }
                 mbar_arrive_expect_tx(fb, bytes);
 #pragma unroll
                 for (int c = 0; c < kBoxes; ++c) {
@@ -280,82 +265,12 @@ __global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
         // every MMA issued above completes before TMEM is freed (error paths)
         if (leader) mma_commit(smem_u32(&bars->drain));
         mbar_wait_warp(smem_u32(&bars->drain), 0, p.wc);
-    } else if (KV4 && warp >= kDThreads / 32 && nx > 0) {
-        // ---------------- 4 bits -> bf16
-        const bool is_v = warp >= kDThreads / 32 + 4;
-        const int r = (threadIdx.x - kDThreads) & 127;  // row of the tile
-        constexpr int V = HD / 32;                      // groups of a row: 16 bytes of codes, one scale
-        using Scales = typename std::conditional<HD == 128, uint2, uint32_t>::type;
-        const uint4 *codes = reinterpret_cast<const uint4 *>(is_v ? p.v_codes : p.k_codes);
-        const Scales *scales = reinterpret_cast<const Scales *>(is_v ? p.v_scales : p.k_scales);
-        // this thread's row of the tile that is written next
-        uint4 code[V];
-        Scales scale{};
-        // walks over the prompt tiles of this CTA, one ahead of the writing
-        int fx = x0, ft = 0;
-        Segment fs{};
-        fs.t1 = 0;
-        auto fetch = [&]() {
-            ++ft;
-            while (ft >= fs.t1) {
-                if (fx >= x1) return;
-                fs = segment(fx);
-                fx = fs.next;
-                ft = fs.e < p.ep ? fs.t0 : fs.t1;  // tails are not ours
-            }
-            const int row = ft * DT + r;
-#pragma unroll
-            for (int i = 0; i < V; ++i) code[i] = make_uint4(0u, 0u, 0u, 0u);
-            scale = Scales{};
-            if (row < p.P) {
-                const int64_t at = ((int64_t)(fs.e / p.nrt_p) * p.Hkv + fs.hkv) * p.P + row;
-#pragma unroll
-                for (int i = 0; i < V; ++i) code[i] = __ldg(codes + at * V + i);
-                scale = __ldg(scales + at);
-            }
-        };
-        fetch();
-        int j = 0;
-        bool ok = true;
-        for (int x = x0; x < x1 && ok;) {
-            const Segment sg = segment(x);
-            x = sg.next;
-            const bool tail = sg.e >= p.ep;
-            for (int t = sg.t0; t < sg.t1; ++t, ++j) {
-                const int s = j % NS;
-                if (j >= NS && !mbar_wait_warp(smem_u32(&bars->kv_empty[s]), ((j / NS) + 1) & 1, p.wc)) {
-                    ok = false;
-                    break;
-                }
-                if (!tail) {
-                    uint8_t *tile = smem + s * kStage + (is_v ? kTile : 0) + r * 128;
-                    const uint32_t *sw = reinterpret_cast<const uint32_t *>(&scale);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const uint32_t s2 = __byte_perm(sw[i / 2], 0, i % 2 ? 0x3232 : 0x1010);
-                        const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int chunk = 4 * i + k;  // 8 channels
-                            uint32_t c[4];
-                            kv4_pairs(w[k], c);
-                            *reinterpret_cast<uint4 *>(tile + chunk / 8 * kDBox + (((chunk & 7) ^ (r & 7)) * 16)) =
-                                make_uint4(bf16x2_mul(c[0], s2), bf16x2_mul(c[1], s2), bf16x2_mul(c[2], s2),
-                                           bf16x2_mul(c[3], s2));
-                        }
-                    }
-                    fetch();
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                if (lane == 0) mbar_arrive(smem_u32(&bars->kv_full[s]));
-            }
-        }
     } else if (warp >= 2 && nx > 0) {
         // ---------------- softmax + partial results
         const int quarter = warp & 3;
         const int ri = quarter * 32 + lane;  // row of the tile
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        const float cl2 = p.scale * 1.4426950408889634f;
         const int per = p.G * p.T;
         int j = 0;
         bool ok = true;
@@ -364,8 +279,6 @@ __global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
             x = sg.next;
             if (sg.t1 <= sg.t0) continue;
             const bool tail = sg.e >= p.ep;
-            const float unit = KV4 && !tail ? kKv4Unit : 1.f;  // of the values in the tiles
-            const float cl2 = p.scale * 1.4426950408889634f * unit;
             // this thread's query row: request b, head h, token t
             int grp, rt, rows;
             if (tail) {
@@ -443,67 +356,6 @@ __global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
                         break;
                     }
                     tc_fence_after();
-                    if constexpr (KV4) {
-                        // columns that are kept, 32 bits at a time
-                        const bool inside = !tail && __any_sync(0xffffffffu, qpos < p.P - 1);
-                        const bool full = !inside && __all_sync(0xffffffffu, kbase + DT - 1 <= hi);
-                        uint32_t keep[DT / 32];
-                        if (!full)
-#pragma unroll
-                            for (int w = 0; w < DT / 32; ++w) {
-                                keep[w] = kept_bits(32 * w, hi - kbase, lo - kbase, 0);
-                                if (inside) {  // a query inside the prompt keeps rows by their position
-                                    keep[w] = 0;
-#pragma unroll 1
-                                    for (int c = 0; c < 32; ++c) {
-                                        const int row = kbase + 32 * w + c;
-                                        if (row < p.P && row_position(p, row) <= qpos) keep[w] |= 1u << c;
-                                    }
-                                }
-                            }
-                        auto scores = [&](int w, uint32_t (&x)[32]) {
-                            tmem_ld32(tS + 32 * w, x);
-                            tmem_ld_wait(x);
-                            if (!full)
-#pragma unroll
-                                for (int c = 0; c < 32; ++c)
-                                    if (!(keep[w] & (1u << c))) x[c] = 0xff800000u;  // -infinity
-                        };
-                        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                        for (int w = 0; w < DT / 32; ++w) {
-                            uint32_t x[32];
-                            scores(w, x);
-#pragma unroll
-                            for (int c = 0; c < 32; c += 2)
-                                top[(c >> 1) & 3] = fmax3(top[(c >> 1) & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-                        }
-                        const float m_tile = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * cl2;
-                        const bool move = n == 0 || m_tile > m_ref + kDRescale;
-                        const float m_new = move ? fmaxf(m_ref, m_tile) : m_ref;
-                        alpha = (n == 0 || !move) ? 1.f : ex2(m_ref - m_new);
-                        const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
-                        const uint64_t cl2x2 = f2(cl2, cl2), nm2 = f2(-m_use, -m_use);
-                        uint64_t acc[2] = {0ull, 0ull};
-#pragma unroll
-                        for (int w = 0; w < DT / 32; ++w) {
-                            uint32_t x[32], pk[16];
-                            scores(w, x);
-#pragma unroll
-                            for (int c = 0; c < 16; ++c) {
-                                const float2 e = f2_split(
-                                    fma2(f2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), cl2x2, nm2));
-                                const float p0 = ex2(e.x), p1 = ex2(e.y);
-                                acc[c & 1] = add2(acc[c & 1], f2(p0, p1));
-                                pk[c] = pack_bf16x2(p0, p1);
-                            }
-                            tmem_st16(tS + 16 * w, pk);  // over scores that were read
-                        }
-                        tmem_st_wait();
-                        const float2 sum = f2_split(add2(acc[0], acc[1]));
-                        l = l * alpha + (sum.x + sum.y);
-                        m_ref = m_new;
-                    } else {
                     float sv[DT];
                     {
                         uint32_t r0[32], r1[32], r2[32], r3[32];
@@ -561,7 +413,6 @@ __global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
                     tmem_st_wait();
                     l = l * alpha + ((s01.x + s01.y) + (s23.x + s23.y));
                     m_ref = m_new;
-                    }
                 }
                 if (n > 0) {
                     // the previous product must be complete before O is
@@ -608,9 +459,8 @@ __global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
                     if (row_on)
 #pragma unroll
                         for (int v = 0; v < 8; ++v)
-                            dst[8 * c + v] =
-                                make_float4(__uint_as_float(rr[4 * v]) * unit, __uint_as_float(rr[4 * v + 1]) * unit,
-                                            __uint_as_float(rr[4 * v + 2]) * unit, __uint_as_float(rr[4 * v + 3]) * unit);
+                            dst[8 * c + v] = make_float4(__uint_as_float(rr[4 * v]), __uint_as_float(rr[4 * v + 1]),
+                                                         __uint_as_float(rr[4 * v + 2]), __uint_as_float(rr[4 * v + 3]));
                 }
                 tc_fence_before();
             }
@@ -625,26 +475,26 @@ __global__ void __launch_bounds__(KV4 ? kDThreads4 : kDThreads, 1)
     }
 }
 
-template <int HD, bool KV4>
-int launch_decode_hd(const void *q, const void *kp, const void *vp, const Kv4Prompt &prompt, const void *kt,
-                     const void *vt, const int32_t *lens, void *o, float *lse, void *workspace, const DecodeArgs &a,
+template <int HD>
+int launch_decode_hd(const void *q, const void *kp, const void *vp, const void *kt, const void *vt,
+                     const int32_t *lens, void *o, float *lse, void *workspace, const DecodeArgs &a,
                      cudaStream_t stream) {
     static PerDeviceOnce once;
     const int attr = once.get([] {
-        return cuda_status(cudaFuncSetAttribute(
-            tc_decode_kernel<HD, KV4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)DecCfg<HD>::kSmemBytes));
+        return cuda_status(cudaFuncSetAttribute(tc_decode_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                (int)DecCfg<HD>::kSmemBytes));
     });
     if (attr != STRIPED_OK) return attr;
     DecPlan plan;
     if (!decode_plan(&plan, a)) return STRIPED_ERR_UNSUPPORTED;
     DecParams &p = plan.p;
-    decode_buffers(&plan, q, prompt, lens, o, lse, workspace);
+    decode_buffers(&plan, q, Kv4Prompt{}, lens, o, lse, workspace);
     CUtensorMap mkp, mvp, mkt, mvt;
     int st;
     if ((st = make_bf16_map(&mkt, kt, a.D, a.C, 1, a.B * a.Hkv, a.C * a.D, a.C * a.D, DT)) ||
         (st = make_bf16_map(&mvt, vt, a.D, a.C, 1, a.B * a.Hkv, a.C * a.D, a.C * a.D, DT)))
         return st;
-    if (p.ep > 0 && !KV4) {
+    if (p.ep > 0) {
         if ((st = make_pos_map(&mkp, kp, a.D, p.g, a.Bp * a.Hkv)) ||
             (st = make_pos_map(&mvp, vp, a.D, p.g, a.Bp * a.Hkv)))
             return st;
@@ -652,8 +502,7 @@ int launch_decode_hd(const void *q, const void *kp, const void *vp, const Kv4Pro
         mkp = mkt;  // never read
         mvp = mvt;
     }
-    tc_decode_kernel<HD, KV4><<<plan.parts, KV4 ? kDThreads4 : kDThreads, DecCfg<HD>::kSmemBytes, stream>>>(
-        mkp, mvp, mkt, mvt, p);
+    tc_decode_kernel<HD><<<plan.parts, kDThreads, DecCfg<HD>::kSmemBytes, stream>>>(mkp, mvp, mkt, mvt, p);
     if ((st = cuda_status(cudaGetLastError()))) return st;
     return launch_after(decode_join_kernel<HD>, dim3((unsigned)(a.B * a.H * a.T)), 128, 0, stream, p, plan.parts);
 }
@@ -669,17 +518,8 @@ size_t decode_workspace(const DecodeArgs &a) {
 int launch_tc_decode(const void *q, const void *kp, const void *vp, const void *kt, const void *vt,
                      const int32_t *lens, void *o, float *lse, void *workspace, const DecodeArgs &a,
                      cudaStream_t stream) {
-    const Kv4Prompt none{};
-    return a.D == 128
-               ? launch_decode_hd<128, false>(q, kp, vp, none, kt, vt, lens, o, lse, workspace, a, stream)
-               : launch_decode_hd<64, false>(q, kp, vp, none, kt, vt, lens, o, lse, workspace, a, stream);
-}
-
-int launch_tc_decode_kv4(const void *q, const Kv4Prompt &prompt, const void *kt, const void *vt, const int32_t *lens,
-                      void *o, float *lse, void *workspace, const DecodeArgs &a, cudaStream_t stream) {
-    return a.D == 128
-               ? launch_decode_hd<128, true>(q, nullptr, nullptr, prompt, kt, vt, lens, o, lse, workspace, a, stream)
-               : launch_decode_hd<64, true>(q, nullptr, nullptr, prompt, kt, vt, lens, o, lse, workspace, a, stream);
+    return a.D == 128 ? launch_decode_hd<128>(q, kp, vp, kt, vt, lens, o, lse, workspace, a, stream)
+                      : launch_decode_hd<64>(q, kp, vp, kt, vt, lens, o, lse, workspace, a, stream);
 }
 
 }  // namespace striped

@@ -1,6 +1,6 @@
 // attn_decode_kv4.cu -- decoding against a prompt in 4 bits when few query rows
 // share a prompt's key/value head (up to 16: its query heads and new tokens).
-// More rows go to the tcgen05 kernel (attn_decode.cu).
+// More rows go to attn_decode_kv4_tc.cu.
 //
 // A stored key and value take 9/32 of their bf16 bytes, so for few rows what
 // bounds the call is no longer only memory (18 KB for 128 keys at D = 128: 780
@@ -154,35 +154,7 @@ __global__ void __launch_bounds__(kQThreads, NT == 1 ? 2 : 1)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const float cl2 = p.scale * 1.4426950408889634f;
 
-    // the running cost of the entries
-    {
-        const int per = (p.entries + kQThreads - 1) / kQThreads;
-        const int e0 = min((int)threadIdx.x * per, p.entries), e1 = min(e0 + per, p.entries);
-        int sum = 0;
-        for (int e = e0; e < e1; ++e) {
-            const int n = entry_tiles<kTailTile>(p, e);
-            cum[e + 1] = sum += n > 0 ? n + p.over : 0;
-        }
-        int run = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, run, o);
-            if (lane >= o) run += v;
-        }
-        if (lane == 31) scan[warp] = run;
-        __syncthreads();
-        int before = run - sum;
-        for (int w = 0; w < warp; ++w) before += scan[w];
-        for (int e = e0; e < e1; ++e) {
-            cum[e + 1] += before;
-            if (blockIdx.x == 0) p.cum[e + 1] = cum[e + 1];
-        }
-        if (threadIdx.x == 0) {
-            cum[0] = 0;
-            if (blockIdx.x == 0) p.cum[0] = 0;
-        }
-        __syncthreads();
-    }
+    entry_costs<kTailTile, kQThreads>(p, cum, scan);
     let_next_begin();
     const int64_t total = (int64_t)cum[p.entries] * p.Hkv;
     const int parts = (int)min((int64_t)gridDim.x, total), cta = blockIdx.x;

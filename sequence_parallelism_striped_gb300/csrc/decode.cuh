@@ -98,6 +98,40 @@ __device__ __forceinline__ int entry_tiles(const DecParams &p, int e) {
     return (len_of(p, (e - p.ep) / p.nrt_t) + TT - 1) / TT;
 }
 
+// The running cost of the entries, cum[0 .. entries] in shared memory and, by
+// block 0, in p.cum, without windows: by all NT threads of a block, with a
+// barrier at the end.
+template <int TT, int NT>
+__device__ __forceinline__ void entry_costs(const DecParams &p, int *cum, int *scan) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int per = (p.entries + NT - 1) / NT;
+    const int e0 = min((int)threadIdx.x * per, p.entries), e1 = min(e0 + per, p.entries);
+    int sum = 0;
+    for (int e = e0; e < e1; ++e) {
+        const int n = entry_tiles<TT>(p, e);
+        cum[e + 1] = sum += n > 0 ? n + p.over : 0;
+    }
+    int run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += v;
+    }
+    if (lane == 31) scan[warp] = run;
+    __syncthreads();
+    int before = run - sum;
+    for (int w = 0; w < warp; ++w) before += scan[w];
+    for (int e = e0; e < e1; ++e) {
+        cum[e + 1] += before;
+        if (blockIdx.x == 0) p.cum[e + 1] = cum[e + 1];
+    }
+    if (threadIdx.x == 0) {
+        cum[0] = 0;
+        if (blockIdx.x == 0) p.cum[0] = 0;
+    }
+    __syncthreads();
+}
+
 // Share of CTA c of `parts`: tiles [share(c), share(c + 1)).
 __device__ __forceinline__ int share(int64_t total, int c, int parts) { return (int)(total * c / parts); }
 

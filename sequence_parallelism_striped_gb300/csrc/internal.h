@@ -176,9 +176,9 @@ struct Kv4Prompt {
     const void *k_codes, *k_scales, *v_codes, *v_scales;
 };
 size_t decode_workspace(const DecodeArgs &a);  // 0: no kernel for these sizes
+// ---- attn_decode_kv4.cu, and with many rows a prompt attn_decode_kv4_tc.cu
 int launch_tc_decode_kv4(const void *q, const Kv4Prompt &prompt, const void *kt, const void *vt, const int32_t *lens,
                          void *o, float *lse, void *workspace, const DecodeArgs &a, cudaStream_t stream);
-// ---- attn_decode_kv4.cu
 int launch_decode_kv4(const void *q, const Kv4Prompt &prompt, const void *kt, const void *vt, const int32_t *lens,
                       void *o, float *lse, void *workspace, const DecodeArgs &a, cudaStream_t stream);
 int launch_tc_decode(const void *q, const void *kp, const void *vp, const void *kt, const void *vt,
