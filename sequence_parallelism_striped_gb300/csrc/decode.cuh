@@ -310,7 +310,10 @@ bool decode_plan(DecPlan *plan, const DecodeArgs &a) {
     // D = 128: 386 us at a cost of 1, 308 at 2, 307 at 3, 309 at 4; 24
     // requests, window 4096, D = 64: 40.3 us at 1, 37.5 at 2, 34.8 at 4, 36.2
     // at 6, 37.5 at 8
-    p.over = a.D == 128 ? 2 : 4;
+    // With a 4-bit prompt a tile takes less: 4 at both D (1 request: 11.5 us at 2,
+    // 10.8 at 4, 11.0 at 6; 32 on one of 131072, tails of 8: 137, 98, 100; tails of
+    // 1000: 110, 111, 114)
+    p.over = a.D == 128 && !a.kv4 ? 2 : 4;
     plan->small = a.kv4 && rows_p <= 16;
     const int tail_tile = plan->small ? kTailTile : DT;
     const int64_t tiles =
