@@ -49,19 +49,20 @@ constexpr int kLBufs = 4;
 
 template <int HD>
 struct WeightCfg {
-    static constexpr int NS = HD == 128 ? 4 : 8;  // Q stages
+    static constexpr int NS = HD == 128 ? 3 : 6;  // Q stages
+    static constexpr int NK = HD == 128 ? 3 : 6;  // K tiles: read that many items ahead
     static constexpr uint32_t kTile = (HD / 64) * kWBox;
-    static constexpr uint32_t kKOff = NS * kTile;  // two K tiles
-    static constexpr uint32_t kLseOff = kKOff + 2 * kTile;
+    static constexpr uint32_t kKOff = NS * kTile;
+    static constexpr uint32_t kLseOff = kKOff + NK * kTile;
     static constexpr uint32_t kCombOff = kLseOff + kLBufs * KT * 4;
     static constexpr uint32_t kBarOff = kCombOff + KT * 4;
     static constexpr size_t kSmemBytes = 1024 + kBarOff + 512;
     static_assert(kSmemBytes <= 232448, "shared memory over the per-block limit");
 };
 
-template <int NS>
+template <int NS, int NK>
 struct WeightBars {
-    uint64_t k_full[2], k_empty[2];    // in shared memory
+    uint64_t k_full[NK], k_empty[NK];  // in shared memory
     uint64_t kt_full[2], kt_empty[2];  // in tensor memory
     uint64_t q_full[NS], q_empty[NS];
     uint64_t s_full[kSBufs], s_empty[kSBufs];
@@ -144,12 +145,12 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     tc_key_weight_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const WeightParams p) {
     using Cfg = WeightCfg<HD>;
-    constexpr int NS = Cfg::NS, kBoxes = HD / 64;
+    constexpr int NS = Cfg::NS, NK = Cfg::NK, kBoxes = HD / 64;
     constexpr uint32_t kTile = Cfg::kTile, kKCol = kSBufs * KT;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem =
         reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    WeightBars<NS> *bars = reinterpret_cast<WeightBars<NS> *>(smem + Cfg::kBarOff);
+    WeightBars<NS, NK> *bars = reinterpret_cast<WeightBars<NS, NK> *>(smem + Cfg::kBarOff);
     float *lse_s = reinterpret_cast<float *>(smem + Cfg::kLseOff);
     float *comb = reinterpret_cast<float *>(smem + Cfg::kCombOff);
     const uint32_t sbase = smem_u32(smem);
@@ -157,9 +158,11 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NK; ++i) {
             mbar_init(smem_u32(&bars->k_full[i]), 1);
             mbar_init(smem_u32(&bars->k_empty[i]), 4);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&bars->kt_full[i]), 4);
             mbar_init(smem_u32(&bars->kt_empty[i]), 1);
         }
@@ -203,21 +206,25 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         // ---------------- TMA producer
         const bool skip_first = p.wc.inject == kInjectFwdSkipKV;  // test hook: the first K tile is never loaded
         const uint32_t bytes = (uint32_t)g.P * 128 * kBoxes;
-        int j = 0, seg = 0;
+        int j = 0, seg = 0, kseg = 0;  // tiles, items whose queries and whose keys were asked for
         bool ok = true;
+        WeightItem kit(p, x0, x1);
         for (WeightItem it(p, x0, x1); it.x < x1 && ok; it.next(p, x1), ++seg) {
-            const int ks = seg & 1, b = it.line / p.Hkv, hkv = it.line - b * p.Hkv;
-            if (seg >= 2 && !mbar_wait(smem_u32(&bars->k_empty[ks]), ((seg >> 1) + 1) & 1, p.wc)) {
-                ok = false;
-                break;
-            }
-            if (!(skip_first && seg == 0)) {
-                const TileAt at = tile_at(g, it.kt);
+            for (; kit.x < x1 && kseg < seg + NK; kit.next(p, x1), ++kseg) {
+                const int ks = kseg % NK;
+                if (kseg >= NK && !mbar_wait(smem_u32(&bars->k_empty[ks]), ((kseg / NK) + 1) & 1, p.wc)) {
+                    ok = false;
+                    break;
+                }
+                if (skip_first && kseg == 0) continue;
+                const TileAt at = tile_at(g, kit.kt);
                 const uint32_t fb = smem_u32(&bars->k_full[ks]), dst = sbase + Cfg::kKOff + ks * kTile;
                 mbar_arrive_expect_tx(fb, bytes);
 #pragma unroll
-                for (int c = 0; c < kBoxes; ++c) tma_load_4d(dst + c * kWBox, &tmK, fb, 64 * c, at.c1, at.c2, it.line);
+                for (int c = 0; c < kBoxes; ++c) tma_load_4d(dst + c * kWBox, &tmK, fb, 64 * c, at.c1, at.c2, kit.line);
             }
+            if (!ok) break;
+            const int b = it.line / p.Hkv, hkv = it.line - b * p.Hkv;
             int head = b * p.H + hkv * p.G + it.n0 / it.cnt, qt = it.qlo + it.n0 % it.cnt;
             for (int n = it.n0; n < it.n1; ++n, ++j) {
                 const int s = j % NS;
@@ -235,8 +242,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         }
         // the last load of each stage has landed before the CTA exits
         for (int t = j > NS ? j - NS : 0; t < j; ++t) mbar_wait(smem_u32(&bars->q_full[t % NS]), (t / NS) & 1, p.wc);
-        for (int t = seg > 2 ? seg - 2 : 0; t < seg; ++t)
-            if (!(skip_first && t == 0)) mbar_wait(smem_u32(&bars->k_full[t & 1]), (t >> 1) & 1, p.wc);
+        for (int t = kseg > NK ? kseg - NK : 0; t < kseg; ++t)
+            if (!(skip_first && t == 0)) mbar_wait(smem_u32(&bars->k_full[t % NK]), (t / NK) & 1, p.wc);
     } else if (warp == 1) {
         // ---------------- MMA issuer (the whole warp, one lane issues)
         const bool leader = elect_one();
@@ -337,9 +344,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         int seg = 0;
         for (WeightItem it(p, x0, x1); it.x < x1; it.next(p, x1), ++seg) {
-            const int ks = seg & 1;
-            if (!mbar_wait_warp(smem_u32(&bars->k_full[ks]), (seg >> 1) & 1, p.wc)) break;
-            const uint8_t *src = smem + Cfg::kKOff + ks * kTile + r * 128;
+            const int ks = seg & 1, kb = seg % NK;
+            if (!mbar_wait_warp(smem_u32(&bars->k_full[kb]), (seg / NK) & 1, p.wc)) break;
+            const uint8_t *src = smem + Cfg::kKOff + kb * kTile + r * 128;
             uint32_t k[HD / 64][32];
 #pragma unroll
             for (int c = 0; c < kBoxes; ++c)
@@ -349,7 +356,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     k[c][4 * i] = w.x, k[c][4 * i + 1] = w.y, k[c][4 * i + 2] = w.z, k[c][4 * i + 3] = w.w;
                 }
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->k_empty[ks]));
+            if (lane == 0) mbar_arrive(smem_u32(&bars->k_empty[kb]));
             if (seg >= 2 && !mbar_wait_warp(smem_u32(&bars->kt_empty[ks]), ((seg >> 1) + 1) & 1, p.wc)) break;
             tc_fence_after();
 #pragma unroll
