@@ -839,7 +839,7 @@ def _evict(tensors, names, weight, keep, sinks, recent, N, layout, outs, index, 
 
 def _kept(keep, weight):
     _rank(weight, "weight", 3)
-    if keep < 1:
+    if not 1 <= keep <= weight.shape[2]:  # before anything of that size is made
         raise StripedError(-1, "striped_kv_evict")
     return weight.get_device()
 
@@ -863,8 +863,9 @@ def striped_kv_evict(k, v, weight, keep: int, sinks: int = 0, recent: int = 0, N
 def striped_kv4_evict(k_codes, k_scales, v_codes, v_scales, weight, keep: int, sinks: int = 0, recent: int = 0,
                       N: int = 1, layout: int = STRIPED, k_codes_out=None, k_scales_out=None, v_codes_out=None,
                       v_scales_out=None, index=None, weight_out=None, stream=None):
-    """striped_kv_evict of rows in 4 bits, as they are.  Returns (k_codes,
-    k_scales, v_codes, v_scales, index, weight) of the kept rows."""
+    """striped_kv_evict of rows in 4 bits, as they are (D a multiple of 64: the
+    scales of a row are whole words).  Returns (k_codes, k_scales, v_codes,
+    v_scales, index, weight) of the kept rows."""
     rows = (k_codes, k_scales, v_codes, v_scales)
     names = ("k_codes", "k_scales", "v_codes", "v_scales")
     for t, m in zip(rows, names):

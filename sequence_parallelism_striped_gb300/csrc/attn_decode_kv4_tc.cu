@@ -1,4 +1,4 @@
-// attn_decode_kv4_tc.cu -- decoding against a prompt in 4 bits when more than 16
+// attn_decode_kv4_tc.cu -- decoding against a prompt in 4 bits when more than 32
 // query rows share a prompt's key/value head (many requests on one prompt), on
 // tcgen05.
 //

@@ -314,7 +314,11 @@ bool decode_plan(DecPlan *plan, const DecodeArgs &a) {
     // 10.8 at 4, 11.0 at 6; 32 on one of 131072, tails of 8: 137, 98, 100; tails of
     // 1000: 110, 111, 114)
     p.over = a.D == 128 && !a.kv4 ? 2 : 4;
-    plan->small = a.kv4 && rows_p <= 16;
+    // Few rows on a 4-bit prompt go to attn_decode_kv4.cu, more to
+    // attn_decode_kv4_tc.cu.  16 prompts of 32768, 8 heads, D = 128 (64), us: 8 rows
+    // 125 against 278 (82, 230), 16 rows 160 against 285 (124, 233), 24 rows 228
+    // against 302 (156, 235), 32 rows 266 against 312 (179, 237)
+    plan->small = a.kv4 && rows_p <= 32;
     const int tail_tile = plan->small ? kTailTile : DT;
     const int64_t tiles =
         (ep * (a.P > 0 ? p.g.nt + p.over : 0) + a.B * nrt_t * ((a.C + tail_tile - 1) / tail_tile + p.over)) * a.Hkv;

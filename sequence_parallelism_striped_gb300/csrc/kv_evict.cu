@@ -11,8 +11,10 @@
 // ones; with the counts of the blocks before it every warp knows where its
 // positions go, so the list is in order and nothing depends on timing.
 //
-// Bound by latency: a pass over the numbers and a cluster barrier per digit.
-// The move is bound by memory: kept rows are read and written once.
+// Bound by latency: a pass over the numbers and a cluster barrier per digit.  The
+// move is bound by memory: kept rows are read and written once.  Measured, 8
+// heads, 16384 of 131072 rows of 128 channels: 46 us, selection 24 (clusters of
+// four blocks: 32, of sixteen: 63), move 22 (6.3 TB/s).
 #include <cooperative_groups.h>
 
 #include "common.cuh"

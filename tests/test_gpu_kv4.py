@@ -126,6 +126,14 @@ CASES += [
     (sp.CONTIGUOUS, 2, 2, 2, 1, 4, 2, 8, 128, 1, [0, 1]),      # tokens before position 0
     (sp.STRIPED, 2, 2, 17, 1, 1, 700, 260, 128, 7, [260, 31]),  # 17 rows
     (sp.STRIPED, 2, 2, 9, 1, 1, 700, 260, 64, 7, [129, 31]),   # 9 rows
+    (sp.STRIPED, 2, 2, 24, 1, 1, 700, 70, 64, 7, [70, 1]),
+    (sp.STRIPED, 2, 2, 5, 1, 5, 700, 70, 128, 7, [70, 3]),     # 25 rows, some inside the prompt
+    (sp.STRIPED, 2, 2, 32, 1, 1, 700, 300, 128, 7, [290, 31]),
+    (sp.STRIPED, 2, 2, 32, 1, 1, 700, 300, 64, 7, [290, 0]),
+    (sp.STRIPED, 8, 2, 8, 1, 1, 1400, 40, 64, 7, None),        # 32 rows of four requests
+    (sp.STRIPED, 2, 2, 33, 1, 1, 700, 300, 128, 7, [290, 31]),
+    (sp.ZIGZAG, 3, 3, 11, 1, 3, 1024, 50, 64, 4, [50, 2, 0]),  # 33 rows, some inside the prompt
+    (sp.STRIPED, 2, 1, 9, 1, 4, 1000, 50, 128, 4, [1, 3]),     # 72 rows, all inside the prompt
     (sp.STRIPED, 5, 1, 4, 4, 1, 1300, 150, 128, 13, [0, 1, 150, 128, 127]),
     (sp.STRIPED, 1, 1, 8, 8, 1, 5000, 9, 128, 8, [4]),         # a row a head
     (sp.STRIPED, 1, 1, 8, 2, 1, 70000, 9, 64, 8, [9]),
@@ -153,7 +161,7 @@ def test_decode(layout, B, Bp, H, Hkv, T, P, C, D, N, lens):
         within(go, o, tol, "o")
 
 
-@pytest.mark.parametrize("D,B,H", [(128, 2, 8), (64, 20, 32), (128, 1, 4), (64, 3, 12)])
+@pytest.mark.parametrize("D,B,H", [(128, 2, 8), (64, 20, 32), (128, 1, 4), (64, 3, 12), (128, 12, 8), (128, 40, 8)])
 def test_long_segments_with_a_growing_maximum(D, B, H):
     Hkv, P, C, N = 4, 40000, 200, 8
     q, kp, vp, kt, vt, lens = _make(B, 1, H, Hkv, 1, P, C, D, None, 7)
@@ -241,7 +249,7 @@ def test_lengths_outside_the_tail_are_clamped():
     assert torch.equal(a[0][0], a[1][0]) and torch.equal(a[0][1], a[1][1])
 
 
-@pytest.mark.parametrize("B,Bp,H,Hkv,T,P,C,D,N", [(40, 1, 8, 1, 1, 2048, 20, 64, 8), (3, 3, 20, 1, 1, 1000, 300, 128, 8)])
+@pytest.mark.parametrize("B,Bp,H,Hkv,T,P,C,D,N", [(40, 1, 8, 1, 1, 2048, 20, 64, 8), (3, 3, 40, 1, 1, 1000, 300, 128, 8)])
 def test_missing_tiles_end_and_leave_the_device_usable(B, Bp, H, Hkv, T, P, C, D, N):
     """Tiles of the tails are never loaded."""
     q, kp, vp, kt, vt, lens = _make(B, Bp, H, Hkv, T, P, C, D, [C] * B, 9)
@@ -280,7 +288,7 @@ def emptied_cache():
     torch.cuda.empty_cache()
 
 
-@pytest.mark.parametrize("H", [32, 1024])
+@pytest.mark.parametrize("H", [32, 2048])
 def test_offsets_past_32_bits(emptied_cache, H):
     """More than 2^31 bytes of codes and elements of tails: the last key/value head of the last request is what it is
     alone, and so are its stored rows."""
