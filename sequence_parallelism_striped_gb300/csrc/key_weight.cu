@@ -19,21 +19,21 @@
 // 65536: 71 us, 2.0 TB/s, 27 items of four half tiles a multiprocessor, whose
 // beginnings and ends are what it waits for.
 //
-// One CTA per multiprocessor, and all (key tile, head, query tile) triples of the
-// call are cut into shares of equal length, one per CTA.  A key tile whose
-// triples lie in several shares leaves partial sums, which a second kernel adds
-// in order: no atomics, the same result in every run.
+// One CTA per multiprocessor.  Two neighbouring key tiles are one item, which goes
+// over the query tiles together, a group of warps for each; all (item, head,
+// query tile) triples of the call are cut into shares of equal length, one per
+// CTA.  An item whose triples lie in several shares leaves partial sums, which a
+// second kernel adds in order: no atomics, the same result in every run.
 //
 //   warp 0       TMA producer: K tile of an item, Q tiles
 //   warp 1       TMEM allocator + tcgen05.mma issuer (one elected lane)
 //   warps 2, 3   log-sum-exp of the query tiles
-//   warps 4..11  two groups that take every other tile; thread t of a group owns
-//                key t
-//   warps 12..15 K tile from shared to tensor memory: as the left operand it is
+//   warps 4..11  two groups, one for each key tile; thread t of a group owns key t
+//   warps 12..15 K tiles from shared to tensor memory: as the left operand they are
 //                read there, and a product takes half the bytes from shared
 //                memory (both operands from there: 512 clocks a tile of its
 //                bandwidth, beside TMA's and the log-sum-exp's)
-// Tensor memory: three S^T of 128 columns, two K tiles.
+// Tensor memory: three S^T of 128 columns, taken in turn, two K tiles.
 #include <math.h>
 
 #include <type_traits>
@@ -50,20 +50,19 @@ constexpr int KT = 128;
 constexpr uint32_t kWBox = 128 * 128;  // 128 rows x 64 bf16
 constexpr int kWtThreads = 512;
 constexpr int kSBufs = 3;
-// Log-sum-exp buffers: an even number, so that a buffer's tiles are all of one
-// writing warp and one reading group.  (A wait tells a phase from the next one
-// only; whoever could be two phases ahead or behind must not wait there.)
+// Log-sum-exp buffers: an even number, so that each is filled by one of the two
+// warps alone.  (A wait tells a phase from the next one only; whoever could be
+// two phases ahead or behind must not wait there.)
 constexpr int kLBufs = 4;
 
 template <int HD>
 struct WeightCfg {
     static constexpr int NS = HD == 128 ? 3 : 6;  // Q stages
-    static constexpr int NK = HD == 128 ? 3 : 6;  // K tiles: read that many items ahead
+    static constexpr int NK = HD == 128 ? 3 : 6;  // K tiles
     static constexpr uint32_t kTile = (HD / 64) * kWBox;
     static constexpr uint32_t kKOff = NS * kTile;
     static constexpr uint32_t kLseOff = kKOff + NK * kTile;
-    static constexpr uint32_t kCombOff = kLseOff + kLBufs * KT * 4;
-    static constexpr uint32_t kBarOff = kCombOff + KT * 4;
+    static constexpr uint32_t kBarOff = kLseOff + kLBufs * KT * 4;
     static constexpr size_t kSmemBytes = 1024 + kBarOff + 512;
     static_assert(kSmemBytes <= 232448, "shared memory over the per-block limit");
 };
@@ -71,11 +70,11 @@ struct WeightCfg {
 template <int NS, int NK>
 struct WeightBars {
     uint64_t k_full[NK], k_empty[NK];  // in shared memory
-    uint64_t kt_full[2], kt_empty[2];  // in tensor memory
+    uint64_t kt_full, kt_empty;        // in tensor memory
     uint64_t q_full[NS], q_empty[NS];
     uint64_t s_full[kSBufs], s_empty[kSBufs];
     uint64_t lse_full[kLBufs], lse_empty[kLBufs];
-    uint64_t comb_full, comb_empty, drain;
+    uint64_t drain;
     uint32_t tmem_slot;
 };
 
@@ -89,62 +88,66 @@ struct WeightParams {
     int accumulate;
     const float *lse;
     float *weight;
-    float *part;          // [parts][2][KT]: of a CTA's first and last item
+    float *part;          // [parts][2][2 KT]: of a CTA's first and last item
     WaitCtl wc;
 };
 
-// Triples of a key/value head before its key tile kt, over the group's heads.
-__host__ __device__ __forceinline__ int64_t weight_before(const PosGeom &g, int f0, int G, int64_t kt) {
-    const int64_t nt = g.nt, f = f0;
-    if (kt <= f) return G * kt * (nt - f);
-    return G * (f * (nt - f) + (kt - f) * nt - (kt * (kt - 1) - f * (f - 1)) / 2);
+// Triples of a key/value head before its item kp (key tiles 2 kp and 2 kp + 1), over
+// the group's heads; the queries of an item begin at the tile of its first key,
+// or at f0.
+__host__ __device__ __forceinline__ int64_t weight_before(const PosGeom &g, int f0, int G, int64_t kp) {
+    const int64_t nt = g.nt, f = f0, kf = f / 2 + 1;  // items that begin at f0
+    if (kp <= kf) return G * kp * (nt - f);
+    return G * (kf * (nt - f) + (kp - kf) * nt - (kp * (kp - 1) - kf * (kf - 1)));
 }
+__host__ __device__ __forceinline__ int weight_items(const PosGeom &g) { return (g.nt + 1) / 2; }
 
 __host__ __device__ __forceinline__ int64_t weight_share(const WeightParams &p, int c) {
     return p.total / p.parts * c + p.total % p.parts * c / p.parts;
 }
 
-// The stretch [n0, n1) of the triples of one key tile that begins at x; next()
-// goes on to the one behind it.
+// The stretch [n0, n1) of the triples of one item that begins at x; next() goes
+// on to the one behind it.
 struct WeightItem {
     int64_t x;
-    int line, kt;       // key/value head of the batch, key tile
+    int line, kp;       // key/value head of the batch, item
     int qlo, cnt, all;  // first query tile, query tiles, triples
     int n0, n1;
     __device__ __forceinline__ WeightItem(const WeightParams &p, int64_t from, int64_t x1) {
         x = from;
-        const int64_t per = weight_before(p.g, p.f0, p.G, p.g.nt);
+        const int64_t per = weight_before(p.g, p.f0, p.G, weight_items(p.g));
         line = (int)(x / per);
         const int64_t in = x - line * per;
-        int a = 0, b = p.g.nt - 1;
+        int a = 0, b = weight_items(p.g) - 1;
         while (a < b) {
             const int m = (int)(((int64_t)a + b + 1) >> 1);
             if (weight_before(p.g, p.f0, p.G, m) <= in) a = m;
             else b = m - 1;
         }
-        kt = a;
-        n0 = (int)(in - weight_before(p.g, p.f0, p.G, kt));
+        kp = a;
+        n0 = (int)(in - weight_before(p.g, p.f0, p.G, kp));
         sizes(p, x1);
     }
     __device__ __forceinline__ void next(const WeightParams &p, int64_t x1) {
         x += n1 - n0;
         n0 = 0;
-        if (++kt == p.g.nt) kt = 0, ++line;
+        if (++kp == weight_items(p.g)) kp = 0, ++line;
         sizes(p, x1);
     }
+    __device__ __forceinline__ bool has(const WeightParams &p, int h) const { return 2 * kp + h < p.g.nt; }
 
   private:
     __device__ __forceinline__ void sizes(const WeightParams &p, int64_t x1) {
-        qlo = max(kt, p.f0);
+        qlo = max(2 * kp, p.f0);
         cnt = p.g.nt - qlo;
         all = p.G * cnt;
         n1 = (int)min((int64_t)all, n0 + (x1 - x));
     }
 };
 
-__device__ __forceinline__ void write_weight(const WeightParams &p, const WeightItem &it, int r, float sum) {
-    if (!tile_has(p.g, it.kt, r)) return;
-    float *dst = p.weight + (int64_t)it.line * p.g.S + tile_row(p.g, it.kt, r);
+__device__ __forceinline__ void write_weight(const WeightParams &p, int line, int kt, int r, float sum) {
+    if (kt >= p.g.nt || !tile_has(p.g, kt, r)) return;
+    float *dst = p.weight + (int64_t)line * p.g.S + tile_row(p.g, kt, r);
     *dst = p.accumulate ? *dst + sum : sum;
 }
 
@@ -160,7 +163,6 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     WeightBars<NS, NK> *bars = reinterpret_cast<WeightBars<NS, NK> *>(smem + Cfg::kBarOff);
     float *lse_s = reinterpret_cast<float *>(smem + Cfg::kLseOff);
-    float *comb = reinterpret_cast<float *>(smem + Cfg::kCombOff);
     const uint32_t sbase = smem_u32(smem);
     const PosGeom &g = p.g;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -170,10 +172,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             mbar_init(smem_u32(&bars->k_full[i]), 1);
             mbar_init(smem_u32(&bars->k_empty[i]), 4);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&bars->kt_full[i]), 4);
-            mbar_init(smem_u32(&bars->kt_empty[i]), 1);
-        }
+        mbar_init(smem_u32(&bars->kt_full), 4);
+        mbar_init(smem_u32(&bars->kt_empty), 1);
         for (int s = 0; s < NS; ++s) {
             mbar_init(smem_u32(&bars->q_full[s]), 1);
             mbar_init(smem_u32(&bars->q_empty[s]), 1);
@@ -184,10 +184,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         }
         for (int i = 0; i < kLBufs; ++i) {
             mbar_init(smem_u32(&bars->lse_full[i]), 1);
-            mbar_init(smem_u32(&bars->lse_empty[i]), 4);
+            mbar_init(smem_u32(&bars->lse_empty[i]), 8);
         }
-        mbar_init(smem_u32(&bars->comb_full), 4);
-        mbar_init(smem_u32(&bars->comb_empty), 4);
         mbar_init(smem_u32(&bars->drain), 1);
         fence_barrier_init();
     }
@@ -214,22 +212,33 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         // ---------------- TMA producer
         const bool skip_first = p.wc.inject == kInjectFwdSkipKV;  // test hook: the first K tile is never loaded
         const uint32_t bytes = (uint32_t)g.P * 128 * kBoxes;
-        int j = 0, seg = 0, kseg = 0;  // tiles, items whose queries and whose keys were asked for
+        int j = 0, kn = 0, kdone = 0;  // query tiles; K tiles asked for, and those of the items begun
         bool ok = true;
         WeightItem kit(p, x0, x1);
-        for (WeightItem it(p, x0, x1); it.x < x1 && ok; it.next(p, x1), ++seg) {
-            for (; kit.x < x1 && kseg < seg + NK; kit.next(p, x1), ++kseg) {
-                const int ks = kseg % NK;
-                if (kseg >= NK && !mbar_wait(smem_u32(&bars->k_empty[ks]), ((kseg / NK) + 1) & 1, p.wc)) {
-                    ok = false;
-                    break;
+        int kh = 0;
+        for (WeightItem it(p, x0, x1); it.x < x1 && ok; it.next(p, x1)) {
+            // this item's K tiles, and of the next ones as many as there is room for
+            kdone += it.has(p, 1) ? 2 : 1;
+            while (kit.x < x1) {
+                const int ks = kn % NK;
+                if (kn >= NK) {
+                    const uint32_t bar = smem_u32(&bars->k_empty[ks]), phase = ((kn / NK) + 1) & 1;
+                    if (kn < kdone ? !mbar_wait(bar, phase, p.wc) : !mbar_try_wait(bar, phase)) {
+                        ok = kn >= kdone;
+                        break;
+                    }
                 }
-                if (skip_first && kseg == 0) continue;
-                const TileAt at = tile_at(g, kit.kt);
-                const uint32_t fb = smem_u32(&bars->k_full[ks]), dst = sbase + Cfg::kKOff + ks * kTile;
-                mbar_arrive_expect_tx(fb, bytes);
+                if (!(skip_first && kn == 0)) {
+                    const TileAt at = tile_at(g, 2 * kit.kp + kh);
+                    const uint32_t fb = smem_u32(&bars->k_full[ks]), dst = sbase + Cfg::kKOff + ks * kTile;
+                    mbar_arrive_expect_tx(fb, bytes);
 #pragma unroll
-                for (int c = 0; c < kBoxes; ++c) tma_load_4d(dst + c * kWBox, &tmK, fb, 64 * c, at.c1, at.c2, kit.line);
+                    for (int c = 0; c < kBoxes; ++c)
+                        tma_load_4d(dst + c * kWBox, &tmK, fb, 64 * c, at.c1, at.c2, kit.line);
+                }
+                ++kn;
+                if (kh == 0 && kit.has(p, 1)) kh = 1;
+                else kh = 0, kit.next(p, x1);
             }
             if (!ok) break;
             const int b = it.line / p.Hkv, hkv = it.line - b * p.Hkv;
@@ -250,7 +259,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         }
         // the last load of each stage has landed before the CTA exits
         for (int t = j > NS ? j - NS : 0; t < j; ++t) mbar_wait(smem_u32(&bars->q_full[t % NS]), (t / NS) & 1, p.wc);
-        for (int t = kseg > NK ? kseg - NK : 0; t < kseg; ++t)
+        for (int t = kn > NK ? kn - NK : 0; t < kn; ++t)
             if (!(skip_first && t == 0)) mbar_wait(smem_u32(&bars->k_full[t % NK]), (t / NK) & 1, p.wc);
     } else if (warp == 1) {
         // ---------------- MMA issuer (the whole warp, one lane issues)
@@ -260,29 +269,33 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         int j = 0, seg = 0;
         bool ok = true;
         for (WeightItem it(p, x0, x1); it.x < x1 && ok; it.next(p, x1), ++seg) {
-            ok = mbar_wait_warp(smem_u32(&bars->kt_full[seg & 1]), (seg >> 1) & 1, p.wc);
-            const uint32_t ta = tm + kKCol + (seg & 1) * (HD / 2);
+            ok = mbar_wait_warp(smem_u32(&bars->kt_full), seg & 1, p.wc);
             int qt = it.qlo + it.n0 % it.cnt;
             for (int n = it.n0; n < it.n1 && ok; ++n, ++j) {
-                const int s = j % NS, u = j % kSBufs;
+                const int s = j % NS, at = qt;
                 ok = mbar_wait_warp(smem_u32(&bars->q_full[s]), (j / NS) & 1, p.wc);
-                if (ok && j >= kSBufs) ok = mbar_wait_warp(smem_u32(&bars->s_empty[u]), ((j / kSBufs) + 1) & 1, p.wc);
-                if (!ok) break;
-                tc_fence_after();
                 // queries before `first` in its tile are left out, 32 at a time
-                const int skip = qt == p.f0 ? (p.first - qt * g.P) / 32 : 0;
+                const int skip = at == p.f0 ? (p.first - at * g.P) / 32 : 0;
                 if (++qt == g.nt) qt = it.qlo;
                 const uint32_t idesc = idesc_bf16_f32(KT, KT, false, false) - ((uint32_t)(skip * 32 / 8) << 17);
-                if (leader) {
-                    const uint64_t db = dq + s * (kTile >> 4) + (skip * 32 * 128 >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < HD / 16; ++kk)
-                        mma_ts(tm + 128 * u + 32 * skip, ta + kk * 8, db + (((kk >> 2) * kWBox + (kk & 3) * 32) >> 4),
-                               idesc, kk > 0 ? 1u : 0u);
-                    // only what will be refilled is released
-                    if (j + NS < nx) mma_commit(smem_u32(&bars->q_empty[s]));
-                    mma_commit(smem_u32(&bars->s_full[u]));
-                    if (n + 1 == it.n1 && it.x + (it.n1 - it.n0) < x1) mma_commit(smem_u32(&bars->kt_empty[seg & 1]));
+                for (int h = 0; h < 2; ++h) {
+                    const int i = 2 * j + h, u = i % kSBufs;
+                    if (ok && i >= kSBufs) ok = mbar_wait_warp(smem_u32(&bars->s_empty[u]), ((i / kSBufs) + 1) & 1, p.wc);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (leader) {
+                        const uint64_t db = dq + s * (kTile >> 4) + (skip * 32 * 128 >> 4);
+                        if (it.has(p, h) && at >= 2 * it.kp + h)  // else no key of the tile is kept
+#pragma unroll
+                            for (int kk = 0; kk < HD / 16; ++kk)
+                                mma_ts(tm + 128 * u + 32 * skip, tm + kKCol + h * (HD / 2) + kk * 8,
+                                       db + (((kk >> 2) * kWBox + (kk & 3) * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
+                        // only what will be refilled is released
+                        if (h && j + NS < nx) mma_commit(smem_u32(&bars->q_empty[s]));
+                        mma_commit(smem_u32(&bars->s_full[u]));
+                        if (h && n + 1 == it.n1 && it.x + (it.n1 - it.n0) < x1) mma_commit(smem_u32(&bars->kt_empty));
+                    }
                 }
             }
         }
@@ -350,29 +363,38 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         // ---------------- K tiles: shared -> tensor memory
         const int r = (warp & 3) * 32 + lane;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-        int seg = 0;
-        for (WeightItem it(p, x0, x1); it.x < x1; it.next(p, x1), ++seg) {
-            const int ks = seg & 1, kb = seg % NK;
-            if (!mbar_wait_warp(smem_u32(&bars->k_full[kb]), (seg / NK) & 1, p.wc)) break;
-            const uint8_t *src = smem + Cfg::kKOff + kb * kTile + r * 128;
-            uint32_t k[HD / 64][32];
+        int seg = 0, kn = 0;
+        bool ok = true;
+        for (WeightItem it(p, x0, x1); it.x < x1 && ok; it.next(p, x1), ++seg) {
+#pragma unroll 1
+            for (int h = 0; h < (it.has(p, 1) ? 2 : 1); ++h, ++kn) {
+                const int kb = kn % NK;
+                ok = mbar_wait_warp(smem_u32(&bars->k_full[kb]), (kn / NK) & 1, p.wc);
+                if (!ok) break;
+                const uint8_t *src = smem + Cfg::kKOff + kb * kTile + r * 128;
+                uint32_t k[HD / 64][32];
 #pragma unroll
-            for (int c = 0; c < kBoxes; ++c)
+                for (int c = 0; c < kBoxes; ++c)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(src + c * kWBox + ((i ^ (r & 7)) * 16));
-                    k[c][4 * i] = w.x, k[c][4 * i + 1] = w.y, k[c][4 * i + 2] = w.z, k[c][4 * i + 3] = w.w;
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 w = *reinterpret_cast<const uint4 *>(src + c * kWBox + ((i ^ (r & 7)) * 16));
+                        k[c][4 * i] = w.x, k[c][4 * i + 1] = w.y, k[c][4 * i + 2] = w.z, k[c][4 * i + 3] = w.w;
+                    }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->k_empty[kb]));
+                if (h == 0 && seg > 0) {  // the last item's products have read theirs
+                    ok = mbar_wait_warp(smem_u32(&bars->kt_empty), (seg + 1) & 1, p.wc);
+                    if (!ok) break;
                 }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->k_empty[kb]));
-            if (seg >= 2 && !mbar_wait_warp(smem_u32(&bars->kt_empty[ks]), ((seg >> 1) + 1) & 1, p.wc)) break;
-            tc_fence_after();
+                tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < kBoxes; ++c) tmem_st32(tmem + kKCol + ks * (HD / 2) + 32 * c + lane_off, k[c]);
+                for (int c = 0; c < kBoxes; ++c) tmem_st32(tmem + kKCol + h * (HD / 2) + 32 * c + lane_off, k[c]);
+            }
+            if (!ok) break;
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->kt_full[ks]));
+            if (lane == 0) mbar_arrive(smem_u32(&bars->kt_full));
         }
     } else if (warp >= 4) {
         // ---------------- weights of the keys
@@ -381,19 +403,17 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
         const float cl2 = p.scale * 1.4426950408889634f;
         const uint64_t cl2x2 = f2(cl2, cl2);
-        int seg = 0;
         bool ok = true;
-        // the group's tiles are j = group, group + 2, ..: their buffer and its phase
-        int j = group, u = group, phase = 0;
-        int j0 = 0;  // first tile of the item
-        for (WeightItem it(p, x0, x1); it.x < x1 && ok; j0 += it.n1 - it.n0, it.next(p, x1), ++seg) {
+        // the group's products are every second one: their buffer and its phase
+        int j = 0, u = group, phase = 0;
+        for (WeightItem it(p, x0, x1); it.x < x1 && ok; it.next(p, x1)) {
             float sum = 0.f;
-            const int j1 = j0 + it.n1 - it.n0;
-            int qt = it.qlo + (it.n0 + j - j0) % it.cnt;
-            for (; j < j1; j += 2) {
+            const int kt = 2 * it.kp + group;
+            const bool has = kt < g.nt;
+            int qt = it.qlo + it.n0 % it.cnt;
+            for (int n = it.n0; n < it.n1; ++n, ++j) {
                 const int at = qt;
-                qt += 2;
-                while (qt >= g.nt) qt -= it.cnt;
+                if (++qt == g.nt) qt = it.qlo;
                 const int lb = j % kLBufs;
                 const uint32_t lse_bar = smem_u32(&bars->lse_full[lb]), s_bar = smem_u32(&bars->s_full[u]);
                 const bool l_ok = mbar_try_wait(lse_bar, (j / kLBufs) & 1), s_ok = mbar_try_wait(s_bar, phase);
@@ -440,15 +460,15 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                         acc[(2 * i + 1) & 3] = add2(acc[(2 * i + 1) & 3], f2(e[2], e[3]));
                     }
                 };
-                if (at != it.kt && at != p.f0 && at + 1 != g.nt) {
+                if (has && at > kt && at != p.f0 && at + 1 != g.nt) {
 #pragma unroll
                     for (int c = 0; c < KT / 32; ++c) add(c, std::false_type{}, c == KT / 32 - 1);
                 } else {
                     // columns that count for some key of this warp: queries from
                     // `first` and, in the keys' own tile, from the warp's first key
-                    const bool diag = at == it.kt;
+                    const bool diag = at == kt;
                     int c = max(max(0, p.first - at * g.P) / 32, diag ? quarter : 0);
-                    const int c1 = (min(g.P, g.S - at * g.P) + 31) / 32;
+                    const int c1 = has && at >= kt ? (min(g.P, g.S - at * g.P) + 31) / 32 : 0;
                     if (diag && c == quarter && c < c1) add(c++, std::true_type{}, false);
 #pragma unroll 1
                     for (; c < c1; ++c) add(c, std::false_type{}, false);
@@ -465,20 +485,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 sum += t.x + t.y;
             }
             if (!ok) break;
-            // the second group's sums go to the first one
-            if (group == 1) {
-                if (seg > 0 && !mbar_wait_warp(smem_u32(&bars->comb_empty), (seg + 1) & 1, p.wc)) break;
-                comb[r] = sum;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars->comb_full));
-            } else {
-                if (!mbar_wait_warp(smem_u32(&bars->comb_full), seg & 1, p.wc)) break;
-                sum += comb[r];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars->comb_empty));
-                if (it.n0 == 0 && it.n1 == it.all) write_weight(p, it, r, sum);
-                else p.part[((int64_t)blockIdx.x * 2 + (it.n0 == 0)) * KT + r] = sum;
-            }
+            if (it.n0 == 0 && it.n1 == it.all) write_weight(p, it.line, kt, r, sum);
+            else p.part[(((int64_t)blockIdx.x * 2 + (it.n0 == 0)) * 2 + group) * KT + r] = sum;
         }
     }
     tc_fence_before();
@@ -490,9 +498,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     }
 }
 
-// A key tile that lies in several shares: block c - 1 adds its sums, if the
-// boundary between the shares of CTAs c - 1 and c is the first one inside it.
-__global__ void __launch_bounds__(KT) key_weight_join_kernel(const WeightParams p) {
+// An item that lies in several shares: block c - 1 adds its sums, if the boundary
+// between the shares of CTAs c - 1 and c is the first one inside it.
+__global__ void __launch_bounds__(2 * KT) key_weight_join_kernel(const WeightParams p) {
     wait_for_previous();
     const int c = blockIdx.x + 1;
     const int64_t x = weight_share(p, c);
@@ -500,9 +508,9 @@ __global__ void __launch_bounds__(KT) key_weight_join_kernel(const WeightParams 
     const int64_t begin = x - it.n0, end = begin + it.all;
     if (it.n0 == 0 || weight_share(p, c - 1) > begin) return;
     const int r = threadIdx.x;
-    float sum = p.part[((int64_t)(c - 1) * 2 + 1) * KT + r];
-    for (int d = c; d < p.parts && weight_share(p, d) < end; ++d) sum += p.part[(int64_t)d * 2 * KT + r];
-    write_weight(p, it, r, sum);
+    float sum = p.part[((int64_t)(c - 1) * 2 + 1) * 2 * KT + r];
+    for (int d = c; d < p.parts && weight_share(p, d) < end; ++d) sum += p.part[(int64_t)d * 4 * KT + r];
+    write_weight(p, it.line, 2 * it.kp + r / KT, r % KT, sum);
 }
 
 bool weight_plan(WeightParams *p, const KeyWeightArgs &a) {
@@ -520,7 +528,7 @@ bool weight_plan(WeightParams *p, const KeyWeightArgs &a) {
     // a head's triples and a CTA's share are counted in 32 bits
     const double all = (double)lines * p->G * p->g.nt * (p->g.nt - p->f0);
     if (all > (double)(1ll << 30) * sms || (double)p->G * p->g.nt > (double)(1ll << 30)) return false;
-    p->total = lines * weight_before(p->g, p->f0, p->G, p->g.nt);
+    p->total = lines * weight_before(p->g, p->f0, p->G, weight_items(p->g));
     p->parts = (int)(p->total < sms ? p->total : sms);
     return true;
 }
@@ -546,14 +554,14 @@ int launch_hd(const void *q, const void *k, const float *lse, float *weight, voi
     tc_key_weight_kernel<HD><<<p.parts, kWtThreads, WeightCfg<HD>::kSmemBytes, stream>>>(mq, mk, p);
     if ((st = cuda_status(cudaGetLastError()))) return st;
     if (p.parts < 2) return STRIPED_OK;
-    return launch_after(key_weight_join_kernel, dim3((unsigned)(p.parts - 1)), KT, 0, stream, p);
+    return launch_after(key_weight_join_kernel, dim3((unsigned)(p.parts - 1)), 2 * KT, 0, stream, p);
 }
 
 }  // namespace
 
 size_t key_weight_workspace(const KeyWeightArgs &a) {
     WeightParams p;
-    return weight_plan(&p, a) ? (size_t)p.parts * 2 * KT * 4 : 0;
+    return weight_plan(&p, a) ? (size_t)p.parts * 4 * KT * 4 : 0;
 }
 
 int launch_tc_key_weight(const void *q, const void *k, const float *lse, float *weight, void *workspace,
