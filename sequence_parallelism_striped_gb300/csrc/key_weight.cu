@@ -11,13 +11,13 @@
 //
 // The bytes are few; per tile of 128 x 128 at D = 128 the products take 512 clocks,
 // the exponentials 512 (8 a clock and quarter).  Measured, 32 + 8 heads, all
-// queries: S = 16384 872 us, 1,261 TFLOP/s of kept products (66 % of the
-// tensor core's burst), 960 clocks a tile: a warp sums 32 columns in about 260
-// clocks, half of them its exponentials, and two warps a quarter do not
-// hide the hand-offs (a third group: 990 us, four for 32 columns each: 1,080;
-// without exponentials 785, without products 870).  The last 64 queries of S =
-// 65536: 71 us, 2.0 TB/s, 27 items of four half tiles a multiprocessor, whose
-// beginnings and ends are what it waits for.
+// queries of S = 16384: 860 us, 1,279 TFLOP/s of kept products (67 % of the
+// tensor core's burst), 950 clocks a tile: a warp sums 32 columns in about 260
+// clocks, half of them its exponentials, and two warps a quarter do not hide the
+// hand-offs (a third group: 990 us, four for 32 columns each: 1,080; without
+// exponentials 785, without products 870).  The last 64 queries of S = 65536: 65
+// us, 2.1 TB/s: 14 items of four half tiles a multiprocessor, for which all
+// multiprocessors read the same few query tiles.
 //
 // One CTA per multiprocessor.  Two neighbouring key tiles are one item, which goes
 // over the query tiles together, a group of warps for each; all (item, head,
