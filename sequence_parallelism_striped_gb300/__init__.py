@@ -133,7 +133,29 @@ def load(build_if_missing: bool = True):
         lib.striped_selftest_timeout.argtypes = [I64, P]
         lib.striped_test_inject.argtypes = [I, I64]
         _lib = lib
+        _bind(path)
         return lib
+
+
+_fast = None  # csrc/binding.cpp, once the library is loaded
+
+
+def _bind(path: str):
+    """Calls that the binding takes in one step: plain ones, without buffers or a stream of the caller's.  It gives None
+    for whatever it does not take, and the wrapper goes on; so it does if the binding could not be built."""
+    global _fast
+    if not os.path.exists(_build.BINDING):
+        return
+    from importlib import machinery, util
+
+    loader = machinery.ExtensionFileLoader("striped_binding", _build.BINDING)
+    try:
+        module = util.module_from_spec(util.spec_from_loader("striped_binding", loader))
+        loader.exec_module(module)
+    except (ImportError, OSError):  # of another torch
+        return
+    if module.use(path):
+        _fast = module
 
 
 def _check(status: int, where: str):
@@ -682,6 +704,10 @@ def striped_kv4_store(k, v, k_codes=None, k_scales=None, v_codes=None, v_scales=
     """Keys and values [B,Hkv,S,D] bf16 in 4 bits, rows in their places:
     returns (k_codes uint8 [B,Hkv,S,D/2], k_scales bf16 [B,Hkv,S,D/32],
     v_codes, v_scales)."""
+    if _fast is not None and stream is None and k_codes is k_scales is v_codes is v_scales is None:
+        r = _fast.kv4_store(k, v)
+        if r is not None:
+            return r
     _rank(k, "k", 4)
     dev = k.get_device()
     if not _here(dev, stream):
@@ -703,6 +729,10 @@ def striped_kv4_store(k, v, k_codes=None, k_scales=None, v_codes=None, v_scales=
 def striped_kv4_load(k_codes, k_scales, v_codes, v_scales, k=None, v=None, stream=None):
     """The values that striped_kv4_store's codes and scales stand for (bf16
     numbers, without a further rounding): returns (k, v) [B,Hkv,S,D]."""
+    if _fast is not None and stream is None and k is v is None:
+        r = _fast.kv4_load(k_codes, k_scales, v_codes, v_scales)
+        if r is not None:
+            return r
     _rank(k_codes, "k_codes", 4)
     dev = k_codes.get_device()
     if not _here(dev, stream):
@@ -745,6 +775,10 @@ def striped_attn_decode_kv4(q, k_codes, k_scales, v_codes, v_scales, k_tail, v_t
     [Bp,Hkv,P,D/32] of striped_kv4_store in `layout` rows; q [B,H,T,D], tails
     [B,Hkv,C,D] bf16, tail_lens int32 [B].  Returns (o [B,H,T,D], lse
     [B,H,T])."""
+    if _fast is not None and stream is None and workspace is out is lse_out is None:
+        r = _fast.decode_kv4(q, k_codes, k_scales, v_codes, v_scales, k_tail, v_tail, tail_lens, N, layout, scale)
+        if r is not None:
+            return r
     _rank(k_codes, "k_codes", 4)
     n = B, Bp, H, Hkv, T, P, C, D = _decode_sizes(q, k_codes, k_tail)
     dev = q.get_device()
@@ -791,6 +825,10 @@ def striped_attn_key_weight(q, k, lse, N: int, layout: int = STRIPED, first: int
     >= first, over the query heads that share it: q [B,H,S,D], k [B,Hkv,S,D]
     bf16 and the forward's lse [B,H,S] in `layout` order.  Returns weight fp32
     [B,Hkv,S]; accumulate adds to the given one."""
+    if _fast is not None and stream is None and workspace is weight is None and not accumulate:
+        r = _fast.key_weight(q, k, lse, N, layout, first, scale)
+        if r is not None:
+            return r
     _rank(q, "q", 4)
     _rank(k, "k", 4)
     if accumulate and weight is None:
@@ -851,6 +889,10 @@ def striped_kv_evict(k, v, weight, keep: int, sinks: int = 0, recent: int = 0, N
     [B,Hkv,S], `keep` in all, in the order of their positions (a contiguous
     prompt: N = 1).  Returns (k_out, v_out [B,Hkv,keep,D], index int32
     [B,Hkv,keep], the kept positions, weight_out fp32 [B,Hkv,keep])."""
+    if _fast is not None and stream is None and k_out is v_out is index is weight_out is None:
+        r = _fast.kv_evict(weight, keep, sinks, recent, N, layout, k, v)
+        if r is not None:
+            return r
     _rank(k, "k", 4)
     _rank(v, "v", 4)
     dev = _kept(keep, weight)
@@ -866,6 +908,11 @@ def striped_kv4_evict(k_codes, k_scales, v_codes, v_scales, weight, keep: int, s
     """striped_kv_evict of rows in 4 bits, as they are (D a multiple of 64: the
     scales of a row are whole words).  Returns (k_codes, k_scales, v_codes,
     v_scales, index, weight) of the kept rows."""
+    if (_fast is not None and stream is None and k_codes_out is k_scales_out is v_codes_out is v_scales_out is None
+            and index is weight_out is None):
+        r = _fast.kv_evict(weight, keep, sinks, recent, N, layout, k_codes, k_scales, v_codes, v_scales)
+        if r is not None:
+            return r
     rows = (k_codes, k_scales, v_codes, v_scales)
     names = ("k_codes", "k_scales", "v_codes", "v_scales")
     for t, m in zip(rows, names):

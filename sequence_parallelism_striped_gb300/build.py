@@ -10,6 +10,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libstriped.so")
+BINDING = os.path.join(BUILD, "striped_binding.so")  # csrc/binding.cpp: some calls from Python in one step
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "permute.cu", "attn_simt.cu", "attn_fwd_tc.cu", "attn_fwd_pair.cu", "attn_bwd_tc.cu", "attn_bwd_noalloc.cu",
            "norm_rope.cu", "attn_window_fwd.cu", "attn_window_bwd.cu", "attn_decode.cu", "attn_decode_kv4.cu",
@@ -41,6 +43,34 @@ def _newest_input() -> float:
     return max(os.path.getmtime(p) for p in paths)
 
 
+def _build_binding():
+    """The Python calls of csrc/binding.cpp, against the headers of the torch that is installed.  Returns what went
+    wrong, or None: without it the wrappers do the same work, slower."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", os.path.join(root, "include"),
+           "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", os.path.join(root, "lib"), "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ldl"]
+    try:
+        res = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        return str(e)
+    if res.returncode != 0:
+        if os.path.exists(BINDING):
+            os.remove(BINDING)
+        return res.stderr
+    os.replace(tmp, BINDING)
+    return None
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile every source and link libstriped.so; returns its path."""
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_input():
@@ -62,8 +92,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             print(res.stdout + res.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_build_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        wrong = binding.result()
+    if wrong:
+        print(f"binding.cpp not built, calls go through ctypes alone: {wrong[-2000:]}", file=sys.stderr)
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, "-shared", *ARCH, "-o", tmp, *objs, "-lcuda"]
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -74,6 +108,4 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
 
 
 if __name__ == "__main__":
-    import sys
-
     print(build(force=True, verbose=True, ptxas_info="-v" in sys.argv))
