@@ -432,7 +432,8 @@ int striped_kv4_load(const void *k_codes, const void *k_scales, const void *v_co
  * the stored values.  Every query keeps all positions at or before it: there
  * is no window.  Limits, lengths, order of sums, workspace and overlaps as for
  * striped_attn_decode; with
- * g = H/Hkv * T rows a request, ceil(B/Bp * g / 128) row tiles a prompt.
+ * g = H/Hkv * T rows a request, ceil(B/Bp * g / 128) row tiles a prompt; with
+ * a scale above 3.6e36, |q| < 2^122.
  */
 int striped_attn_decode_kv4(const void *q, const void *k_codes, const void *k_scales, const void *v_codes,
                             const void *v_scales, const void *k_tail, const void *v_tail, const int32_t *tail_lens,

@@ -159,7 +159,6 @@ __global__ void __launch_bounds__(kQThreads, NT == 1 ? 2 : 1)
     float *stat = reinterpret_cast<float *>(smem + Cfg::kStatOff);
     __shared__ int scan[kQWarps];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-    const float cl2 = p.scale * 1.4426950408889634f;
 
     entry_costs<kTailTile, kQThreads>(p, cum, scan);
     let_next_begin();
@@ -177,6 +176,8 @@ __global__ void __launch_bounds__(kQThreads, NT == 1 ? 2 : 1)
         const int grp = tail ? sg.e - p.ep : sg.e;
         const int rows = tail ? p.rows_t : p.rows_p, per = p.G * p.T;
         const int end = tail ? len_of(p, grp) : p.P;  // keys of the item
+        const bool by_scale = p.scale <= kKv4MostScale;  // what undoes the keys' 2^-6
+        const float cl2 = p.scale * 1.4426950408889634f * (!tail && by_scale ? kKv4Unit : 1.f);
 
         // ---------------- query rows
         __syncthreads();  // shared memory of the segment before is free
@@ -187,6 +188,9 @@ __global__ void __launch_bounds__(kQThreads, NT == 1 ? 2 : 1)
                 const int j = r / per, in = r - j * per;
                 const int b = tail ? grp : grp * p.R + j, h = sg.hkv * p.G + in / p.T;
                 w = __ldg(reinterpret_cast<const uint4 *>(p.q + (((int64_t)b * p.H + h) * p.T + in % p.T) * HD) + c);
+                if (!tail && !by_scale)
+                    w = make_uint4(bf16x2_mul(w.x, kKv4Query), bf16x2_mul(w.y, kKv4Query), bf16x2_mul(w.z, kKv4Query),
+                                   bf16x2_mul(w.w, kKv4Query));
             }
             *reinterpret_cast<uint4 *>(smem + Cfg::kQOff + r * Cfg::kQRow + c * 16) = w;
         }
@@ -311,7 +315,7 @@ __global__ void __launch_bounds__(kQThreads, NT == 1 ? 2 : 1)
                 }
                 if (inside || key0 + kStep - 1 > hi_min) masked(s, key0);
                 uint32_t pt[2][NT][2];
-                st.template softmax<2>(s, pt, cl2 * kKv4Unit);
+                st.template softmax<2>(s, pt, cl2);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     // this thread's keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of the 16

@@ -308,7 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (sg.t1 <= sg.t0) continue;
             const bool tail = sg.e >= p.ep;
             const float unit = tail ? 1.f : kKv4Unit;  // of the values in the tiles
-            const float cl2 = p.scale * 1.4426950408889634f * unit;
+            const bool by_scale = p.scale <= kKv4MostScale;  // what undoes the keys' 2^-6
+            const float cl2 = p.scale * 1.4426950408889634f * (by_scale ? unit : 1.f);
             // this thread's query row: request b, head hq, token t
             int grp, rt, rows;
             if (tail) {
@@ -345,6 +346,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const uint4 w = row_on ? __ldg(src + 8 * c + v) : make_uint4(0u, 0u, 0u, 0u);
                             qa[4 * v] = w.x, qa[4 * v + 1] = w.y, qa[4 * v + 2] = w.z, qa[4 * v + 3] = w.w;
                         }
+                        if (!tail && !by_scale)
+#pragma unroll
+                            for (int v = 0; v < 32; ++v) qa[v] = bf16x2_mul(qa[v], kKv4Query);
                         tmem_st32(tmem + kQCol + lane_off + 32 * c, qa);
                     }
                     tmem_st_wait();

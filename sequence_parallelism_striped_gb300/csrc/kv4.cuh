@@ -51,6 +51,11 @@ __device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t 
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
+// Scores of keys made so are 2^-6 of themselves.  The scale of the softmax undoes
+// that, up to where 64 of it times log2(e) is still a number; beyond it (1e38 is
+// allowed) the queries do, 64 of them, which is exact below 2^122.
+constexpr float kKv4MostScale = 3.6e36f;
+constexpr uint32_t kKv4Query = 0x42804280u;  // 64, 64
 __device__ __forceinline__ void kv4_pairs(uint32_t w, uint32_t (&c)[4]) {
     constexpr uint32_t k2e127 = 0x7f007f00u, k2e123 = 0x7d007d00u, kMinus8th = 0xbe00be00u;
     const uint32_t h = w >> 8;
