@@ -412,7 +412,9 @@ size_t striped_attn_decode_workspace_size(int64_t B, int64_t Bp, int64_t H, int6
  * number.  Four bytes hold 8 consecutive channels as a little-endian 32-bit
  * word: code + 8 of channel c of the eight at bit 16 (c mod 2) + 4 (c / 2).
  *  k, v:              [B,Hkv,S,D] bf16 (any row order: rows keep their places);
- *                     |x| <= 3e38, finite.
+ *                     |x| <= 3e38.  A group with a NaN gets the scale NaN, one
+ *                     with an infinity an infinite one: no value of it reads
+ *                     back finite.
  *  k_codes, v_codes:  [B,Hkv,S,D/2] bytes.
  *  k_scales, v_scales:[B,Hkv,S,D/32] bf16.
  * D a multiple of 32 up to 256 (STRIPED_ERR_UNSUPPORTED otherwise), 16-byte

@@ -43,6 +43,18 @@ __device__ __forceinline__ uint32_t kv4_pack(const float (&x)[8], float inv) {
     return w;
 }
 
+// Maxima that a NaN passes through.
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 __global__ void __launch_bounds__(kKThreads) kv4_store_kernel(const Kv4Args a) {
     const bool second = blockIdx.y != 0;
     const uint4 *x = second ? a.x[1] : a.x[0];
@@ -64,15 +76,17 @@ __global__ void __launch_bounds__(kKThreads) kv4_store_kernel(const Kv4Args a) {
         for (int j = 0; j < 4; ++j) {
             f[2 * j] = __uint_as_float(raw[j] << 16);
             f[2 * j + 1] = __uint_as_float(raw[j] & 0xffff0000u);
-            top = fmax3(top, fabsf(f[2 * j]), fabsf(f[2 * j + 1]));
+            top = fmax3_nan(top, fabsf(f[2 * j]), fabsf(f[2 * j + 1]));
         }
         // all lanes of a warp are here: groups never straddle the end (n is a
         // multiple of 4)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const uint32_t t = __float_as_uint(top / 7.f);
-        // to 5 significant bits: the lowest 19 of the 23 fraction bits go
-        const float s = top < 0x1p-100f ? 0.f : __uint_as_float((t + 0x3ffffu + ((t >> 19) & 1u)) & 0xfff80000u);
+        // to 5 significant bits: the lowest 19 of the 23 fraction bits go (a NaN
+        // stays one: the group's values are NaN, whatever their codes)
+        float s = top < 0x1p-100f ? 0.f : __uint_as_float((t + 0x3ffffu + ((t >> 19) & 1u)) & 0xfff80000u);
+        if (top != top) s = top;
         const uint32_t w = kv4_pack(f, s > 0.f ? 1.f / s : 0.f);
         if (v < a.n) {
             codes[v] = w;
