@@ -376,7 +376,8 @@ int striped_attn_window_bwd(const void *q, const void *k, const void *v, const v
  * Token t stands at position P + len - T + t and keeps the keys at or before
  * it; with window > 0 only those less than `window` before it or among the
  * first `sinks` positions (window = 0: all).  A token before position 0
- * (len + P < T) keeps none: o = 0, lse = -infinity.
+ * (len + P < T) keeps none: o = 0, lse = -infinity.  A query with a NaN that
+ * keeps any has o and lse NaN.
  * bf16 with D == 64 or 128, at most 128 stripes in the striped placement,
  * zig-zag as for striped_attn_fwd, P + C + T <= 2^31 - 256, B * H * T <= 2^30
  * and at most 2^30 key tiles over all heads; with g = H/Hkv * T

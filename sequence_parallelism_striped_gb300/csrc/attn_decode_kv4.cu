@@ -461,7 +461,8 @@ __global__ void __launch_bounds__(kQThreads, NT == 1 ? 2 : 1)
 #pragma unroll
                 for (int w = 0; w < kQWarps; ++w) {
                     const float m = sm[w * 8 * NT + r];
-                    l += m == -INFINITY ? 0.f : sl[w * 8 * NT + r] * ex2(m - top);
+                    // without a maximum the sum is 0, or NaN, which stays
+                    l += m == -INFINITY ? sl[w * 8 * NT + r] : sl[w * 8 * NT + r] * ex2(m - top);
                 }
                 *reinterpret_cast<float2 *>(p.part_ml[tail] + 2 * (slot + r)) = make_float2(top, l);
             }

@@ -232,16 +232,22 @@ __global__ void __launch_bounds__(128) decode_join_kernel(const DecParams p, int
         float m_new = m;
 #pragma unroll
         for (int u = 0; u < U; ++u) m_new = fmaxf(m_new, ml[u].x);
-        if (m_new == -INFINITY) continue;
+        // a segment without a maximum has the sum 0, or NaN if its scores are no
+        // numbers: that one is kept
+        if (m_new == -INFINITY) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) l += ml[u].y;
+            continue;
+        }
         const float old = ex2(m - m_new);
         l *= old;
 #pragma unroll
         for (int i = 0; i < E; ++i) acc[i] *= old;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (ml[u].x == -INFINITY) continue;  // no key kept, or no segment
             const float w = ex2(ml[u].x - m_new);
             l = fmaf(ml[u].y, w, l);
+            if (ml[u].x == -INFINITY) continue;  // no key kept, or no segment
 #pragma unroll
             for (int i = 0; i < E; ++i) acc[i] = fmaf(v[u][i], w, acc[i]);
         }
@@ -260,8 +266,9 @@ __global__ void __launch_bounds__(128) decode_join_kernel(const DecParams p, int
         w[i] = sm[i] == -INFINITY ? 0.f : ex2(sm[i] - m);
         l = fmaf(sl[i], w[i], l);
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    if (threadIdx.x == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    // l is 0 if no key was kept, NaN if scores are no numbers: so is the result then
+    const float inv = l > 0.f ? 1.f / l : l;
+    if (threadIdx.x == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : l == 0.f ? -INFINITY : l;
     if (threadIdx.x < HD / 2) {
         float o2[2];
 #pragma unroll
