@@ -142,17 +142,19 @@ _fast = None  # csrc/binding.cpp, once the library is loaded
 
 def _bind(path: str):
     """Calls that the binding takes in one step: plain ones, without buffers or a stream of the caller's.  It gives None
-    for whatever it does not take, and the wrapper goes on; so it does if the binding could not be built."""
+    for whatever it does not take, and the wrapper goes on; so it does if the binding of this torch and of the
+    library's header could not be built."""
     global _fast
-    if not os.path.exists(_build.BINDING):
+    binding = _build.binding_path()
+    if binding is None or not os.path.exists(binding):
         return
     from importlib import machinery, util
 
-    loader = machinery.ExtensionFileLoader("striped_binding", _build.BINDING)
+    loader = machinery.ExtensionFileLoader("striped_binding", binding)
     try:
         module = util.module_from_spec(util.spec_from_loader("striped_binding", loader))
         loader.exec_module(module)
-    except (ImportError, OSError):  # of another torch
+    except (ImportError, OSError):  # a library of torch's that it needs is not there
         return
     if module.use(path):
         _fast = module
