@@ -30,6 +30,17 @@ struct Library {
     decltype(&striped_kv_evict) evict;
 } lib{};
 
+// One of the library's calls.  The interpreter's lock is given up for it: a launch
+// waits where the GPU's queue is full, perhaps for a host function that needs
+// the lock.  (Addresses are taken before that, as arguments of this function.)
+template <typename F, typename... A>
+int launched(F call, A... args) {
+    PyThreadState *state = PyEval_SaveThread();
+    const int status = call(args...);
+    PyEval_RestoreThread(state);
+    return status;
+}
+
 // One call's tensors: the first one tells the device, which has to be current.
 class Call {
   public:
@@ -116,8 +127,8 @@ PyObject *kv4_store(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int64_t cs[4] = {B, H, S, D / 2}, ss[4] = {B, H, S, D / 32};
         at::Tensor kc = c.make(cs, at::kByte), ks = c.make(ss, at::kBFloat16), vc = c.make(cs, at::kByte),
                    vs = c.make(ss, at::kBFloat16);
-        if (lib.kv4_store(k->data_ptr(), v->data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), B, H,
-                          S, D, STRIPED_BF16, c.stream()))
+        if (launched(lib.kv4_store, k->data_ptr(), v->data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(),
+                     vs.data_ptr(), B, H, S, D, STRIPED_BF16, c.stream()))
             return nullptr;
         return tuple_of(kc, ks, vc, vs);
     });
@@ -134,8 +145,8 @@ PyObject *kv4_load(PyObject *, PyObject *const *a, Py_ssize_t n) {
                          *vs = c.take(a[3], ss, at::kBFloat16);
         if (!ks || !vc || !vs) return nullptr;
         at::Tensor k = c.make(xs, at::kBFloat16), v = c.make(xs, at::kBFloat16);
-        if (lib.kv4_load(kc->data_ptr(), ks->data_ptr(), vc->data_ptr(), vs->data_ptr(), k.data_ptr(), v.data_ptr(), B, H,
-                         S, D, STRIPED_BF16, c.stream()))
+        if (launched(lib.kv4_load, kc->data_ptr(), ks->data_ptr(), vc->data_ptr(), vs->data_ptr(), k.data_ptr(),
+                     v.data_ptr(), B, H, S, D, STRIPED_BF16, c.stream()))
             return nullptr;
         return tuple_of(k, v);
     });
@@ -163,10 +174,10 @@ PyObject *decode_kv4(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (bytes <= 0) return nullptr;
         const int64_t os[4] = {B, H, T, D}, lses[3] = {B, H, T}, wss[1] = {bytes};
         at::Tensor o = c.make(os, at::kBFloat16), lse = c.make(lses, at::kFloat), ws = c.make(wss, at::kByte);
-        if (lib.decode(q->data_ptr(), kc->data_ptr(), ks->data_ptr(), vc->data_ptr(), vs->data_ptr(), kt->data_ptr(),
-                       vt->data_ptr(), static_cast<const int32_t *>(lens->data_ptr()), o.data_ptr(),
-                       static_cast<float *>(lse.data_ptr()), ws.data_ptr(), (size_t)bytes, B, Bp, H, Hkv, T, P, C, D, N,
-                       layout, STRIPED_BF16, scale, c.stream()))
+        if (launched(lib.decode, q->data_ptr(), kc->data_ptr(), ks->data_ptr(), vc->data_ptr(), vs->data_ptr(),
+                     kt->data_ptr(), vt->data_ptr(), static_cast<const int32_t *>(lens->data_ptr()), o.data_ptr(),
+                     static_cast<float *>(lse.data_ptr()), ws.data_ptr(), (size_t)bytes, B, Bp, H, Hkv, T, P, C, D, N,
+                     layout, STRIPED_BF16, scale, c.stream()))
             return nullptr;
         return tuple_of(o, lse);
     });
@@ -191,9 +202,9 @@ PyObject *key_weight(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (bytes <= 0) return nullptr;
         const int64_t wss[1] = {bytes};
         at::Tensor w = c.make(wts, at::kFloat), ws = c.make(wss, at::kByte);
-        if (lib.weight(q->data_ptr(), k->data_ptr(), static_cast<const float *>(lse->data_ptr()),
-                       static_cast<float *>(w.data_ptr()), ws.data_ptr(), (size_t)bytes, B, H, Hkv, S, D, N, layout,
-                       STRIPED_BF16, first, 0, scale, c.stream()))
+        if (launched(lib.weight, q->data_ptr(), k->data_ptr(), static_cast<const float *>(lse->data_ptr()),
+                     static_cast<float *>(w.data_ptr()), ws.data_ptr(), (size_t)bytes, B, H, Hkv, S, D, N, layout,
+                     STRIPED_BF16, first, 0, scale, c.stream()))
             return nullptr;
         return THPVariable_Wrap(std::move(w));
     });
@@ -226,8 +237,9 @@ PyObject *kv_evict(PyObject *, PyObject *const *a, Py_ssize_t n) {
         }
         const int64_t ks[3] = {B, H, keep};
         at::Tensor index = c.make(ks, at::kInt), weight = c.make(ks, at::kFloat);
-        if (lib.evict(x, y, row, m, static_cast<const float *>(w->data_ptr()), static_cast<int32_t *>(index.data_ptr()),
-                      static_cast<float *>(weight.data_ptr()), B, H, S, keep, sinks, recent, N, layout, c.stream()))
+        if (launched(lib.evict, x, y, row, m, static_cast<const float *>(w->data_ptr()),
+                     static_cast<int32_t *>(index.data_ptr()), static_cast<float *>(weight.data_ptr()), B, H, S, keep,
+                     sinks, recent, N, layout, c.stream()))
             return nullptr;
         return m == 2 ? tuple_of(out[0], out[1], index, weight) : tuple_of(out[0], out[1], out[2], out[3], index, weight);
     });
