@@ -142,8 +142,8 @@ _fast = None  # csrc/binding.cpp, once the library is loaded
 
 def _bind(path: str):
     """Calls that the binding takes in one step: plain ones, without buffers or a stream of the caller's.  It gives None
-    for whatever it does not take, and the wrapper goes on; so it does if the binding of this torch and of the
-    library's header could not be built."""
+    for whatever it does not take or the library refuses, and the wrapper goes on; so it does if the binding of this
+    torch and of the library's header could not be built.  A call that failed it raises itself."""
     global _fast
     binding = _build.binding_path()
     if binding is None or not os.path.exists(binding):
@@ -156,7 +156,7 @@ def _bind(path: str):
         loader.exec_module(module)
     except (ImportError, OSError):  # a library of torch's that it needs is not there
         return
-    if module.use(path):
+    if module.use(path, StripedError):
         _fast = module
 
 

@@ -5,8 +5,9 @@
 // to 25 us of the host's time, most of it for reading attributes one by one and
 // for results made through Python.  Here a function takes the plain case: tensors
 // of the right types, shapes and device, contiguous, that device current, no
-// buffer given.  Anything else, and any status but 0, gives None: the wrapper then
-// goes its own way, and what is wrong is named there.
+// buffer given.  Anything else, and what the library refuses, gives None: the wrapper
+// then goes its own way, and what is wrong is named there.  A call that failed is
+// not made again: its status is raised here.
 #include <Python.h>
 #include <dlfcn.h>
 
@@ -29,16 +30,23 @@ struct Library {
     decltype(&striped_attn_key_weight_workspace_size) weight_size;
     decltype(&striped_kv_evict) evict;
 } lib{};
+PyObject *failed = nullptr;  // failed(status, name) is the exception of a call that failed
 
-// One of the library's calls.  The interpreter's lock is given up for it: a launch
+// One of the library's calls: false if it refused its arguments, or failed, which is
+// then the interpreter's error.  The interpreter's lock is given up for it: a launch
 // waits where the GPU's queue is full, perhaps for a host function that needs
 // the lock.  (Addresses are taken before that, as arguments of this function.)
 template <typename F, typename... A>
-int launched(F call, A... args) {
+bool launched(const char *name, F call, A... args) {
     PyThreadState *state = PyEval_SaveThread();
     const int status = call(args...);
     PyEval_RestoreThread(state);
-    return status;
+    if (status == STRIPED_ERR_CUDA) {
+        PyObject *e = PyObject_CallFunction(failed, "is", status, name);
+        if (e) PyErr_SetObject(reinterpret_cast<PyObject *>(Py_TYPE(e)), e);
+        Py_XDECREF(e);
+    }
+    return status == STRIPED_OK;
 }
 
 // One call's tensors: the first one tells the device, which has to be current.
@@ -127,7 +135,7 @@ PyObject *kv4_store(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int64_t cs[4] = {B, H, S, D / 2}, ss[4] = {B, H, S, D / 32};
         at::Tensor kc = c.make(cs, at::kByte), ks = c.make(ss, at::kBFloat16), vc = c.make(cs, at::kByte),
                    vs = c.make(ss, at::kBFloat16);
-        if (launched(lib.kv4_store, k->data_ptr(), v->data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(),
+        if (!launched("striped_kv4_store", lib.kv4_store, k->data_ptr(), v->data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(),
                      vs.data_ptr(), B, H, S, D, STRIPED_BF16, c.stream()))
             return nullptr;
         return tuple_of(kc, ks, vc, vs);
@@ -145,7 +153,7 @@ PyObject *kv4_load(PyObject *, PyObject *const *a, Py_ssize_t n) {
                          *vs = c.take(a[3], ss, at::kBFloat16);
         if (!ks || !vc || !vs) return nullptr;
         at::Tensor k = c.make(xs, at::kBFloat16), v = c.make(xs, at::kBFloat16);
-        if (launched(lib.kv4_load, kc->data_ptr(), ks->data_ptr(), vc->data_ptr(), vs->data_ptr(), k.data_ptr(),
+        if (!launched("striped_kv4_load", lib.kv4_load, kc->data_ptr(), ks->data_ptr(), vc->data_ptr(), vs->data_ptr(), k.data_ptr(),
                      v.data_ptr(), B, H, S, D, STRIPED_BF16, c.stream()))
             return nullptr;
         return tuple_of(k, v);
@@ -174,7 +182,7 @@ PyObject *decode_kv4(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (bytes <= 0) return nullptr;
         const int64_t os[4] = {B, H, T, D}, lses[3] = {B, H, T}, wss[1] = {bytes};
         at::Tensor o = c.make(os, at::kBFloat16), lse = c.make(lses, at::kFloat), ws = c.make(wss, at::kByte);
-        if (launched(lib.decode, q->data_ptr(), kc->data_ptr(), ks->data_ptr(), vc->data_ptr(), vs->data_ptr(),
+        if (!launched("striped_attn_decode_kv4", lib.decode, q->data_ptr(), kc->data_ptr(), ks->data_ptr(), vc->data_ptr(), vs->data_ptr(),
                      kt->data_ptr(), vt->data_ptr(), static_cast<const int32_t *>(lens->data_ptr()), o.data_ptr(),
                      static_cast<float *>(lse.data_ptr()), ws.data_ptr(), (size_t)bytes, B, Bp, H, Hkv, T, P, C, D, N,
                      layout, STRIPED_BF16, scale, c.stream()))
@@ -202,7 +210,7 @@ PyObject *key_weight(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (bytes <= 0) return nullptr;
         const int64_t wss[1] = {bytes};
         at::Tensor w = c.make(wts, at::kFloat), ws = c.make(wss, at::kByte);
-        if (launched(lib.weight, q->data_ptr(), k->data_ptr(), static_cast<const float *>(lse->data_ptr()),
+        if (!launched("striped_attn_key_weight", lib.weight, q->data_ptr(), k->data_ptr(), static_cast<const float *>(lse->data_ptr()),
                      static_cast<float *>(w.data_ptr()), ws.data_ptr(), (size_t)bytes, B, H, Hkv, S, D, N, layout,
                      STRIPED_BF16, first, 0, scale, c.stream()))
             return nullptr;
@@ -237,7 +245,7 @@ PyObject *kv_evict(PyObject *, PyObject *const *a, Py_ssize_t n) {
         }
         const int64_t ks[3] = {B, H, keep};
         at::Tensor index = c.make(ks, at::kInt), weight = c.make(ks, at::kFloat);
-        if (launched(lib.evict, x, y, row, m, static_cast<const float *>(w->data_ptr()),
+        if (!launched("striped_kv_evict", lib.evict, x, y, row, m, static_cast<const float *>(w->data_ptr()),
                      static_cast<int32_t *>(index.data_ptr()), static_cast<float *>(weight.data_ptr()), B, H, S, keep,
                      sinks, recent, N, layout, c.stream()))
             return nullptr;
@@ -245,10 +253,12 @@ PyObject *kv_evict(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// The library that is loaded already, by its path; True if it has all calls.
-PyObject *use(PyObject *, PyObject *path) {
-    const char *name = PyUnicode_AsUTF8(path);
-    if (!name) return nullptr;
+// The library that is loaded already, by its path, and the exception for its
+// failures; True if it has all calls.
+PyObject *use(PyObject *, PyObject *args) {
+    const char *name;
+    PyObject *exception;
+    if (!PyArg_ParseTuple(args, "sO", &name, &exception)) return nullptr;
     void *h = dlopen(name, RTLD_NOW | RTLD_NOLOAD);
     if (!h) Py_RETURN_FALSE;
     Library l{};
@@ -262,6 +272,9 @@ PyObject *use(PyObject *, PyObject *path) {
         !get(l.evict, "striped_kv_evict"))
         Py_RETURN_FALSE;
     lib = l;
+    Py_INCREF(exception);
+    Py_XDECREF(failed);
+    failed = exception;
     Py_RETURN_TRUE;
 }
 
@@ -270,7 +283,7 @@ PyCFunction fast(F f) {
     return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
 }
 
-PyMethodDef methods[] = {{"use", use, METH_O, nullptr},
+PyMethodDef methods[] = {{"use", use, METH_VARARGS, nullptr},
                          {"kv4_store", fast(kv4_store), METH_FASTCALL, nullptr},
                          {"kv4_load", fast(kv4_load), METH_FASTCALL, nullptr},
                          {"decode_kv4", fast(decode_kv4), METH_FASTCALL, nullptr},

@@ -18,9 +18,9 @@ def fake(tmp_path):
     if sp._fast is None:
         pytest.skip("the binding was not built for this torch")
     lib = Fake(tmp_path)
-    assert sp._fast.use(lib.path)
+    assert sp._fast.use(lib.path, sp.StripedError)
     yield lib
-    assert sp._fast.use(sp.library_path())
+    assert sp._fast.use(sp.library_path(), sp.StripedError)
 
 
 def _calls():
@@ -59,3 +59,24 @@ def test_other_threads_go_on_while_a_call_waits(fake, which):
     stop.set()
     thread.join()
     assert waited >= 0.5 and max(gaps) < 0.25
+
+
+@pytest.mark.parametrize("which", range(6))
+def test_a_call_that_failed_is_not_made_again(fake, which):
+    """A CUDA error: the first kernel may have been launched, and the device may be broken."""
+    call = _calls()[which]
+    fake["status"] = -4
+    with pytest.raises(sp.StripedError) as e:
+        call()
+    assert e.value.status == -4 and "CUDA error" in str(e.value) and "striped_" in str(e.value)
+    assert fake["calls"] == 1
+
+
+@pytest.mark.parametrize("which", range(6))
+@pytest.mark.parametrize("status", [-1, -2, -3, -6])
+def test_a_refused_call_is_the_wrappers(fake, which, status):
+    """Nothing was launched: the wrapper looks at the arguments and makes the call (to the library itself here)."""
+    call = _calls()[which]
+    fake["status"] = status
+    call()
+    assert fake["calls"] == 1 and sp.check_error() == 0
