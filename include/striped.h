@@ -383,6 +383,9 @@ int striped_attn_window_bwd(const void *q, const void *k, const void *v, const v
  * and at most 2^30 key tiles over all heads; with g = H/Hkv * T
  * rows a request, Bp * ceil(B/Bp * g / 128) (P > 0) + B * ceil(g / 128)
  * <= 2048: else STRIPED_ERR_UNSUPPORTED (split the batch).
+ * The weights of a softmax are rounded to bf16 for the product with V (their
+ * sum is of fp32): o is off by up to 2^-8 of the weighted sum of |v|, and by its
+ * own rounding.
  * Segments are joined in a fixed order: results are the same from run to run
  * (on the same kind of GPU).  workspace: 256-byte aligned, >=
  * striped_attn_decode_workspace_size() bytes, contents ignored; calls that
@@ -433,7 +436,7 @@ int striped_kv4_load(const void *k_codes, const void *k_scales, const void *v_co
  * v_scales [Bp,Hkv,P,D/32], rows in `layout` order, P >= 1; tails as for
  * striped_attn_decode (bf16).  The result is that of striped_attn_decode on
  * the stored values.  Every query keeps all positions at or before it: there
- * is no window.  Limits, lengths, order of sums, workspace and overlaps as for
+ * is no window.  Limits, lengths, roundings, order of sums, workspace and overlaps as for
  * striped_attn_decode; with
  * g = H/Hkv * T rows a request, ceil(B/Bp * g / 128) row tiles a prompt; with
  * a scale above 3.6e36, |q| < 2^122.

@@ -28,11 +28,17 @@
 // and their join are those of attn_decode.cu; tails are read straight to
 // registers.
 //
+// The weights P are rounded to bf16 (2^-8 of a weight at most), as everywhere in
+// this library: an m16n8k16 of 16-bit operands takes them as they are, and fp32
+// ones would be two products of halves each.  The sum of a row adds the
+// unrounded ones.
+//
 // Measured in a graph at D = 128, 32 query heads on 8, one new token: 16 requests
-// with prompts of their own of 32768 124 us, 5.0 TB/s (bf16 prompts 309); one
-// request on 4096 10.8 us (10.6).  The integer pipe is busy most of the time:
-// before it had fewer operations a word (kv4_pairs) 152 us.  On the tcgen05 kernel
-// the 16 requests took 452.
+// with prompts of their own of 32768 122 us, 5.1 TB/s (bf16 prompts 309); one
+// request on 4096 10.7 us (10.5).  What bounds it is latency: the integer pipe,
+// the issue slots and DRAM are each busy about half of the time (47, 50 and 50 %;
+// a stretch is read one stretch ahead), so that fewer operations a word helped
+// (kv4_pairs: 152 us before).  On the tcgen05 kernel the 16 requests took 452.
 #include <math.h>
 
 #include "common.cuh"

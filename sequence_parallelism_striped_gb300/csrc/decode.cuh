@@ -323,8 +323,8 @@ bool decode_plan(DecPlan *plan, const DecodeArgs &a) {
     p.over = a.D == 128 && !a.kv4 ? 2 : 4;
     // Few rows on a 4-bit prompt go to attn_decode_kv4.cu, more to
     // attn_decode_kv4_tc.cu.  16 prompts of 32768, 8 heads, D = 128 (64), us: 8 rows
-    // 125 against 278 (82, 230), 16 rows 160 against 285 (124, 233), 24 rows 228
-    // against 302 (156, 235), 32 rows 266 against 312 (179, 237)
+    // 123 against 278 (80, 230), 16 rows 162 against 285 (125, 233), 24 rows 215
+    // against 302 (155, 235), 32 rows 265 against 312 (179, 237)
     plan->small = a.kv4 && rows_p <= 32;
     const int tail_tile = plan->small ? kTailTile : DT;
     const int64_t tiles =
